@@ -18,7 +18,8 @@ import math
 import os
 
 __all__ = ["FAError", "lib", "fa_fwd", "fa_bwd", "fa_bwd_noalloc", "fa_bwd_launches", "fa_get_status", "fa_status_string", "fa_debug_set",
-           "fa_debug_exp2", "fa_tune", "TUNE_EXP2_SPLIT", "TUNE_CTA_PAIRS", "TUNE_BWD_SPLIT", "fa_profile_events", "fa_trace", "forward", "backward", "STATUS"]
+           "fa_debug_exp2", "fa_tune", "TUNE_EXP2_SPLIT", "TUNE_CTA_PAIRS", "TUNE_BWD_SPLIT", "fa_profile_events", "fa_trace", "forward", "backward", "STATUS",
+           "fa_fwd_varlen", "fa_fwd_paged", "fa_cache_append", "forward_varlen", "forward_paged", "cache_append"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -67,6 +68,13 @@ def lib() -> ctypes.CDLL:
         L.fa_bwd_noalloc.restype = i
         L.fa_bwd_launches.argtypes = [i] * 7
         L.fa_bwd_launches.restype = i
+        ll = ctypes.c_longlong
+        L.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [ll, ll, ll, f, i, i, vp]
+        L.fa_fwd_varlen.restype = i
+        L.fa_fwd_paged.argtypes = [vp] * 8 + [i] * 8 + [ll, f, i, i, vp]
+        L.fa_fwd_paged.restype = i
+        L.fa_cache_append.argtypes = [vp] * 7 + [i] * 7 + [ll, ll, vp]
+        L.fa_cache_append.restype = i
         L.fa_get_status.argtypes = [vp]
         L.fa_get_status.restype = i
         L.fa_status_string.argtypes = [i]
@@ -271,3 +279,166 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
     if st != 0:
         raise FAError(st, "fa_bwd")
     return dq, dk, dv
+
+
+# --- sequences of different lengths (see fa.h) ---------------------------------
+
+def fa_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, B, Hq, Hkv, total_q, total_k, d, q_stride, k_stride, v_stride, scale,
+                  window_left, window_right, stream=None) -> int:
+    return lib().fa_fwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q), _ptr(cu_k), B, Hq, Hkv,
+                               total_q, total_k, d, q_stride, k_stride, v_stride, float(scale), int(window_left),
+                               int(window_right), _stream(stream))
+
+
+def fa_fwd_paged(q, k_pages, v_pages, o, lse, cu_q, lens_k, page_table, B, Hq, Hkv, total_q, num_pages, page_size,
+                 max_pages, d, q_stride, scale, window_left, window_right, stream=None) -> int:
+    return lib().fa_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(o), _ptr(lse), _ptr(cu_q), _ptr(lens_k),
+                              _ptr(page_table), B, Hq, Hkv, total_q, num_pages, page_size, max_pages, d, q_stride,
+                              float(scale), int(window_left), int(window_right), _stream(stream))
+
+
+def fa_cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, B, Hkv, total_q, num_pages, page_size, max_pages,
+                    d, k_stride, v_stride, stream=None) -> int:
+    return lib().fa_cache_append(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(cu_q), _ptr(lens_k),
+                                 _ptr(page_table), B, Hkv, total_q, num_pages, page_size, max_pages, d, k_stride,
+                                 v_stride, _stream(stream))
+
+
+def _tokens(name, t, device=None, shape=None):
+    """Checks a packed [total, H, d] tensor; returns its elements between tokens."""
+    import torch
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor of shape [tokens, heads, d]")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, q is on {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have the shape {shape}")
+    n, h, d = t.shape
+    s = t.stride()
+    if n <= 1:  # the stride of an axis of one has no meaning
+        s = (h * d, s[1], s[2])
+    if s[2] != 1 or (h > 1 and s[1] != d) or s[0] < h * d:
+        raise ValueError(f"{name}: the heads of a token must be contiguous, and tokens must not overlap")
+    return s[0]
+
+
+def _ints(name, t, shape, device):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+
+
+def _pages(k_pages, v_pages, hkv, d, device):
+    import torch
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if (t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape != k_pages.shape or tuple(t.shape[2:]) != (hkv, d)
+                or not t.is_contiguous() or t.device != device):
+            raise ValueError(f"{name} must be a contiguous bf16 tensor of shape [pages, page_size, {hkv}, {d}] on {device}")
+    return k_pages.shape[0], k_pages.shape[1]
+
+
+class _on:
+    """The device of the call's tensors made current, and the call's stream
+    for the outputs that it allocates (so that the allocator reuses their
+    memory in that stream's order)."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _seq_out(q, out):
+    """The given (o, lse) after a check, or new ones."""
+    import torch
+    total, hq, d = q.shape
+    if out is None:
+        return (torch.empty((total, hq, d), device=q.device, dtype=torch.bfloat16),
+                torch.empty((hq, total), device=q.device, dtype=torch.float32))
+    o, lse = out
+    if tuple(o.shape) != (total, hq, d) or o.dtype != torch.bfloat16 or not o.is_contiguous() or o.device != q.device:
+        raise ValueError(f"o must be a contiguous bf16 tensor of shape {(total, hq, d)} on {q.device}")
+    if tuple(lse.shape) != (hq, total) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != q.device:
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(hq, total)} on {q.device}")
+    return o, lse
+
+
+def forward_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | None = None, out=None, stream=None,
+                   window=None):
+    """O [total_q, Hq, d] and LSE [Hq, total_q] of packed sequences: q
+    [total_q, Hq, d], k/v [total_k, Hkv, d] (bf16, CUDA; tokens may be strided),
+    cu_q, cu_k int32 [B + 1] row offsets on the device (see fa.h fa_fwd_varlen).
+    Rows outside every sequence are left as they are (unset in new outputs)."""
+    qs = _tokens("q", q)
+    total_q, hq, d = q.shape
+    total_k, hkv = k.shape[0], k.shape[1]
+    ks, vs = _tokens("k", k, q.device, (total_k, hkv, d)), _tokens("v", v, q.device, (total_k, hkv, d))
+    B = cu_q.shape[0] - 1
+    _ints("cu_q", cu_q, (B + 1,), q.device)
+    _ints("cu_k", cu_k, (B + 1,), q.device)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(q.device, stream):
+        o, lse = _seq_out(q, out)
+        st = fa_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, B, hq, hkv, total_q, total_k, d, qs, ks, vs, scale,
+                           *_window_args(causal, window))
+    if st != 0:
+        raise FAError(st, "fa_fwd_varlen")
+    return o, lse
+
+
+def forward_paged(q, k_pages, v_pages, cu_q, lens_k, page_table, causal: bool = True, scale: float | None = None,
+                  out=None, stream=None, window=None):
+    """O [total_q, Hq, d] and LSE [Hq, total_q] of new tokens q [total_q, Hq, d]
+    (bf16, CUDA; tokens may be strided) over a cache of pages [num_pages,
+    page_size, Hkv, d]; cu_q [B + 1], lens_k [B] and page_table [B, max_pages]
+    are int32 on the device (see fa.h fa_fwd_paged)."""
+    qs = _tokens("q", q)
+    total_q, hq, d = q.shape
+    hkv = k_pages.shape[2] if k_pages.dim() == 4 else 0
+    num_pages, page_size = _pages(k_pages, v_pages, hkv, d, q.device)
+    B = cu_q.shape[0] - 1
+    max_pages = page_table.shape[-1]
+    _ints("cu_q", cu_q, (B + 1,), q.device)
+    _ints("lens_k", lens_k, (B,), q.device)
+    _ints("page_table", page_table, (B, max_pages), q.device)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(q.device, stream):
+        o, lse = _seq_out(q, out)
+        st = fa_fwd_paged(q, k_pages, v_pages, o, lse, cu_q, lens_k, page_table, B, hq, hkv, total_q, num_pages,
+                          page_size, max_pages, d, qs, scale, *_window_args(causal, window))
+    if st != 0:
+        raise FAError(st, "fa_fwd_paged")
+    return o, lse
+
+
+def cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, stream=None) -> None:
+    """k, v [total_q, Hkv, d] of new tokens (bf16, CUDA; tokens may be strided)
+    into the pages, in place; lens_k are the lengths with the new tokens (see
+    fa.h fa_cache_append)."""
+    ks = _tokens("k", k)
+    total, hkv, d = k.shape
+    vs = _tokens("v", v, k.device, (total, hkv, d))
+    num_pages, page_size = _pages(k_pages, v_pages, hkv, d, k.device)
+    B = cu_q.shape[0] - 1
+    max_pages = page_table.shape[-1]
+    _ints("cu_q", cu_q, (B + 1,), k.device)
+    _ints("lens_k", lens_k, (B,), k.device)
+    _ints("page_table", page_table, (B, max_pages), k.device)
+    with _on(k.device, stream):
+        st = fa_cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, B, hkv, total, num_pages, page_size,
+                             max_pages, d, ks, vs)
+    if st != 0:
+        raise FAError(st, "fa_cache_append")

@@ -333,6 +333,134 @@ extern "C" int fa_bwd_window(const void* q, const void* k, const void* v, const 
   return bwd_pooled(p, o, lse, dout, dq, dk, dv, stream);
 }
 
+namespace {
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes and strides shared by the calls on sequences of different lengths.
+int check_seq_sizes(int B, int Hq, int Hkv, int total, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || total < 0 || d < 1) return FA_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  // a tile of 128 rows holds whole tokens of a group; rows (token, head) and
+  // work items are counted in 32 bits
+  if (Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
+  if (total > (1 << 28) || B > (1 << 28)) return FA_ERR_UNSUPPORTED;
+  if (1LL * (total + 1LL) * Hq >= (1LL << 31) || 1LL * (1LL * total + B) * Hkv >= (1LL << 30)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+// elements between the tokens of a tensor of `heads` heads
+int check_stride(long long stride, int heads, int d, int total) {
+  if (stride < 1LL * heads * d || stride % 8 != 0) return FA_ERR_INVALID_ARG;
+  if (stride >= (1LL << 38) || stride * 2 * (total > 0 ? total : 1) >= (1LL << 40)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+int check_pages(int num_pages, int page_size, int max_pages, int Hkv, int d) {
+  if (num_pages < 1 || page_size < 1 || max_pages < 1) return FA_ERR_INVALID_ARG;
+  if (page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (1LL * max_pages * page_size > (1LL << 28) || num_pages > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  if (2.0 * num_pages * page_size * Hkv * d >= double(1LL << 40)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+// window bounds as the kernels take them; `reach` keys and rows at most
+int clip_window(int w, long long reach) { return w < 0 || w >= reach ? -1 : w; }
+
+int seq_result(cudaError_t e) {
+  if (e == cudaSuccess) return FA_OK;
+  cudaGetLastError();
+  return e == cudaErrorMemoryAllocation ? FA_ERR_ALLOC : FA_ERR_LAUNCH;
+}
+}  // namespace
+
+extern "C" int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_q,
+                             const int* cu_k, int B, int Hq, int Hkv, int total_q, int total_k, int d,
+                             long long q_stride, long long k_stride, long long v_stride, float scale, int window_left,
+                             int window_right, void* stream) {
+  int st = check_seq_sizes(B, Hq, Hkv, total_q, d);
+  if (st == FA_OK) st = check_seq_sizes(B, Hq, Hkv, total_k, d);
+  if (st != FA_OK) return st;
+  if (!std::isfinite(scale) || !aligned4(cu_q) || !aligned4(cu_k)) return FA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!aligned16(q) || !aligned16(o) || !aligned16(lse))) return FA_ERR_INVALID_ARG;
+  if (total_k > 0 && (!aligned16(k) || !aligned16(v))) return FA_ERR_INVALID_ARG;
+  st = check_stride(q_stride, Hq, d, total_q);
+  if (st == FA_OK) st = check_stride(k_stride, Hkv, d, total_k);
+  if (st == FA_OK) st = check_stride(v_stride, Hkv, d, total_k);
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total_q == 0) return st;
+  SeqProblem p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.cu_q = cu_q;
+  p.cu_k = cu_k;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.total_q = total_q;
+  p.total_k = total_k;
+  p.d = d;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.scale = scale;
+  p.window_left = clip_window(window_left, 1LL * total_q + total_k);
+  p.window_right = clip_window(window_right, 1LL * total_q + total_k);
+  return seq_result(launch_seq_fwd(p, o, lse, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                            const int* cu_q, const int* lens_k, const int* page_table, int B, int Hq, int Hkv,
+                            int total_q, int num_pages, int page_size, int max_pages, int d, long long q_stride,
+                            float scale, int window_left, int window_right, void* stream) {
+  int st = check_seq_sizes(B, Hq, Hkv, total_q, d);
+  if (st == FA_OK) st = check_pages(num_pages, page_size, max_pages, Hkv, d);
+  if (st != FA_OK) return st;
+  if (!std::isfinite(scale) || !aligned4(cu_q) || !aligned4(lens_k) || !aligned4(page_table)) return FA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!aligned16(q) || !aligned16(o) || !aligned16(lse))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
+  st = check_stride(q_stride, Hq, d, total_q);
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total_q == 0) return st;
+  SeqProblem p{};
+  p.q = q;
+  p.k = k_pages;
+  p.v = v_pages;
+  p.cu_q = cu_q;
+  p.lens_k = lens_k;
+  p.page_table = page_table;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.total_q = total_q;
+  p.d = d;
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.q_stride = q_stride;
+  p.scale = scale;
+  p.window_left = clip_window(window_left, total_q + 1LL * max_pages * page_size);
+  p.window_right = clip_window(window_right, total_q + 1LL * max_pages * page_size);
+  return seq_result(launch_seq_fwd(p, o, lse, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, const int* cu_q,
+                               const int* lens_k, const int* page_table, int B, int Hkv, int total_q, int num_pages,
+                               int page_size, int max_pages, int d, long long k_stride, long long v_stride,
+                               void* stream) {
+  int st = check_seq_sizes(B, Hkv, Hkv, total_q, d);
+  if (st == FA_OK) st = check_pages(num_pages, page_size, max_pages, Hkv, d);
+  if (st != FA_OK) return st;
+  if (!aligned4(cu_q) || !aligned4(lens_k) || !aligned4(page_table)) return FA_ERR_INVALID_ARG;
+  if (total_q > 0 && (!aligned16(k) || !aligned16(v))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
+  st = check_stride(k_stride, Hkv, d, total_q);
+  if (st == FA_OK) st = check_stride(v_stride, Hkv, d, total_q);
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total_q == 0) return st;
+  const AppendProblem p{k,       v,         k_pages,   v_pages,   cu_q, lens_k,   page_table, B, Hkv,
+                        total_q, d,         num_pages, page_size, max_pages, k_stride, v_stride};
+  return seq_result(launch_cache_append(p, static_cast<cudaStream_t>(stream)));
+}
+
 extern "C" int fa_get_status(void* stream) {
   if (check_device() != FA_OK) return FA_ERR_NO_DEVICE;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_LAUNCH;
@@ -340,7 +468,7 @@ extern "C" int fa_get_status(void* stream) {
   if (cudaMemcpyFromSymbol(&v, g_fa_status, sizeof(v)) != cudaSuccess) return FA_ERR_LAUNCH;
   const unsigned zero = 0;
   if (cudaMemcpyToSymbol(g_fa_status, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_LAUNCH;
-  return (v & kDevTimeout) ? FA_ERR_TIMEOUT : FA_OK;
+  return (v & kDevTimeout) ? FA_ERR_TIMEOUT : (v & kDevBadArg) ? FA_ERR_INVALID_ARG : FA_OK;
 }
 
 extern "C" const char* fa_status_string(int status) {

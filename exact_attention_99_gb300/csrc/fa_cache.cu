@@ -1,0 +1,102 @@
+// fa_cache_append: K and V rows of new tokens into the pages of a cache.
+//
+// A copy of 2 * total_q * Hkv * d bf16 values, each read once and written
+// once, so memory bound: 16 bytes per lane, four rows' worth of loads in
+// flight per thread. A block takes kRows tokens; its first threads find
+// where each goes (binary search of the token in cu_q, then the page of its
+// place in the sequence) while the others wait, and the rows are then copied
+// as runs of Hkv * d values.
+#include <cuda_bf16.h>
+
+#include "fa_internal.h"
+#include "fa_seq.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kRows = 8, kThreads = 256;
+
+struct AppendArgs {
+  const uint4* k;
+  const uint4* v;
+  uint4* k_pages;
+  uint4* v_pages;
+  const int* table;
+  seq::Lens L;
+  int row16;  // 16-byte pieces of a token's row
+  int num_pages, page_size, max_pages;
+  long long k_stride16, v_stride16;
+  unsigned* status;
+};
+
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+  __shared__ long long to[kRows];  // row of the pool, or -1
+  const int tid = threadIdx.x;
+  const int t0 = blockIdx.x * kRows;
+  if (tid < kRows) {
+    const int t = t0 + tid;
+    long long at = -1;
+    if (t < a.L.total_q) {
+      // the last sequence that begins at or before t
+      int lo = 0, hi = a.L.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.L.cu_q[mid] <= t) {
+          lo = mid;
+        } else {
+          hi = mid;
+        }
+      }
+      seq::Seq s;
+      const bool ok = seq::seq_at(a.L, lo, s) && s.qlen <= s.klen;
+      if (!ok) {
+        atomicOr(a.status, kDevBadArg);
+      } else if (t >= s.q0 && t < s.q0 + s.qlen) {  // (rows before the first and behind the last sequence go nowhere)
+        const int place = s.klen - s.qlen + (t - s.q0);
+        const int pg = place / a.page_size;
+        const int page = a.table[size_t(lo) * a.max_pages + pg];
+        if (page < 0 || page >= a.num_pages) {
+          atomicOr(a.status, kDevBadArg);
+        } else {
+          at = 1LL * page * a.page_size + (place - pg * a.page_size);
+        }
+      }
+    }
+    to[tid] = at;
+  }
+  __syncthreads();
+  const int n = kRows * a.row16;
+  for (int i = tid; i < n; i += kThreads) {
+    const int r = i / a.row16, c = i - r * a.row16;
+    const long long at = to[r];
+    if (at < 0) continue;
+    const uint4 x = __ldcs(a.k + (t0 + r) * a.k_stride16 + c), y = __ldcs(a.v + (t0 + r) * a.v_stride16 + c);
+    a.k_pages[at * a.row16 + c] = x;
+    a.v_pages[at * a.row16 + c] = y;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendProblem& pb, cudaStream_t stream) {
+  AppendArgs a{};
+  a.k = static_cast<const uint4*>(pb.k);
+  a.v = static_cast<const uint4*>(pb.v);
+  a.k_pages = static_cast<uint4*>(pb.k_pages);
+  a.v_pages = static_cast<uint4*>(pb.v_pages);
+  a.table = pb.page_table;
+  a.L = seq::Lens{pb.cu_q, nullptr, pb.lens_k, pb.B, pb.total_q, 0, 1LL * pb.max_pages * pb.page_size};
+  a.row16 = pb.Hkv * pb.d / 8;
+  a.num_pages = pb.num_pages;
+  a.page_size = pb.page_size;
+  a.max_pages = pb.max_pages;
+  a.k_stride16 = pb.k_stride / 8;
+  a.v_stride16 = pb.v_stride / 8;
+  a.status = status_word();
+  if (a.status == nullptr) return cudaErrorLaunchFailure;
+  append_kernel<<<unsigned((1LL * pb.total_q + kRows - 1) / kRows), kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

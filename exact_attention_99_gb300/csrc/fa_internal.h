@@ -8,6 +8,7 @@ namespace fa {
 
 // Status bits written by kernels into the per-device status word.
 constexpr unsigned kDevTimeout = 1u;
+constexpr unsigned kDevBadArg = 2u;  // lengths or pages on the device that the tensors cannot hold
 
 struct Problem {
   const void* q;
@@ -86,6 +87,41 @@ size_t bwd_workspace_bytes(const Problem& p);
 int bwd_launch_count(const Problem& p);
 cudaError_t launch_bwd(const Problem& p, const void* o, const float* lse, const void* dout, void* dq, void* dk,
                        void* dv, float* ws, cudaStream_t stream);
+
+// Sequences of different lengths (fa_fwd_varlen, fa_fwd_paged): lengths and
+// pages are device arrays. Strides are elements between tokens.
+struct SeqProblem {
+  const void* q;
+  const void* k;  // packed [total_k, Hkv, d], or pages [num_pages, page_size, Hkv, d]
+  const void* v;
+  const int* cu_q;        // [B + 1]
+  const int* cu_k;        // packed: [B + 1]
+  const int* lens_k;      // paged: [B]
+  const int* page_table;  // paged: [B, max_pages]; null: packed
+  int B, Hq, Hkv, total_q, total_k, d;
+  int num_pages, page_size, max_pages;
+  long long q_stride, k_stride, v_stride;
+  float scale;
+  int window_left, window_right;  // -1: no limit
+};
+// cudaErrorMemoryAllocation: the workspace could not be allocated
+cudaError_t launch_seq_fwd(const SeqProblem& p, void* o, float* lse, cudaStream_t stream);
+
+// Rows of k and v (row strides in elements) into the pages.
+struct AppendProblem {
+  const void* k;
+  const void* v;
+  void* k_pages;
+  void* v_pages;
+  const int* cu_q;
+  const int* lens_k;
+  const int* page_table;
+  int B, Hkv, total_q, d;
+  int num_pages, page_size, max_pages;
+  long long k_stride, v_stride;
+};
+cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t stream);
+
 cudaError_t launch_debug_exp2(const float* x, float* y, int n, int mode, cudaStream_t stream);
 
 }  // namespace fa

@@ -219,10 +219,86 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
                    int causal, void* stream);
 
 /*
+ * Sequences of different lengths.
+ *
+ * The calls below take a batch whose sequences differ in length, as language
+ * models have them: packed one behind the other for training and prompts
+ * (fa_fwd_varlen), or new tokens over a cache that is kept in pages
+ * (fa_cache_append, fa_fwd_paged). Shared conventions:
+ *   Tokens   : q, o [total_q, Hq, d], k, v [total_k, Hkv, d] (bf16), the heads
+ *              of a token contiguous; consecutive tokens of q, k and v lie
+ *              q_stride, k_stride and v_stride elements apart (multiples of 8,
+ *              at least heads * d), so that they may be slices of one fused
+ *              projection. o is contiguous; lse is [Hq, total_q] fp32.
+ *   Lengths  : device arrays of 32-bit integers, read when the kernels run (a
+ *              captured graph reads those of each replay). Sequence b has the
+ *              rows cu_q[b] .. cu_q[b + 1] - 1 of q and o (0 <= cu_q[0] <= ...
+ *              <= cu_q[B] <= total_q), n_b in number, and m_b keys. Either may
+ *              be 0. Rows before cu_q[0] and from cu_q[B] on are left as
+ *              they are.
+ *   Mask     : key j of the sequence is visible to its row i iff
+ *                i + off - window_left <= j <= i + off + window_right,
+ *              off = m_b - n_b; a negative bound is no limit. Causal is
+ *              window_left = -1, window_right = 0. A row that sees no key gets
+ *              o = 0 and lse = -inf. What lies past a sequence's keys (other
+ *              sequences, unused rows of a page) is never used, whatever its
+ *              bits; v rows that only the window hides must be finite.
+ *   Sizes    : B >= 1, total_q, total_k >= 0 (0: nothing, or no keys at all),
+ *              Hq % Hkv == 0, Hq / Hkv <= 128, d in {64, 128}, any finite scale.
+ *   Workspace: from the per-device pool that fa_bwd uses, on `stream` (about
+ *              1 KB per SM and row of a tile: 80 MB at d = 128).
+ *   Errors   : as above for what the host can see. Lengths or pages on the
+ *              device that the tensors cannot hold set FA_ERR_INVALID_ARG in the
+ *              status word (fa_get_status); bad lengths: the outputs stay as
+ *              they are; a bad page: it reads as zeros, or is not written.
+ */
+
+/*
+ * fa_fwd_varlen — the forward pass over packed sequences.
+ *   in : q, k, v, cu_q [B + 1], cu_k [B + 1] (sequence b has the rows
+ *        cu_k[b] .. cu_k[b + 1] - 1 of k and v; cu_k may be cu_q)
+ *   out: o, lse
+ */
+int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_q, const int* cu_k,
+                  int B, int Hq, int Hkv, int total_q, int total_k, int d, long long q_stride, long long k_stride,
+                  long long v_stride, float scale, int window_left, int window_right, void* stream);
+
+/*
+ * fa_fwd_paged — the forward pass of new tokens over a paged cache: one token
+ *   per sequence, a chunk, a whole prompt, or any mixture in one call.
+ *   in : q, cu_q [B + 1]
+ *        k_pages, v_pages [num_pages, page_size, Hkv, d] (bf16, contiguous),
+ *        page_size a multiple of 16
+ *        lens_k [B]: keys of each sequence (with its new tokens, if those are
+ *        in the cache), at most max_pages * page_size
+ *        page_table [B, max_pages]: key j of sequence b is row j % page_size of
+ *        page page_table[b][j / page_size]; entries past its last page are
+ *        not read
+ *   out: o, lse
+ */
+int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse, const int* cu_q,
+                 const int* lens_k, const int* page_table, int B, int Hq, int Hkv, int total_q, int num_pages,
+                 int page_size, int max_pages, int d, long long q_stride, float scale, int window_left,
+                 int window_right, void* stream);
+
+/*
+ * fa_cache_append — the new tokens' k and v into the pages: row i of sequence
+ *   b goes to place lens_k[b] - n_b + i of the sequence (lens_k: the lengths
+ *   with the new tokens, as fa_fwd_paged takes them next; n_b <= lens_k[b]).
+ *   Every other row of the pages stays as it is. Two rows that the table
+ *   sends to one place leave either's values. Needs no workspace.
+ */
+int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, const int* cu_q, const int* lens_k,
+                    const int* page_table, int B, int Hkv, int total_q, int num_pages, int page_size, int max_pages,
+                    int d, long long k_stride, long long v_stride, void* stream);
+
+/*
  * fa_get_status — synchronises `stream`, then returns and clears the
  * current device's status word: FA_OK, or FA_ERR_TIMEOUT if any kernel of
- * this library gave up on a bounded wait since the last call. A CUDA error
- * seen while synchronising is returned as FA_ERR_LAUNCH.
+ * this library gave up on a bounded wait since the last call, or else
+ * FA_ERR_INVALID_ARG if one found lengths or pages on the device that its
+ * tensors cannot hold. A CUDA error seen while synchronising is returned as
+ * FA_ERR_LAUNCH.
  */
 int fa_get_status(void* stream);
 
