@@ -19,7 +19,8 @@ import os
 
 __all__ = ["FAError", "lib", "fa_fwd", "fa_bwd", "fa_bwd_noalloc", "fa_bwd_launches", "fa_get_status", "fa_status_string", "fa_debug_set",
            "fa_debug_exp2", "fa_tune", "TUNE_EXP2_SPLIT", "TUNE_CTA_PAIRS", "TUNE_BWD_SPLIT", "fa_profile_events", "fa_trace", "forward", "backward", "STATUS",
-           "fa_fwd_varlen", "fa_fwd_paged", "fa_cache_append", "forward_varlen", "forward_paged", "cache_append"]
+           "fa_fwd_varlen", "fa_bwd_varlen", "fa_fwd_paged", "fa_cache_append", "forward_varlen", "backward_varlen",
+           "forward_paged", "cache_append"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -71,6 +72,8 @@ def lib() -> ctypes.CDLL:
         ll = ctypes.c_longlong
         L.fa_fwd_varlen.argtypes = [vp] * 7 + [i] * 6 + [ll, ll, ll, f, i, i, vp]
         L.fa_fwd_varlen.restype = i
+        L.fa_bwd_varlen.argtypes = [vp] * 11 + [i] * 6 + [ll, ll, ll, f, i, i, vp]
+        L.fa_bwd_varlen.restype = i
         L.fa_fwd_paged.argtypes = [vp] * 8 + [i] * 8 + [ll, f, i, i, vp]
         L.fa_fwd_paged.restype = i
         L.fa_cache_append.argtypes = [vp] * 7 + [i] * 7 + [ll, ll, vp]
@@ -290,6 +293,13 @@ def fa_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, B, Hq, Hkv, total_q, total_k, d, 
                                int(window_right), _stream(stream))
 
 
+def fa_bwd_varlen(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, B, Hq, Hkv, total_q, total_k, d, q_stride, k_stride,
+                  v_stride, scale, window_left, window_right, stream=None) -> int:
+    return lib().fa_bwd_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv),
+                               _ptr(cu_q), _ptr(cu_k), B, Hq, Hkv, total_q, total_k, d, q_stride, k_stride, v_stride,
+                               float(scale), int(window_left), int(window_right), _stream(stream))
+
+
 def fa_fwd_paged(q, k_pages, v_pages, o, lse, cu_q, lens_k, page_table, B, Hq, Hkv, total_q, num_pages, page_size,
                  max_pages, d, q_stride, scale, window_left, window_right, stream=None) -> int:
     return lib().fa_fwd_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(o), _ptr(lse), _ptr(cu_q), _ptr(lens_k),
@@ -361,6 +371,12 @@ class _on:
             g.__exit__(*exc)
 
 
+def _packed(name, t, shape, device):
+    import torch
+    if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous bf16 tensor of shape {shape} on {device}")
+
+
 def _seq_out(q, out):
     """The given (o, lse) after a check, or new ones."""
     import torch
@@ -369,8 +385,7 @@ def _seq_out(q, out):
         return (torch.empty((total, hq, d), device=q.device, dtype=torch.bfloat16),
                 torch.empty((hq, total), device=q.device, dtype=torch.float32))
     o, lse = out
-    if tuple(o.shape) != (total, hq, d) or o.dtype != torch.bfloat16 or not o.is_contiguous() or o.device != q.device:
-        raise ValueError(f"o must be a contiguous bf16 tensor of shape {(total, hq, d)} on {q.device}")
+    _packed("o", o, (total, hq, d), q.device)
     if tuple(lse.shape) != (hq, total) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != q.device:
         raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(hq, total)} on {q.device}")
     return o, lse
@@ -397,6 +412,38 @@ def forward_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | Non
     if st != 0:
         raise FAError(st, "fa_fwd_varlen")
     return o, lse
+
+
+def backward_varlen(q, k, v, o, lse, dout, cu_q, cu_k, causal: bool = False, scale: float | None = None, out=None,
+                    stream=None, window=None):
+    """dQ [total_q, Hq, d], dK, dV [total_k, Hkv, d] for the forward_varlen
+    that gave o and lse (same offsets, mask and scale); dout [total_q, Hq, d].
+    Rows outside every sequence are left as they are (unset in new outputs)."""
+    import torch
+    qs = _tokens("q", q)
+    total_q, hq, d = q.shape
+    total_k, hkv = k.shape[0], k.shape[1]
+    ks, vs = _tokens("k", k, q.device, (total_k, hkv, d)), _tokens("v", v, q.device, (total_k, hkv, d))
+    B = cu_q.shape[0] - 1
+    _ints("cu_q", cu_q, (B + 1,), q.device)
+    _ints("cu_k", cu_k, (B + 1,), q.device)
+    _seq_out(q, (o, lse))
+    _packed("dout", dout, (total_q, hq, d), q.device)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(q.device, stream):
+        if out is None:
+            dq, dk, dv = (torch.empty(s, device=q.device, dtype=torch.bfloat16)
+                          for s in ((total_q, hq, d), (total_k, hkv, d), (total_k, hkv, d)))
+        else:
+            dq, dk, dv = out
+            _packed("dq", dq, (total_q, hq, d), q.device)
+            _packed("dk", dk, (total_k, hkv, d), q.device)
+            _packed("dv", dv, (total_k, hkv, d), q.device)
+        st = fa_bwd_varlen(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, B, hq, hkv, total_q, total_k, d, qs, ks, vs,
+                           scale, *_window_args(causal, window))
+    if st != 0:
+        raise FAError(st, "fa_bwd_varlen")
+    return dq, dk, dv
 
 
 def forward_paged(q, k_pages, v_pages, cu_q, lens_k, page_table, causal: bool = True, scale: float | None = None,

@@ -371,22 +371,21 @@ int seq_result(cudaError_t e) {
 }
 }  // namespace
 
-extern "C" int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_q,
-                             const int* cu_k, int B, int Hq, int Hkv, int total_q, int total_k, int d,
-                             long long q_stride, long long k_stride, long long v_stride, float scale, int window_left,
-                             int window_right, void* stream) {
+namespace {
+// the checks of fa_fwd_varlen and fa_bwd_varlen, and their common problem
+int varlen_problem(SeqProblem& p, const void* q, const void* k, const void* v, const int* cu_q, const int* cu_k, int B,
+                   int Hq, int Hkv, int total_q, int total_k, int d, long long q_stride, long long k_stride,
+                   long long v_stride, float scale, int window_left, int window_right) {
   int st = check_seq_sizes(B, Hq, Hkv, total_q, d);
   if (st == FA_OK) st = check_seq_sizes(B, Hq, Hkv, total_k, d);
   if (st != FA_OK) return st;
   if (!std::isfinite(scale) || !aligned4(cu_q) || !aligned4(cu_k)) return FA_ERR_INVALID_ARG;
-  if (total_q > 0 && (!aligned16(q) || !aligned16(o) || !aligned16(lse))) return FA_ERR_INVALID_ARG;
+  if (total_q > 0 && !aligned16(q)) return FA_ERR_INVALID_ARG;
   if (total_k > 0 && (!aligned16(k) || !aligned16(v))) return FA_ERR_INVALID_ARG;
   st = check_stride(q_stride, Hq, d, total_q);
   if (st == FA_OK) st = check_stride(k_stride, Hkv, d, total_k);
   if (st == FA_OK) st = check_stride(v_stride, Hkv, d, total_k);
-  if (st == FA_OK) st = check_device();
-  if (st != FA_OK || total_q == 0) return st;
-  SeqProblem p{};
+  if (st != FA_OK) return st;
   p.q = q;
   p.k = k;
   p.v = v;
@@ -404,7 +403,38 @@ extern "C" int fa_fwd_varlen(const void* q, const void* k, const void* v, void* 
   p.scale = scale;
   p.window_left = clip_window(window_left, 1LL * total_q + total_k);
   p.window_right = clip_window(window_right, 1LL * total_q + total_k);
+  return FA_OK;
+}
+}  // namespace
+
+extern "C" int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* lse, const int* cu_q,
+                             const int* cu_k, int B, int Hq, int Hkv, int total_q, int total_k, int d,
+                             long long q_stride, long long k_stride, long long v_stride, float scale, int window_left,
+                             int window_right, void* stream) {
+  SeqProblem p{};
+  int st = varlen_problem(p, q, k, v, cu_q, cu_k, B, Hq, Hkv, total_q, total_k, d, q_stride, k_stride, v_stride, scale,
+                          window_left, window_right);
+  if (st == FA_OK && total_q > 0 && (!aligned16(o) || !aligned16(lse))) st = FA_ERR_INVALID_ARG;
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total_q == 0) return st;
   return seq_result(launch_seq_fwd(p, o, lse, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                             const void* dout, void* dq, void* dk, void* dv, const int* cu_q, const int* cu_k, int B,
+                             int Hq, int Hkv, int total_q, int total_k, int d, long long q_stride, long long k_stride,
+                             long long v_stride, float scale, int window_left, int window_right, void* stream) {
+  SeqProblem p{};
+  int st = varlen_problem(p, q, k, v, cu_q, cu_k, B, Hq, Hkv, total_q, total_k, d, q_stride, k_stride, v_stride, scale,
+                          window_left, window_right);
+  if (st == FA_OK && total_q > 0 && (!aligned16(o) || !aligned16(lse) || !aligned16(dout) || !aligned16(dq)))
+    st = FA_ERR_INVALID_ARG;
+  if (st == FA_OK && total_k > 0 && (!aligned16(dk) || !aligned16(dv))) st = FA_ERR_INVALID_ARG;
+  // rows of the padded accumulator are counted in 32 bits
+  if (st == FA_OK && 128.0 * Hkv * (total_q / (128 / (Hq / Hkv)) + 1.0 * B) >= 2147483648.0) st = FA_ERR_UNSUPPORTED;
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || (total_q == 0 && total_k == 0)) return st;
+  return seq_result(launch_seq_bwd(p, o, lse, dout, dq, dk, dv, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,

@@ -106,6 +106,8 @@ struct SeqProblem {
 };
 // cudaErrorMemoryAllocation: the workspace could not be allocated
 cudaError_t launch_seq_fwd(const SeqProblem& p, void* o, float* lse, cudaStream_t stream);
+cudaError_t launch_seq_bwd(const SeqProblem& p, const void* o, const float* lse, const void* dout, void* dq, void* dk,
+                           void* dv, cudaStream_t stream);
 
 // Rows of k and v (row strides in elements) into the pages.
 struct AppendProblem {

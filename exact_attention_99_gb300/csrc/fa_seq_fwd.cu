@@ -38,7 +38,7 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
-#include "fa_seq.cuh"
+#include "fa_seq_plan.cuh"
 #include "sm103_math.cuh"
 #include "sm103_ptx.cuh"
 
@@ -48,251 +48,6 @@ namespace seq {
 constexpr int kThreads = 512;
 constexpr uint32_t kOCol0 = 256;
 constexpr float kTau = 8.0f;  // rescale threshold (log2 units), as in the dense forward
-constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 2048;  // of the sort by key tiles; more tiles than that sort as equal
-
-// --------------------------------------------------------------------------
-// planning
-// --------------------------------------------------------------------------
-struct PlanArgs {
-  Lens L;
-  Plan P;
-  int Hkv, group, tok, G;
-  int wl, wr;
-  unsigned* status;
-};
-
-struct Range {
-  int kt, nt;
-};
-// key tiles seen by the tokens [pos, pos + ntok) of a sequence of klen keys
-__device__ __forceinline__ Range tiles_seen(int pos, int ntok, int klen, int wl, int wr) {
-  const int lo = wl >= 0 ? max(0, pos - wl) : 0;
-  const int hi = wr >= 0 ? min(klen - 1, pos + ntok - 1 + wr) : klen - 1;
-  if (hi < lo) return Range{0, 0};
-  return Range{lo >> 7, (hi >> 7) - (lo >> 7) + 1};
-}
-
-// inclusive scan over the block (kPlanThreads threads); total in `sum`
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& sum) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, v, m);
-    if (lane >= m) v += o;
-  }
-  __syncthreads();  // the previous scan's sums have been read
-  if (lane == 31) warp_sums[w] = v;
-  __syncthreads();
-  if (w == 0) {
-    long long x = warp_sums[lane];
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, x, m);
-      if (lane >= m) x += o;
-    }
-    warp_sums[lane] = x;
-  }
-  __syncthreads();
-  sum = warp_sums[31];
-  return v + (w > 0 ? warp_sums[w - 1] : 0);
-}
-
-// the sequence of unit u: the last b with ustart[b] <= u
-__device__ __forceinline__ int seq_of_unit(const int* ustart, int B, int u) {
-  int lo = 0, hi = B;  // ustart[lo] <= u < ustart[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ustart[mid] <= u) {
-      lo = mid;
-    } else {
-      hi = mid;
-    }
-  }
-  return lo;
-}
-
-// One block. A unit is a block of 2 * tok tokens of a sequence (its last one
-// may be shorter); an item is a unit, or part of one, for one kv head.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
-  __shared__ long long sums[32];
-  __shared__ int hist[kBuckets];
-  __shared__ long long worst;
-  __shared__ int bad;
-  const int tid = threadIdx.x;
-  const int B = a.L.B, G = a.G, ut = 2 * a.tok;
-  const Plan& P = a.P;
-  if (tid == 0) {
-    bad = 0;
-    worst = 0;
-  }
-  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
-  for (int c = tid; c < G; c += kPlanThreads) {
-    P.first[c] = 0x7fffffff;
-    P.last[c] = -1;
-    P.cuts[c].c1 = -1;
-  }
-  grid_dep_launch();  // the main kernel may start its set-up meanwhile
-  // units of each sequence
-  long long n_units = 0, sum;
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int n = 0;
-    if (b < B) {
-      Seq s;
-      if (seq_at(a.L, b, s)) {
-        n = (s.qlen + ut - 1) / ut;
-      } else {
-        bad = 1;
-      }
-    }
-    const long long end = block_scan(n, sums, sum) + n_units;
-    if (b < B) P.ustart[b] = int(end - n < P.max_units ? end - n : P.max_units);
-    n_units += sum;
-  }
-  __syncthreads();
-  if (bad || n_units > P.max_units) {  // lengths that the tensors cannot hold: nothing is computed
-    if (tid == 0) {
-      *P.head = PlanHead{0, 0, {0, 0}};
-      atomicOr(a.status, kDevBadArg);
-    }
-    return;
-  }
-  const int U = int(n_units);
-  if (tid == 0) P.ustart[B] = U;
-  __syncthreads();
-  // key tiles of each unit: their running sum, their histogram
-  auto unit = [&](int u, Seq& s, int& t0, int& ntok, int& b) -> Range {
-    b = seq_of_unit(P.ustart, B, u);
-    seq_at(a.L, b, s);
-    t0 = (u - P.ustart[b]) * ut;
-    ntok = min(ut, s.qlen - t0);
-    return tiles_seen(s.klen - s.qlen + t0, ntok, s.klen, a.wl, a.wr);
-  };
-  long long T = 0;
-  for (int u0 = 0; u0 < U; u0 += kPlanThreads) {
-    const int u = u0 + tid;
-    int n = 0;
-    if (u < U) {
-      Seq s;
-      int t0, ntok, b;
-      n = unit(u, s, t0, ntok, b).nt;
-      atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1);
-    }
-    const long long end = block_scan(n, sums, sum) + T;
-    if (u < U) P.cost[u] = end - n;
-    T += sum;
-  }
-  if (tid == 0) P.cost[U] = T;
-  __syncthreads();
-  // sorted order, most key tiles first (order within a bucket is arbitrary and
-  // changes no result)
-  {
-    long long base = 0;
-    for (int i0 = 0; i0 < kBuckets; i0 += kPlanThreads) {
-      const int n = hist[i0 + tid];
-      const long long end = block_scan(n, sums, sum) + base;
-      hist[i0 + tid] = int(end - n);
-      base += sum;
-    }
-    __syncthreads();
-  }
-  for (int u = tid; u < U; u += kPlanThreads) {
-    const int n = int(P.cost[u + 1] - P.cost[u]);
-    P.order[atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1)] = u;
-  }
-  __syncthreads();
-  // The longest worker in sorted order against an even division, in half key
-  // tiles: an item costs one more tile than it has, parts cost their store
-  // and the last kernel.
-  const long long n_items = 1LL * U * a.Hkv;
-  for (int c = tid; c < G; c += kPlanThreads) {
-    long long t = 0;
-    for (long long r = 0; r * G < n_items; ++r) {
-      const long long i = r * G + ((r & 1) ? G - 1 - c : c);
-      if (i < n_items) {
-        const int u = P.order[i / a.Hkv];
-        t += 2 * (P.cost[u + 1] - P.cost[u]) + 1;
-      }
-    }
-    atomicMax(reinterpret_cast<unsigned long long*>(&worst), static_cast<unsigned long long>(t));
-  }
-  __syncthreads();
-  const long long Ttot = T * a.Hkv;
-  const bool split = Ttot > 0 && worst > 2 * ((Ttot + G - 1) / G) + 8;
-  if (tid == 0) *P.head = PlanHead{int(n_items), split ? 1 : 0, {0, 0}};
-  for (long long i = tid; i < n_items; i += kPlanThreads) {
-    Seq s;
-    int t0, ntok, b;
-    Item it;
-    if (!split) {
-      const int u = P.order[i / a.Hkv];
-      const Range r = unit(u, s, t0, ntok, b);
-      it.q0 = s.q0 + t0;
-      it.ntok_flags = ntok | (ntok <= a.tok ? kKeyMode : 0);
-      it.kvh = int(i % a.Hkv);
-      it.kbase = a.L.cu_k != nullptr ? s.k0 : b;
-      it.klen = s.klen;
-      it.pos = s.klen - s.qlen + t0;
-      it.kt = r.kt;
-      it.nt = r.nt;
-      P.items[i] = it;
-      continue;
-    }
-    // order (sequence, kv head, unit): find the sequence of item i, then its
-    // place [x0, x1) among all key tiles; worker c has the tiles [y(c), y(c + 1))
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (1LL * P.ustart[mid] * a.Hkv <= i) {
-        lo = mid;
-      } else {
-        hi = mid;
-      }
-    }
-    const int us = P.ustart[lo], per = P.ustart[lo + 1] - us;
-    const int j = int(i - 1LL * us * a.Hkv);
-    const int kvh = j / per, u = us + (j - kvh * per);
-    const Range r = unit(u, s, t0, ntok, b);
-    const long long of_seq = P.cost[us + per] - P.cost[us];
-    const long long x0 = P.cost[us] * a.Hkv + kvh * of_seq + (P.cost[u] - P.cost[us]), x1 = x0 + r.nt;
-    it.q0 = s.q0 + t0;
-    it.kvh = kvh;
-    it.kbase = a.L.cu_k != nullptr ? s.k0 : b;
-    it.klen = s.klen;
-    it.pos = s.klen - s.qlen + t0;
-    const int base_flags = ntok | (ntok <= a.tok ? kKeyMode : 0);
-    auto share = [&](int c) -> long long { return Ttot * c / G; };
-    int c = int(min(x0 * G / Ttot, 1LL * G - 1));  // the worker that has tile x0 (fewer tiles than workers: the last such)
-    while (c > 0 && share(c) > x0) --c;
-    while (c + 1 < G && share(c + 1) <= x0) ++c;
-    const int c0 = c;
-    long long x = x0;
-    do {
-      const long long e = c + 1 < G ? min(x1, share(c + 1)) : x1;
-      const bool part = x > x0 || e < x1;
-      it.ntok_flags = base_flags | (part ? kPart : 0) | (x > x0 ? kCont : 0);
-      it.kt = r.kt + int(x - x0);
-      it.nt = int(e - x);
-      const int at = int(i) + c;  // one item or part per (i, c), in order; no two have the same sum
-      P.items[at] = it;
-      atomicMin(&P.first[c], at);
-      atomicMax(&P.last[c], at);
-      x = e;
-      if (x < x1)
-        do ++c;
-        while (c + 1 < G && share(c + 1) <= x);
-    } while (x < x1);
-    if (c > c0) {
-      Cut& k = P.cuts[c0 + 1];
-      k.q0 = it.q0;
-      k.ntok_flags = base_flags;
-      k.kvh = kvh;
-      k.c0 = c0;
-      k.c1 = c;
-    }
-  }
-}
 
 // --------------------------------------------------------------------------
 // main kernel
@@ -303,7 +58,7 @@ struct Params {
   const PlanHead* head;
   const int* first;
   const int* last;
-  const Item* items;
+  const FwdItem* items;
   const Cut* cuts;
   float* part_o;       // [2 G][2 * 128][D] partial O
   float2* part_ml;     // [2 G][2 * 128] their (m, l)
@@ -345,55 +100,27 @@ struct __align__(8) Ctl {
 //   key mode: stage t & 1, as its step t >> 1;
 //   else    : both stages, stage s while a[s] <= t < a[s] + n[s].
 struct Work {
-  Item it;
+  FwdItem it;
   int n[2], a[2];
   int rows[2];  // rows of each stage (key mode: both have the same)
   bool key;
 };
 
-struct Walk {
-  int i, r, G, c;
-  int n_items, last;
-  bool split;
-};
-
-__device__ __forceinline__ Walk walk_begin(const Params& p) {
-  Walk w;
-  const PlanHead h = *p.head;
-  w.G = gridDim.x;
-  w.c = blockIdx.x;
-  w.n_items = h.n_items;
-  w.split = h.split != 0;
-  w.r = 0;
-  if (w.split) {
-    w.i = p.first[w.c];
-    w.last = p.last[w.c];
-  } else {
-    w.i = w.c;
-    w.last = h.n_items - 1;
-  }
-  return w;
-}
 // the next item of this CTA, false when there is none
 __device__ __forceinline__ bool walk_next(const Params& p, Walk& w, Work& x) {
   if (w.i > w.last) return false;
   const int4* src = reinterpret_cast<const int4*>(p.items + w.i);
   const int4 u = src[0], v = src[1];
   x.it.q0 = u.x;
-  x.it.ntok_flags = u.y;
+  x.it.count = u.y;
   x.it.kvh = u.z;
   x.it.kbase = u.w;
   x.it.klen = v.x;
   x.it.pos = v.y;
   x.it.kt = v.z;
   x.it.nt = v.w;
-  if (w.split) {
-    ++w.i;
-  } else {
-    ++w.r;
-    w.i = w.r * w.G + ((w.r & 1) ? w.G - 1 - w.c : w.c);
-  }
-  x.key = (x.it.ntok_flags & kKeyMode) != 0;
+  walk_step(w);
+  x.key = (x.it.count & kKeyMode) != 0;
   const int ntok = x.it.ntok(), nt = x.it.nt;
   if (x.key) {
     x.rows[0] = x.rows[1] = ntok * p.group;
@@ -468,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();    // the plan
   grid_dep_launch();  // the joining kernel may start (and wait) meanwhile
   const uint32_t tmem = ctl.tmem_base;
-  Walk wk = walk_begin(p);
+  Walk wk = walk_begin(p.head, p.first, p.last);
   Work x;
 
   if (wg <= 1) {
@@ -623,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       // epilogue
       const int ntok = x.it.ntok();
-      const bool part = (x.it.ntok_flags & kPart) != 0;
-      const int slot = 2 * int(blockIdx.x) + ((x.it.ntok_flags & kCont) ? 0 : 1);
+      const bool part = (x.it.count & kPart) != 0;
+      const int slot = 2 * int(blockIdx.x) + ((x.it.count & kCont) ? 0 : 1);
       // the stages' rows are the same rows in key mode: one pass over both
       const int passes = x.key || ntok <= p.tok ? 1 : 2;
 #pragma unroll 1
@@ -973,7 +700,7 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
   const Cut k = p.cuts[blockIdx.x];
   if (k.c1 < 0) return;
   const int lane = threadIdx.x & 31;
-  const int ntok = k.ntok_flags & 0xffff, rows = ntok * p.group;
+  const int ntok = k.count, rows = ntok * p.group;
   const int per_stage = p.tok * p.group;
   constexpr int V = D / 32;  // columns per lane
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
@@ -1000,7 +727,7 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
       l = l * wa + ml.y * wb;
       m = mn;
     }
-    const int tok = r / p.group, head = k.kvh * p.group + (r - tok * p.group), token = k.q0 + tok;
+    const int tok = r / p.group, head = k.kvh * p.group + (r - tok * p.group), token = k.row0 + tok;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat16* dst = p.o + (size_t(token) * p.Hq + head) * D + lane * V;
     if constexpr (V == 4) {
@@ -1016,38 +743,23 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
 // --------------------------------------------------------------------------
 // launch
 // --------------------------------------------------------------------------
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 // the workspace, carved from `base` (null: its size alone)
 struct Space {
-  Plan plan;
+  Plan<FwdItem> plan;
   float* part_o;
   float2* part_ml;
   size_t bytes;
 };
 Space carve(uint8_t* base, const SeqProblem& pb, int G, int tok) {
   Space s{};
-  size_t at = 0;
-  auto take = [&](size_t n) {
-    uint8_t* r = base == nullptr ? nullptr : base + at;
-    at += align256(n);
-    return r;
-  };
+  Carver c{base, 0};
   // a sequence of n tokens has ceil(n / (2 tok)) units
   long long units = pb.total_q / (2 * tok) + pb.B;
   if (units > pb.total_q) units = pb.total_q;
-  s.plan.max_units = int(units);
-  s.plan.head = reinterpret_cast<PlanHead*>(take(sizeof(PlanHead)));
-  s.plan.first = reinterpret_cast<int*>(take(sizeof(int) * G));
-  s.plan.last = reinterpret_cast<int*>(take(sizeof(int) * G));
-  s.plan.cuts = reinterpret_cast<Cut*>(take(sizeof(Cut) * G));
-  s.plan.ustart = reinterpret_cast<int*>(take(sizeof(int) * (size_t(pb.B) + 1)));
-  s.plan.cost = reinterpret_cast<long long*>(take(sizeof(long long) * (units + 1)));
-  s.plan.order = reinterpret_cast<int*>(take(sizeof(int) * units));
-  s.plan.items = reinterpret_cast<Item*>(take(sizeof(Item) * (units * pb.Hkv + G)));
-  s.part_ml = reinterpret_cast<float2*>(take(sizeof(float2) * 2 * G * 256));
-  s.part_o = reinterpret_cast<float*>(take(sizeof(float) * 2 * G * 256 * pb.d));
-  s.bytes = at;
+  s.plan = carve_plan<FwdItem>(c, pb.B, units, pb.Hkv, G);
+  s.part_ml = c.take<float2>(size_t(2) * G * 256);
+  s.part_o = c.take<float>(size_t(2) * G * 256 * pb.d);
+  s.bytes = c.at;
   return s;
 }
 
@@ -1097,15 +809,13 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr, pb, G, tok).bytes, pool, stream) != cudaSuccess)
     return cudaErrorMemoryAllocation;
   const Space sp = carve(static_cast<uint8_t*>(ws), pb, G, tok);
-  PlanArgs a{};
+  PlanArgs<FwdSide> a{};
   a.L = Lens{pb.cu_q, pb.cu_k, pb.lens_k, pb.B, pb.total_q, pb.total_k, 1LL * pb.max_pages * pb.page_size};
   a.P = sp.plan;
+  a.side = FwdSide{tok, pb.window_left, pb.window_right, pb.page_table != nullptr ? 1 : 0};
   a.Hkv = pb.Hkv;
-  a.group = group;
-  a.tok = tok;
   a.G = G;
-  a.wl = pb.window_left;
-  a.wr = pb.window_right;
+  a.part_cost = 8;
   a.status = p.status;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -1131,7 +841,7 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   const DebugCfg dc = debug_cfg();
   p.wait_limit_ns = dc.wait_limit_ns;
   p.inject = dc.inject;
-  plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  plan_kernel<FwdSide><<<1, kPlanThreads, 0, stream>>>(a);
   e = cudaGetLastError();
   // the kernels after it start while the one before ends, and wait for it
   cudaLaunchAttribute pdl[1];

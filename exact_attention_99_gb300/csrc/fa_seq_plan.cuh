@@ -1,0 +1,425 @@
+// The division of work of the calls on sequences of different lengths, made
+// on the device (the lengths are there) by one block before the main kernel.
+//
+// Work is counted in tile products. The forward's unit is up to two tiles of
+// query rows of a sequence and its n key tiles; the backward's is a key tile
+// and its n tiles of query rows; either for every kv head. A tile of query
+// rows holds `tok` = 128 / group tokens with all query heads of the group
+// (row = token * group + head), so that they share the key tiles.
+//
+// Two divisions, whichever promises the earlier end:
+//   sorted: the units by n, longest first, over the CTAs in snake order;
+//   split : all tile products laid end to end (sequence, kv head, unit), an
+//           equal share to each CTA. A unit that a boundary falls into is
+//           done in parts, and a last kernel joins them in the CTAs' order.
+// Sorted order leaves no parts and ends within its shortest units where there
+// are many; few units (a chunk of new tokens over long caches) would leave
+// CTAs idle, and are split.
+#pragma once
+#include "fa_seq.cuh"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+namespace seq {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBuckets = 2048;  // of the sort by n; units of more tiles sort as equal
+
+// An item is a unit, or a part of one, for one kv head.
+struct __align__(16) FwdItem {
+  int q0;     // first packed token
+  int count;  // tokens (at most 2 * tok, in the low 16 bits) and the flags below
+  int kvh;
+  int kbase;  // packed: the sequence's first key row; paged: the sequence
+  int klen;
+  int pos;    // place of the first token among the keys (klen - qlen + its place in the sequence)
+  int kt, nt; // key tiles [kt, kt + nt)
+  __device__ __forceinline__ int ntok() const { return count & 0xffff; }
+};
+static_assert(sizeof(FwdItem) == 32, "two 16-byte loads");
+
+struct __align__(16) BwdItem {
+  int krow;   // first packed key row of the tile
+  int count;  // its keys (at most 128, in the low 16 bits) and the flags below
+  int kvh;
+  int q0, qlen;  // the sequence's queries
+  int rel;       // place of its first token among the tile's keys: klen - qlen - 128 * (tile)
+  int tiles;     // first row tile of the sequence in the padded arrays
+  int i0, n;     // row tiles [i0, i0 + n) of the sequence
+  int pad[3];
+  __device__ __forceinline__ int nkey() const { return count & 0xffff; }
+};
+static_assert(sizeof(BwdItem) == 48, "three 16-byte loads");
+
+// Forward, at most `tok` tokens (one tile of rows): the two stages of the
+// pipeline take alternate key tiles of the same rows; else each has rows of its own.
+constexpr int kKeyMode = 1 << 16;
+// The item is part of a unit: its results go to a slot, to be joined with the
+// other parts'. kCont: not the unit's first part.
+constexpr int kPart = 1 << 17;
+constexpr int kCont = 1 << 18;
+
+// A unit divided between the workers c0 .. c1: parts in slot 2 * c0 + 1 and,
+// for the others that have a share, slot 2 * c. Kept at index c0 + 1.
+struct Cut {
+  int row0, count, kvh, c0, c1;  // c1 < 0: nothing
+  int pad[3];
+};
+
+struct PlanHead {
+  int n_items;  // sorted: worker c takes items c, 2G-1-c, 2G+c, ...
+  int split;    // 1: worker c takes items [first[c], last[c]] instead
+  int bad;      // the lengths say something that the tensors cannot hold
+  int pad;
+};
+
+template <class Item>
+struct Plan {
+  PlanHead* head;
+  int* first;       // [G]
+  int* last;        // [G]
+  Cut* cuts;        // [G]
+  int* ustart;      // [B + 1] first unit of each sequence
+  int* tstart;      // [B + 1] first row tile of each sequence
+  long long* cost;  // [units + 1] tile products of the units before
+  int* order;       // [units] longest first
+  Item* items;      // [units * Hkv + G]
+  int max_units;
+};
+
+// Takes pieces of a workspace, 256-byte aligned (base null: sizes alone).
+struct Carver {
+  uint8_t* base;
+  size_t at;
+  template <class T>
+  T* take(size_t n) {
+    uint8_t* r = base == nullptr ? nullptr : base + at;
+    at += (n * sizeof(T) + 255) & ~size_t(255);
+    return reinterpret_cast<T*>(r);
+  }
+};
+template <class Item>
+Plan<Item> carve_plan(Carver& c, int B, long long units, int Hkv, int G) {
+  Plan<Item> p{};
+  p.max_units = int(units);
+  p.head = c.take<PlanHead>(1);
+  p.first = c.take<int>(G);
+  p.last = c.take<int>(G);
+  p.cuts = c.take<Cut>(G);
+  p.ustart = c.take<int>(size_t(B) + 1);
+  p.tstart = c.take<int>(size_t(B) + 1);
+  p.cost = c.take<long long>(size_t(units) + 1);
+  p.order = c.take<int>(size_t(units));
+  p.items = c.take<Item>(size_t(units) * Hkv + G);
+  return p;
+}
+
+#ifdef __CUDACC__
+
+struct Range {
+  int first, n;
+};
+
+struct FwdSide {
+  using Item = FwdItem;
+  int tok, wl, wr, paged;
+  __device__ __forceinline__ int units(const Seq& s) const { return (s.qlen + 2 * tok - 1) / (2 * tok); }
+  __device__ __forceinline__ int row_tiles(const Seq&) const { return 0; }
+  // key tiles seen by unit j's tokens
+  __device__ __forceinline__ Range range(const Seq& s, int j) const {
+    const int t0 = j * 2 * tok, ntok = min(2 * tok, s.qlen - t0), pos = s.klen - s.qlen + t0;
+    const int lo = wl >= 0 ? max(0, pos - wl) : 0;
+    const int hi = wr >= 0 ? min(s.klen - 1, pos + ntok - 1 + wr) : s.klen - 1;
+    if (hi < lo) return Range{0, 0};
+    return Range{lo >> 7, (hi >> 7) - (lo >> 7) + 1};
+  }
+  __device__ __forceinline__ Item item(const Seq& s, int b, int j, int kvh, int) const {
+    Item it;
+    const int t0 = j * 2 * tok, ntok = min(2 * tok, s.qlen - t0);
+    it.q0 = s.q0 + t0;
+    it.count = ntok | (ntok <= tok ? kKeyMode : 0);
+    it.kvh = kvh;
+    it.kbase = paged ? b : s.k0;
+    it.klen = s.klen;
+    it.pos = s.klen - s.qlen + t0;
+    return it;
+  }
+  __device__ __forceinline__ static void set_range(Item& it, int first, int n) {
+    it.kt = first;
+    it.nt = n;
+  }
+  __device__ __forceinline__ static int row0(const Item& it) { return it.q0; }
+};
+
+struct BwdSide {
+  using Item = BwdItem;
+  int tok, wl, wr;
+  __device__ __forceinline__ int units(const Seq& s) const { return (s.klen + 127) >> 7; }
+  __device__ __forceinline__ int row_tiles(const Seq& s) const { return (s.qlen + tok - 1) / tok; }
+  // row tiles with a token that sees a key of tile j
+  __device__ __forceinline__ Range range(const Seq& s, int j) const {
+    const int off = s.klen - s.qlen, k0 = j * 128, k1 = min(k0 + 127, s.klen - 1);
+    const int lo = wr >= 0 ? max(0, k0 - off - wr) : 0;
+    const int hi = wl >= 0 ? min(s.qlen - 1, k1 - off + wl) : s.qlen - 1;
+    if (hi < lo) return Range{0, 0};
+    return Range{lo / tok, hi / tok - lo / tok + 1};
+  }
+  __device__ __forceinline__ Item item(const Seq& s, int, int j, int kvh, int tiles) const {
+    Item it;
+    it.krow = s.k0 + j * 128;
+    it.count = min(128, s.klen - j * 128);
+    it.kvh = kvh;
+    it.q0 = s.q0;
+    it.qlen = s.qlen;
+    it.rel = s.klen - s.qlen - j * 128;
+    it.tiles = tiles;
+    return it;
+  }
+  __device__ __forceinline__ static void set_range(Item& it, int first, int n) {
+    it.i0 = first;
+    it.n = n;
+  }
+  __device__ __forceinline__ static int row0(const Item& it) { return it.krow; }
+};
+
+template <class Side>
+struct PlanArgs {
+  Lens L;
+  Plan<typename Side::Item> P;
+  Side side;
+  int Hkv, G;
+  int part_cost;  // what dividing units costs, in half tile products
+  unsigned* status;
+};
+
+// inclusive scan over the block (kPlanThreads threads); total in `sum`
+__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& sum) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, v, m);
+    if (lane >= m) v += o;
+  }
+  __syncthreads();  // the previous scan's sums have been read
+  if (lane == 31) warp_sums[w] = v;
+  __syncthreads();
+  if (w == 0) {
+    long long x = warp_sums[lane];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, x, m);
+      if (lane >= m) x += o;
+    }
+    warp_sums[lane] = x;
+  }
+  __syncthreads();
+  sum = warp_sums[31];
+  return v + (w > 0 ? warp_sums[w - 1] : 0);
+}
+
+// the last b in [0, B) with start[b] * scale <= x
+__device__ __forceinline__ int find_seq(const int* start, int B, int scale, long long x) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (1LL * start[mid] * scale <= x) {
+      lo = mid;
+    } else {
+      hi = mid;
+    }
+  }
+  return lo;
+}
+
+template <class Side>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side> a) {
+  using Item = typename Side::Item;
+  __shared__ long long sums[32];
+  __shared__ int hist[kBuckets];
+  __shared__ unsigned long long worst;
+  __shared__ int bad;
+  const int tid = threadIdx.x;
+  const int B = a.L.B, G = a.G;
+  const Plan<Item>& P = a.P;
+  if (tid == 0) {
+    bad = 0;
+    worst = 0;
+  }
+  for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+  for (int c = tid; c < G; c += kPlanThreads) {
+    P.first[c] = 0x7fffffff;
+    P.last[c] = -1;
+    P.cuts[c].c1 = -1;
+  }
+  grid_dep_launch();  // the next kernel may start its set-up meanwhile
+  __syncthreads();
+  // units (low half) and row tiles (high half) of the sequences before each
+  long long n_units = 0, sum;
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    long long n = 0;
+    if (b < B) {
+      Seq s;
+      if (seq_at(a.L, b, s)) {
+        n = a.side.units(s) | (static_cast<long long>(a.side.row_tiles(s)) << 32);
+      } else {
+        bad = 1;
+      }
+    }
+    const long long end = block_scan(n, sums, sum) + n_units;
+    if (b < B) {
+      P.ustart[b] = int((end - n) & 0x7fffffff);
+      P.tstart[b] = int((end - n) >> 32);
+    }
+    n_units += sum;
+  }
+  __syncthreads();
+  // lengths that the tensors cannot hold (overlapping sequences among them,
+  // by their sum): nothing is computed
+  if (bad || (n_units & 0xffffffffll) > P.max_units) {
+    if (tid == 0) {
+      *P.head = PlanHead{0, 0, 1, 0};
+      atomicOr(a.status, kDevBadArg);
+    }
+    return;
+  }
+  const int U = int(n_units & 0xffffffffll);
+  if (tid == 0) {
+    P.ustart[B] = U;
+    P.tstart[B] = int(n_units >> 32);
+  }
+  __syncthreads();
+  // n of each unit: running sum and histogram
+  long long T = 0;
+  for (int u0 = 0; u0 < U; u0 += kPlanThreads) {
+    const int u = u0 + tid;
+    int n = 0;
+    if (u < U) {
+      Seq s;
+      const int b = find_seq(P.ustart, B, 1, u);
+      seq_at(a.L, b, s);
+      n = a.side.range(s, u - P.ustart[b]).n;
+      atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1);
+    }
+    const long long end = block_scan(n, sums, sum) + T;
+    if (u < U) P.cost[u] = end - n;
+    T += sum;
+  }
+  if (tid == 0) P.cost[U] = T;
+  __syncthreads();
+  // sorted order (arbitrary within a bucket, which changes no result)
+  long long base = 0;
+  for (int i0 = 0; i0 < kBuckets; i0 += kPlanThreads) {
+    const int n = hist[i0 + tid];
+    const long long end = block_scan(n, sums, sum) + base;
+    hist[i0 + tid] = int(end - n);
+    base += sum;
+  }
+  __syncthreads();
+  for (int u = tid; u < U; u += kPlanThreads) {
+    const int n = int(P.cost[u + 1] - P.cost[u]);
+    P.order[atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1)] = u;
+  }
+  __syncthreads();
+  // The busiest worker in sorted order against an equal division, in half
+  // tile products: an item costs half a product more than it has; dividing
+  // costs part_cost (the parts' stores and the last kernel).
+  const long long n_items = 1LL * U * a.Hkv;
+  for (int c = tid; c < G; c += kPlanThreads) {
+    unsigned long long t = 0;
+    for (long long r = 0; r * G < n_items; ++r) {
+      const long long i = r * G + ((r & 1) ? G - 1 - c : c);
+      if (i < n_items) {
+        const int u = P.order[i / a.Hkv];
+        t += 2 * (P.cost[u + 1] - P.cost[u]) + 1;
+      }
+    }
+    atomicMax(&worst, t);
+  }
+  __syncthreads();
+  const long long Ttot = T * a.Hkv;
+  const bool split = Ttot > 0 && static_cast<long long>(worst) > 2 * ((Ttot + G - 1) / G) + a.part_cost;
+  if (tid == 0) *P.head = PlanHead{int(n_items), split ? 1 : 0, 0, 0};
+  auto share = [&](int c) -> long long { return Ttot * c / G; };
+  for (long long i = tid; i < n_items; i += kPlanThreads) {
+    Seq s;
+    if (!split) {
+      const int u = P.order[i / a.Hkv], b = find_seq(P.ustart, B, 1, u);
+      seq_at(a.L, b, s);
+      const Range r = a.side.range(s, u - P.ustart[b]);
+      Item it = a.side.item(s, b, u - P.ustart[b], int(i % a.Hkv), P.tstart[b]);
+      Side::set_range(it, r.first, r.n);
+      P.items[i] = it;
+      continue;
+    }
+    // order (sequence, kv head, unit): the place [x0, x1) of item i among all
+    // tile products; worker c has [share(c), share(c + 1))
+    const int b = find_seq(P.ustart, B, a.Hkv, i);
+    seq_at(a.L, b, s);
+    const int us = P.ustart[b], per = P.ustart[b + 1] - us;
+    const int j = int(i - 1LL * us * a.Hkv), kvh = j / per, ju = j - kvh * per;
+    const Range r = a.side.range(s, ju);
+    const long long of_seq = P.cost[us + per] - P.cost[us];
+    const long long x0 = P.cost[us] * a.Hkv + kvh * of_seq + (P.cost[us + ju] - P.cost[us]), x1 = x0 + r.n;
+    Item it = a.side.item(s, b, ju, kvh, P.tstart[b]);
+    const int count = it.count;
+    // the worker that has product x0 (fewer products than workers: the last
+    // of those whose share begins there)
+    int c = int(min(x0 * G / Ttot, 1LL * G - 1));
+    while (c > 0 && share(c) > x0) --c;
+    while (c + 1 < G && share(c + 1) <= x0) ++c;
+    const int c0 = c;
+    long long x = x0;
+    do {
+      const long long e = c + 1 < G ? min(x1, share(c + 1)) : x1;
+      const bool part = x > x0 || e < x1;
+      it.count = count | (part ? kPart : 0) | (x > x0 ? kCont : 0);
+      Side::set_range(it, r.first + int(x - x0), int(e - x));
+      // one entry per (item, worker), in order: no two have the same sum, and
+      // a worker's entries follow one another
+      const int at = int(i) + c;
+      P.items[at] = it;
+      atomicMin(&P.first[c], at);
+      atomicMax(&P.last[c], at);
+      x = e;
+      if (x < x1)
+        do ++c;
+        while (c + 1 < G && share(c + 1) <= x);
+    } while (x < x1);
+    if (c > c0) {
+      Cut& k = P.cuts[c0 + 1];
+      k.row0 = Side::row0(it);
+      k.count = count & 0xffff;
+      k.kvh = kvh;
+      k.c0 = c0;
+      k.c1 = c;
+    }
+  }
+}
+
+// A worker's walk over its items.
+struct Walk {
+  int i, r, last;
+  bool split;
+};
+__device__ __forceinline__ Walk walk_begin(const PlanHead* head, const int* first, const int* last) {
+  Walk w;
+  w.split = head->split != 0;
+  w.r = 0;
+  w.i = w.split ? first[blockIdx.x] : int(blockIdx.x);
+  w.last = w.split ? last[blockIdx.x] : head->n_items - 1;
+  return w;
+}
+__device__ __forceinline__ void walk_step(Walk& w) {
+  if (w.split) {
+    ++w.i;
+  } else {
+    ++w.r;
+    w.i = w.r * int(gridDim.x) + ((w.r & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
+  }
+}
+
+#endif  // __CUDACC__
+
+}  // namespace seq
+}  // namespace fa

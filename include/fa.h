@@ -264,6 +264,21 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
                   long long v_stride, float scale, int window_left, int window_right, void* stream);
 
 /*
+ * fa_bwd_varlen — the backward pass of fa_fwd_varlen for L = sum(dout * o).
+ *   in : q, k, v, cu_q, cu_k and the strides as the forward had them; o, lse as
+ *        it wrote them; dout [total_q, Hq, d] (contiguous)
+ *   out: dq [total_q, Hq, d], dk, dv [total_k, Hkv, d] (bf16, contiguous): the
+ *        rows of every sequence; other rows are left as they are.
+ * dk and dv are sums over the query heads of a group, taken in a fixed order;
+ * the additions into dq are not ordered (as in fa_bwd). Workspace: fp32 dQ
+ * (about 4 * total_q * Hq * d bytes) and 80 MB at d = 128.
+ */
+int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                  void* dq, void* dk, void* dv, const int* cu_q, const int* cu_k, int B, int Hq, int Hkv, int total_q,
+                  int total_k, int d, long long q_stride, long long k_stride, long long v_stride, float scale,
+                  int window_left, int window_right, void* stream);
+
+/*
  * fa_fwd_paged — the forward pass of new tokens over a paged cache: one token
  *   per sequence, a chunk, a whole prompt, or any mixture in one call.
  *   in : q, cu_q [B + 1]

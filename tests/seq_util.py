@@ -88,6 +88,70 @@ def check_forward(o, lse, want, cu):
         assert (go[~fin.T] == 0).all(), f"sequence {b}: O of empty rows"
 
 
+def reference_backward(seqs, douts, os, scale, causal=False, window=None):
+    """Per sequence the oracle's (dQ, dK, dV) in 64 bits with elementwise
+    bounds for a backward pass that was given the bf16 outputs `os`.
+
+    Bounds. dV_j = sum_i P_ij dO_i, dS_ij = P_ij (dP_ij - D_i), dQ_i = scale sum_j
+    dS_ij K_j, dK_j = scale sum_i dS_ij Q_i, with P and dS rounded to bf16 before the
+    products (2^-8 of each term) and the results rounded to bf16 (2^-8). P
+    itself comes from 32-bit scores and the 32-bit LSE: off by 2^-11 of itself
+    (scores below 2^-12.9, see the module's notes, and as much again for LSE);
+    dP and D are sums of d fp32 products, off by (d + 2) 2^-24 sum |dO_c V_c| each.
+    D is formed from the bf16 O: dS moves by P_ij |dO_i . (O_bf16 - O)_i|.
+    With R_ij = P_ij (|dP_ij| + |D_i|) and E_ij = P_ij (|dO_i . dO_err| + 2^-15 (A_i)),
+    A_i = sum_c |dO_ic| max_j |V_jc|, the bounds are the products of (2^-8 + 2^-10) R + E
+    with |K| and |Q|."""
+    out = []
+    for (q, k, v), do, o in zip(seqs, douts, os):
+        n, hq, d = q.shape
+        m, hk, _ = k.shape
+        G = hq // hk
+        Q, K, V, DO, O = (n64(x) for x in (q, k, v, do, o))
+        dq, dk, dv = np.zeros_like(Q), np.zeros_like(K), np.zeros_like(V)
+        bq, bk, bv = np.zeros_like(Q), np.zeros_like(K), np.zeros_like(V)
+        if n and m:
+            see = attn_ref.visible_mask(np.arange(n), n, m, causal, window)
+            for h in range(hq):
+                g = h // G
+                s = np.where(see, scale * Q[:, h] @ K[:, g].T, -np.inf)
+                top = s.max(1, keepdims=True)
+                e = np.exp(s - np.where(np.isfinite(top), top, 0.0))
+                l = e.sum(1, keepdims=True)
+                p = e / np.where(l > 0, l, 1.0)
+                ex = p @ V[:, g]
+                dp = DO[:, h] @ V[:, g].T
+                D = (DO[:, h] * ex).sum(1, keepdims=True)
+                ds = p * (dp - D)
+                dq[:, h] = scale * ds @ K[:, g]
+                dk[:, g] += scale * ds.T @ Q[:, h]
+                dv[:, g] += p.T @ DO[:, h]
+                R = p * (np.abs(dp) + np.abs(D))
+                err = np.abs((DO[:, h] * (O[:, h] - ex)).sum(1, keepdims=True))
+                A = (np.abs(DO[:, h]) * np.abs(V[:, g]).max(0)).sum(1, keepdims=True)
+                t = (2.0 ** -8 + 2.0 ** -10) * R + p * (err + 2.0 ** -15 * A)
+                a = abs(scale)
+                bq[:, h] = a * t @ np.abs(K[:, g])
+                bk[:, g] += a * t.T @ np.abs(Q[:, h])
+                bv[:, g] += (2.0 ** -8 + 2.0 ** -10) * p.T @ np.abs(DO[:, h])
+        for x, b in ((dq, bq), (dk, bk), (dv, bv)):
+            b += 2.0 ** -8 * (np.abs(x) + b)
+        out.append(((dq, dk, dv), (bq, bk, bv)))
+    return out
+
+
+def check_backward(got, want, cq, ck):
+    """got: dq, dk, dv tensors; want: reference_backward()."""
+    for b, (refs, bounds) in enumerate(want):
+        for name, t, cu, ref, bound in zip(("dq", "dk", "dv"), got, (cq, ck, ck), refs, bounds):
+            x = n64(t[int(cu[b]):int(cu[b + 1])])
+            assert np.isfinite(x).all(), f"sequence {b}: {name} is not finite"
+            off = np.abs(x - ref) - bound
+            if off.size:
+                assert (off <= 0).all(), (f"sequence {b}: {name} is {off.max():.3e} beyond its bound "
+                                          f"{bound.flat[off.argmax()]:.3e} at {np.unravel_index(off.argmax(), off.shape)}")
+
+
 class Cache:
     """A paged cache filled with sequences; every unused row is NaN."""
 

@@ -22,7 +22,9 @@ PAGED = dict(q=P16, k_pages=P16, v_pages=P16, o=P16, lse=P16, cu_q=P16, lens_k=P
              window_right=0)
 APPEND = dict(k=P16, v=P16, k_pages=P16, v_pages=P16, cu_q=P16, lens_k=P16, page_table=P16, B=2, Hkv=2, total_q=50,
               num_pages=9, page_size=16, max_pages=4, d=128, k_stride=256, v_stride=256)
-CALLS = {"fa_fwd_varlen": VARLEN, "fa_fwd_paged": PAGED, "fa_cache_append": APPEND}
+BWD = dict(q=P16, k=P16, v=P16, o=P16, lse=P16, dout=P16, dq=P16, dk=P16, dv=P16)
+BWD.update({n: VARLEN[n] for n in VARLEN if n not in BWD})
+CALLS = {"fa_bwd_varlen": BWD, "fa_fwd_varlen": VARLEN, "fa_fwd_paged": PAGED, "fa_cache_append": APPEND}
 
 
 def call(fa, name, **kw):
@@ -39,7 +41,7 @@ OF_PAGES = [(dict(num_pages=0), 1), (dict(page_size=0), 1), (dict(page_size=8), 
 OF_Q = [(dict(Hq=3), 1), (dict(Hq=0), 1), (dict(Hq=258, q_stride=1 << 16), 2), (dict(scale=float("nan")), 1),
         (dict(scale=float("inf")), 1), (dict(q_stride=511), 1), (dict(q_stride=504), 1), (dict(q_stride=1 << 39), 2)]
 OF_KV = [(dict(k_stride=248), 1), (dict(v_stride=257), 1), (dict(v_stride=1 << 39), 2)]
-BAD = ([("fa_fwd_varlen", b, c) for b, c in SHARED + OF_Q + OF_KV + [(dict(total_k=-1), 1), (dict(total_k=1 << 29), 2)]]
+BAD = ([(f, b, c) for f in ("fa_fwd_varlen", "fa_bwd_varlen") for b, c in SHARED + OF_Q + OF_KV + [(dict(total_k=-1), 1), (dict(total_k=1 << 29), 2)]]
        + [("fa_fwd_paged", b, c) for b, c in SHARED + OF_Q + OF_PAGES]
        + [("fa_cache_append", b, c) for b, c in SHARED + OF_KV + OF_PAGES])
 
@@ -64,9 +66,11 @@ def test_bad_pointers(fa, name):
 def test_good_arguments_reach_the_device_check(fa, name):
     assert call(fa, name) == 6
     # nothing to do, and null pointers for it: still needs a device
-    assert call(fa, name, total_q=0, **({"q": 0, "o": 0, "lse": 0} if "q" in CALLS[name] else {"k": 0, "v": 0})) == 6
+    assert call(fa, name, total_q=0, **{a: 0 for a in ("q", "o", "lse", "dout", "dq") if a in CALLS[name]}) == 6
     if name == "fa_fwd_varlen":
         assert call(fa, name, total_k=0, k=0, v=0) == 6
+    if name == "fa_bwd_varlen":
+        assert call(fa, name, total_k=0, k=0, v=0, dk=0, dv=0) == 6
     if "window_left" in CALLS[name]:
         assert call(fa, name, window_left=2**31 - 1, window_right=-2**31) == 6
 
