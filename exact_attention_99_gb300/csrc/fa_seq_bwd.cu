@@ -812,7 +812,7 @@ template <int D>
 cudaError_t launch_t(const SeqProblem& pb, const void* o, const float* lse, const void* dout, void* dq, void* dk,
                      void* dv, cudaStream_t stream) {
   using C = Cfg<D>;
-  const int G = num_sms();
+  const int G = std::min(num_sms(), seq::kMaxWorkers);
   const int group = pb.Hq / pb.Hkv, tok = 128 / group;
   unsigned* status = status_word();
   if (status == nullptr) return cudaErrorLaunchFailure;

@@ -27,13 +27,14 @@
 //     the product reads them, as 0 * NaN would stay NaN.
 //
 //   CTA = 512 threads, persistent (one per SM):
-//     warps 0-3 / 4-7  softmax of stage 0 / 1   (one thread per row)
-//     warps 8-11       correction + epilogue
-//     warp 12 TMA producer, warp 13 MMA issuer, warp 14 V tail, 15 idle
+//     warps 0-3 / 4-7  softmax of stage 0 / 1 (a thread per row)
+//     warps 8-11       correction (O rescaled when a row's maximum grows) and epilogue
+//     warp 12 TMA producer, 13 MMA issuer, 14 V tail, 15 work items
 //   TMEM as in the dense forward: S/P of the stages at columns 0 and 128, O
 //   at 256 and 256 + d.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/fa.h"
@@ -64,6 +65,7 @@ struct Params {
   float2* part_ml;     // [2 G][2 * 128] their (m, l)
   const int* table;    // paged: [B, max_pages]
   int Hq, group, tok, total_q;
+  int o_box;           // tokens of a warp's 32 rows, if they are whole tokens (tmO's boxes), else 0
   int num_pages, page_size, box_rows, max_pages;
   float scale_log2;    // |scale| * log2(e)
   uint32_t neg_s;      // 1 for a negative scale
@@ -71,23 +73,71 @@ struct Params {
   unsigned long long wait_limit_ns;
   int inject;
   unsigned* status;
+  unsigned long long* trace;  // optional pipeline trace
 };
+
+// Trace points (fa_trace); a step is the CTA's running key-tile counter (in
+// key mode two tiles, one of each stage):
+//   MMA         0 tiles loaded, 1+s PV of stage s issued, 3 the next S of both issued
+//   softmax s   4+3s S ready, 5+3s alpha published, 6+3s P stored
+//   correction  10+s O released for PV
+//   epilogue s  12+s O written (step of the item's last tile)
+constexpr int kItems = 4;  // ring of work items
 
 template <int D>
 struct Tiles {
   static constexpr int kChunks = D / 64;
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kSlots = D == 128 ? 4 : 8;
-  static constexpr int kStgBytes = 16384;  // 4 warps x [32 rows x 64 columns] bf16
+  static constexpr int kStgBytes = 16384;  // O staging: 4 warps x [32 rows x 64 columns] bf16
   static constexpr int kSmemDyn = (2 + kSlots) * kTileBytes + kStgBytes + 1024;
 };
 constexpr int kMaxSlots = 8;
 
+// mbar_wait_bounded in less code: there are some fifty waits in the kernel,
+// and its roles share the instruction cache.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                             uint64_t limit_ns) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(addr, parity); ++n) {
+    if ((n & 31) != 0) continue;
+    if (*abort_flag) return false;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) {
+      t0 = t;
+    } else if (t - t0 > limit_ns) {
+      *abort_flag = 1u;
+      return false;
+    }
+  }
+  return true;
+}
+// bits of the MMA issuer's phases: Q loaded, P stored (a pair each)
+constexpr int kPhQ = 0, kPhP = 2;
+
+// An item as the roles see it, laid out by warp 15. Its key tile t is taken by
+//   key mode: stage t & 1, as its step t >> 1;
+//   else    : both stages, stage s while a[s] <= t < a[s] + n[s].
+struct Work {
+  int q0, ntok, kvh, kbase, klen, pos, kt, nt;
+  int n[2], a[2];
+  int rows[2];  // rows of each stage (key mode: both have the same)
+  int flags;    // kKeyMode | kPart | kCont; -1: there are no more items
+  int fill;     // keys of the last tile if the sequence ends inside it, else 0
+};
+
 struct __align__(8) Ctl {
-  uint64_t q_full[2], q_empty;
+  Work it[kItems];
+  uint64_t it_full[kItems], it_empty[kItems];
+  uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
-  uint64_t s_full[2], p_full[2], alpha_full[2], o_ready[2], o_full[2], stats_full[2], stats_empty[2];
-  uint64_t seen[kMaxSlots];  // the tail warp is done with the slot's tile (its rows past the sequence's end are zeroed)
+  // a V tile that the sequence ends in: loaded into the slot (being loaded), its rows past the end zeroed
+  uint64_t tail_req[kMaxSlots], tail_done[kMaxSlots];
+  // p_full: P stored (4 softmax warps) and O corrected, or read by the epilogue
+  // of the stage's item before (4 correction warps)
+  uint64_t s_full[2], p_full[2], alpha_full[2], o_full[2];
+  uint64_t stats_full[2], stats_empty[2];
   uint64_t drain;
   float alpha[2][128];
   float stat_l[2][128];
@@ -96,58 +146,47 @@ struct __align__(8) Ctl {
   uint32_t abort;
 };
 
-// An item as the roles see it: key tile t of the item is taken by
-//   key mode: stage t & 1, as its step t >> 1;
-//   else    : both stages, stage s while a[s] <= t < a[s] + n[s].
-struct Work {
-  FwdItem it;
-  int n[2], a[2];
-  int rows[2];  // rows of each stage (key mode: both have the same)
-  bool key;
-};
-
-// the next item of this CTA, false when there is none
-__device__ __forceinline__ bool walk_next(const Params& p, Walk& w, Work& x) {
-  if (w.i > w.last) return false;
-  const int4* src = reinterpret_cast<const int4*>(p.items + w.i);
-  const int4 u = src[0], v = src[1];
-  x.it.q0 = u.x;
-  x.it.count = u.y;
-  x.it.kvh = u.z;
-  x.it.kbase = u.w;
-  x.it.klen = v.x;
-  x.it.pos = v.y;
-  x.it.kt = v.z;
-  x.it.nt = v.w;
-  walk_step(w);
-  x.key = (x.it.count & kKeyMode) != 0;
-  const int ntok = x.it.ntok(), nt = x.it.nt;
-  if (x.key) {
-    x.rows[0] = x.rows[1] = ntok * p.group;
-    x.n[0] = (nt + 1) >> 1;
-    x.n[1] = nt >> 1;
+// The laid-out form of the item at `src`.
+__device__ __forceinline__ Work work_of(const Params& p, const FwdItem* src) {
+  const int4 u = reinterpret_cast<const int4*>(src)[0], v = reinterpret_cast<const int4*>(src)[1];
+  Work x;
+  x.q0 = u.x;
+  x.ntok = u.y & 0xffff;
+  x.flags = u.y & ~0xffff;
+  x.kvh = u.z;
+  x.kbase = u.w;
+  x.klen = v.x;
+  x.pos = v.y;
+  x.kt = v.z;
+  x.nt = v.w;
+  const int end = x.klen & 127;
+  x.fill = x.nt > 0 && x.kt + x.nt - 1 == (x.klen - 1) >> 7 ? end : 0;
+  if (x.flags & kKeyMode) {
+    x.rows[0] = x.rows[1] = x.ntok * p.group;
+    x.n[0] = (x.nt + 1) >> 1;
+    x.n[1] = x.nt >> 1;
     x.a[0] = x.a[1] = 0;
   } else {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int mine = s == 0 ? p.tok : ntok - p.tok;
+      const int mine = s == 0 ? p.tok : x.ntok - p.tok;
       x.rows[s] = mine * p.group;
-      const int pos = x.it.pos + s * p.tok;
+      const int pos = x.pos + s * p.tok;
       const int lo = p.wl >= 0 ? max(0, pos - p.wl) : 0;
-      const int hi = p.wr >= 0 ? min(x.it.klen - 1, pos + mine - 1 + p.wr) : x.it.klen - 1;
+      const int hi = p.wr >= 0 ? min(x.klen - 1, pos + mine - 1 + p.wr) : x.klen - 1;
       // this stage's tiles within the item's
-      const int t0 = max(lo >> 7, x.it.kt), t1 = min(hi >> 7, x.it.kt + nt - 1);
+      const int t0 = max(lo >> 7, x.kt), t1 = min(hi >> 7, x.kt + x.nt - 1);
       x.n[s] = hi < lo || t1 < t0 ? 0 : t1 - t0 + 1;
-      x.a[s] = x.n[s] > 0 ? t0 - x.it.kt : 0;
+      x.a[s] = x.n[s] > 0 ? t0 - x.kt : 0;
     }
   }
-  return true;
+  return x;
 }
 
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const Params p) {
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const Params p) {
   using C = Tiles<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
@@ -161,22 +200,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     ctl.abort = 0;
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&ctl.it_full[i], 1);
+      mbar_init(&ctl.it_empty[i], 15);  // every warp but this one's
+    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.q_full[s], 1);
+      mbar_init(&ctl.q_empty[s], 1);
       mbar_init(&ctl.s_full[s], 1);
-      mbar_init(&ctl.p_full[s], 4);
+      mbar_init(&ctl.p_full[s], 8);
       mbar_init(&ctl.alpha_full[s], 4);
-      mbar_init(&ctl.o_ready[s], 4);
       mbar_init(&ctl.o_full[s], 1);
       mbar_init(&ctl.stats_full[s], 4);
       mbar_init(&ctl.stats_empty[s], 4);
     }
-    mbar_init(&ctl.q_empty, 1);
     mbar_init(&ctl.drain, 1);
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&ctl.kv_full[i], 1);
-      mbar_init(&ctl.seen[i], 1);
-      mbar_init(&ctl.kv_empty[i], 2);  // the products that read it, and the tail warp
+      mbar_init(&ctl.kv_empty[i], 1);
+      mbar_init(&ctl.tail_req[i], 1);
+      mbar_init(&ctl.tail_done[i], 1);
     }
     fence_mbar_init();
   }
@@ -195,112 +238,133 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();    // the plan
   grid_dep_launch();  // the joining kernel may start (and wait) meanwhile
   const uint32_t tmem = ctl.tmem_base;
-  Walk wk = walk_begin(p.head, p.first, p.last);
-  Work x;
+  // item i of this CTA, or null when there is none (or a wait ran out)
+  auto item = [&](int i) -> const Work* {
+    if (!wait_bounded(&ctl.it_full[i % kItems], (i / kItems) & 1, abort_flag, LIM)) return nullptr;
+    const Work* x = &ctl.it[i % kItems];
+    return x->flags < 0 ? nullptr : x;
+  };
+  auto release = [&](int i) { mbar_arrive(&ctl.it_empty[i % kItems]); };  // by one lane of each warp
 
   if (wg <= 1) {
     // ------------------------------------------------------------ softmax
     setmaxnreg_inc<176>();
-    const int s = wg;
-    const int row = ((warp & 3) << 5) + lane;
-    const uint32_t t_s = tmem + (uint32_t(warp & 3) << 21) + uint32_t(s * 128);
+    const int s = wg, wq = warp & 3;
+    const int row = (wq << 5) + lane;
+    const uint32_t t_s = tmem + (uint32_t(wq) << 21) + uint32_t(s * 128);  // lane quarter + S columns
     const float sl = p.scale_log2;
     const int row_tok = row / p.group;
-    uint32_t ph_s = 0, ph_se = 0;
+    uint32_t ph_s = 0, ph_st = 0;
+    int step0 = 0;  // running key-tile counter (trace only)
     bool ok = true;
-    while (ok && walk_next(p, wk, x)) {
-      const int n = x.n[s];
-      if (n == 0) continue;
-      const bool mine = ((warp & 3) << 5) < x.rows[s];  // the warp has rows
-      const int stage_pos = x.it.pos + (x.key ? 0 : s * p.tok);
-      const int pos = stage_pos + row_tok;  // this row's place among the keys
-      const int pos_l = stage_pos + (x.key ? x.it.ntok() : s == 0 ? p.tok : x.it.ntok() - p.tok) - 1;  // the last row's
-      const int kt0 = x.it.kt + (x.key ? s : x.a[s]), dkt = x.key ? 2 : 1;
-      const int klen = x.it.klen;
+    for (int i = 0; ok; ++i) {
+      const Work* const w = item(i);
+      if (w == nullptr) break;
+      const bool key = (w->flags & kKeyMode) != 0;
+      const int step = step0 + w->a[s];
+      step0 += key ? w->n[0] : w->nt;
+      const int n = w->n[s];
+      const bool mine = (wq << 5) < w->rows[s];  // the warp has rows
       float m_run = -INFINITY, l_run = 0.0f;
-      for (int j = 0; j < n; ++j) {
-        if (!mbar_wait_bounded(&ctl.s_full[s], ph_s, abort_flag, LIM)) { ok = false; break; }
-        ph_s ^= 1;
-        if (!mine) {
-          if (lane == 0) {
-            mbar_arrive(&ctl.alpha_full[s]);
-            mbar_arrive(&ctl.p_full[s]);
+      if (n > 0) {
+        const int stage_pos = w->pos + (key ? 0 : s * p.tok);
+        const int pos = stage_pos + row_tok;  // this row's place among the keys
+        const int pos_l = stage_pos + (key ? w->ntok : s == 0 ? p.tok : w->ntok - p.tok) - 1;  // the last row's
+        const int klen = w->klen;
+        const int dkb = key ? 256 : 128;
+        int kb = (w->kt + (key ? s : w->a[s])) * 128;  // the tile's first key
+        for (int j = 0; j < n; ++j, kb += dkb) {
+          if (!wait_bounded(&ctl.s_full[s], ph_s, abort_flag, LIM)) { ok = false; break; }
+          ph_s ^= 1;
+          if (row == 0) trace_stamp(p.trace, step + j, 4 + 3 * s);
+          if (!mine) {
+            if (lane == 0) {
+              if (j > 0) mbar_arrive(&ctl.alpha_full[s]);
+              mbar_arrive(&ctl.p_full[s]);
+            }
+            continue;
           }
-          continue;
+          tc_fence_after();
+          uint32_t v[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+          tmem_wait_ld();
+          // masked where the tile reaches past the keys or crosses a bound of some row
+          if (kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl)) {
+            int hi = klen - kb;  // columns [lo, hi) are visible
+            int lo = 0;
+            if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
+            if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
+            const uint32_t span = uint32_t(max(hi - lo, 0));
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+          }
+          float mA = -INFINITY, mB = -INFINITY, mC = -INFINITY, mD = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            mA = fmax3(mA, u2f(v[c]), u2f(v[c + 1]));
+            mB = fmax3(mB, u2f(v[c + 2]), u2f(v[c + 3]));
+            mC = fmax3(mC, u2f(v[c + 4]), u2f(v[c + 5]));
+            mD = fmax3(mD, u2f(v[c + 6]), u2f(v[c + 7]));
+          }
+          const float mx = fmaxf(fmaxf(mA, mB), fmaxf(mC, mD));
+          const float m_cand = fmaxf(m_run, mx * sl);
+          const float m_new = (m_cand > m_run + kTau) ? m_cand : m_run;
+          const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
+          const float alpha = ex2_mufu(m_run - m_use);
+          if (j > 0) {  // (there is no O to correct before the first)
+            ctl.alpha[s][row] = alpha;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
+          }
+          if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
+          const uint64_t sl2 = pack2(sl, sl);
+          const uint64_t nm2 = pack2(-m_use, -m_use);
+          uint64_t acc0 = 0, acc1 = 0, acc2 = 0, acc3 = 0;
+          uint32_t pk[64];
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const uint64_t y = ffma2(pack2(u2f(v[2 * c]), u2f(v[2 * c + 1])), sl2, nm2);
+            float a, b;
+            unpack2(y, a, b);
+            a = ex2_mufu(a);
+            b = ex2_mufu(b);
+            const uint64_t pr = pack2(a, b);
+            if ((c & 3) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
+            if ((c & 3) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
+            if ((c & 3) == 2) acc2 = c == 2 ? pr : fadd2(acc2, pr);
+            if ((c & 3) == 3) acc3 = c == 3 ? pr : fadd2(acc3, pr);
+            // P to bf16 (nearest even), the type that the P V product takes
+            // beside a bf16 V: off by at most 2^-8 of each probability; the row
+            // sum keeps the 32-bit values
+            pk[c] = pack_bf16x2(a, b);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[c * 16]));
+          const uint64_t acc = fadd2(fadd2(acc0, acc1), fadd2(acc2, acc3));
+          float la, lb;
+          unpack2(acc, la, lb);
+          l_run = fmaf(l_run, alpha, la + lb);
+          m_run = m_new;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
+          if (lane == 0) mbar_arrive(&ctl.p_full[s]);
         }
-        tc_fence_after();
-        uint32_t v[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
-        tmem_wait_ld();
-        const int kb = (kt0 + j * dkt) * 128;
-        // masked where the tile reaches past the keys or crosses a bound of some row
-        if (kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl)) {
-          int hi = klen - kb;  // columns [lo, hi) are visible
-          int lo = 0;
-          if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
-          if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
-          const uint32_t span = uint32_t(max(hi - lo, 0));
-#pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
-        }
-        float mA = -INFINITY, mB = -INFINITY, mC = -INFINITY, mD = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 128; c += 8) {
-          mA = fmax3(mA, u2f(v[c]), u2f(v[c + 1]));
-          mB = fmax3(mB, u2f(v[c + 2]), u2f(v[c + 3]));
-          mC = fmax3(mC, u2f(v[c + 4]), u2f(v[c + 5]));
-          mD = fmax3(mD, u2f(v[c + 6]), u2f(v[c + 7]));
-        }
-        const float mx = fmaxf(fmaxf(mA, mB), fmaxf(mC, mD));
-        const float m_cand = fmaxf(m_run, mx * sl);
-        const float m_new = (m_cand > m_run + kTau) ? m_cand : m_run;
-        const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
-        const float alpha = ex2_mufu(m_run - m_use);
-        ctl.alpha[s][row] = alpha;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
-        const uint64_t sl2 = pack2(sl, sl);
-        const uint64_t nm2 = pack2(-m_use, -m_use);
-        uint64_t acc0 = 0, acc1 = 0, acc2 = 0, acc3 = 0;
-        uint32_t pk[64];
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const uint64_t y = ffma2(pack2(u2f(v[2 * c]), u2f(v[2 * c + 1])), sl2, nm2);
-          float a, b;
-          unpack2(y, a, b);
-          a = ex2_mufu(a);
-          b = ex2_mufu(b);
-          const uint64_t pr = pack2(a, b);
-          if ((c & 3) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
-          if ((c & 3) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
-          if ((c & 3) == 2) acc2 = c == 2 ? pr : fadd2(acc2, pr);
-          if ((c & 3) == 3) acc3 = c == 3 ? pr : fadd2(acc3, pr);
-          // P to bf16 (nearest even), the type the P V product takes beside a
-          // bf16 V: off by at most 2^-9 of each probability's binade top; the row sum
-          // keeps the 32-bit values
-          pk[c] = pack_bf16x2(a, b);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[c * 16]));
-        const uint64_t acc = fadd2(fadd2(acc0, acc1), fadd2(acc2, acc3));
-        float la, lb;
-        unpack2(acc, la, lb);
-        l_run = fmaf(l_run, alpha, la + lb);
-        m_run = m_new;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full[s]);
+        if (!ok) break;
       }
-      if (!ok) break;
-      if (!mbar_wait_bounded(&ctl.stats_empty[s], ph_se ^ 1, abort_flag, LIM)) { ok = false; break; }
-      ph_se ^= 1;
-      ctl.stat_l[s][row] = l_run;
-      ctl.stat_m[s][row] = m_run;
+      if (n > 0) {  // the rows' statistics for the epilogue
+        if (!wait_bounded(&ctl.stats_empty[s], ph_st ^ 1, abort_flag, LIM)) { ok = false; break; }
+        ph_st ^= 1;
+        ctl.stat_l[s][row] = l_run;
+        ctl.stat_m[s][row] = m_run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.stats_full[s]);
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.stats_full[s]);
+      if (lane == 0) release(i);
     }
   } else if (wg == 2) {
     // ------------------------------------------------ correction + epilogue
@@ -308,18 +372,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int wq = warp & 3;
     const int row = (wq << 5) + lane;
     const uint32_t t_lane = tmem + (uint32_t(wq) << 21) + kOCol0;
+    uint8_t* stg = sStg + wq * 4096;
     const int row_tok = row / p.group, row_head = row - row_tok * p.group;
-    uint32_t ph_a[2] = {0, 0}, ph_st[2] = {0, 0}, ph_of[2] = {0, 0};
+    uint32_t ph_a = 0, ph_st = 0, ph_of = 0;  // phases, a bit to each stage
+    if (lane == 0) {  // O of both stages may be written
+      mbar_arrive(&ctl.p_full[0]);
+      mbar_arrive(&ctl.p_full[1]);
+    }
+    int step0 = 0;
     bool ok = true;
-    while (ok && walk_next(p, wk, x)) {
-      const int steps = x.key ? x.n[0] : x.it.nt;
+    for (int i = 0; ok; ++i) {
+      const Work* const w = item(i);
+      if (w == nullptr) break;
+      const bool key = (w->flags & kKeyMode) != 0;
+      const int steps = key ? w->n[0] : w->nt;
+      const int n0 = w->n[0], n1 = w->n[1], a0 = w->a[0], a1 = w->a[1];
+      const bool mine0 = (wq << 5) < w->rows[0], mine1 = (wq << 5) < w->rows[1];  // the warp has rows
       for (int j = 0; j < steps && ok; ++j) {
-#pragma unroll
+#pragma unroll 1
         for (int s = 0; s < 2; ++s) {
-          if (j < x.a[s] || j >= x.a[s] + x.n[s]) continue;
-          if (!mbar_wait_bounded(&ctl.alpha_full[s], ph_a[s], abort_flag, LIM)) { ok = false; break; }
-          ph_a[s] ^= 1;
-          if ((wq << 5) < x.rows[s] && j > x.a[s]) {
+          const int as = s == 0 ? a0 : a1, es = s == 0 ? a0 + n0 : a1 + n1;
+          if (j <= as || j >= es) continue;  // (a stage's first product overwrites O)
+          if (!wait_bounded(&ctl.alpha_full[s], (ph_a >> s) & 1, abort_flag, LIM)) { ok = false; break; }
+          ph_a ^= 1u << s;
+          if (s == 0 ? mine0 : mine1) {
             const float a = ctl.alpha[s][row];
             if (__any_sync(0xffffffffu, a < 1.0f)) {
               tc_fence_after();
@@ -331,11 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(t_o + c * 32, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
+                for (int e = 0; e < 32; e += 2) {
                   float lo, hi;
-                  unpack2(fmul2(pack2(u2f(v[i]), u2f(v[i + 1])), a2), lo, hi);
-                  v[i] = f2u(lo);
-                  v[i + 1] = f2u(hi);
+                  unpack2(fmul2(pack2(u2f(v[e]), u2f(v[e + 1])), a2), lo, hi);
+                  v[e] = f2u(lo);
+                  v[e + 1] = f2u(hi);
                 }
                 tmem_st32(t_o + c * 32, v);
               }
@@ -344,179 +420,249 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.o_ready[s]);
+          if (row == 0) trace_stamp(p.trace, step0 + j, 10 + s);
+          if (lane == 0) mbar_arrive(&ctl.p_full[s]);
         }
       }
       if (!ok) break;
-      // epilogue
-      const int ntok = x.it.ntok();
-      const bool part = (x.it.count & kPart) != 0;
-      const int slot = 2 * int(blockIdx.x) + ((x.it.count & kCont) ? 0 : 1);
-      // the stages' rows are the same rows in key mode: one pass over both
-      const int passes = x.key || ntok <= p.tok ? 1 : 2;
+      step0 += steps;
+      // Epilogue: each stage's rows in turn, or in key mode, where both have
+      // the same rows, the two joined.
+      const bool part = (w->flags & kPart) != 0;
+      const int q0 = w->q0, kvh = w->kvh;
 #pragma unroll 1
-      for (int s = 0; s < passes && ok; ++s) {
-        const int s1 = x.key ? 1 : s;  // the stages joined by this pass: s and s1
-        const bool valid = row < x.rows[s];
-        // packed (token, head) row of o, and its place in lse; -1 for none
-        const int token = x.it.q0 + s * p.tok + row_tok;
-        const int head = x.it.kvh * p.group + row_head;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if ((t != s && t != s1) || x.n[t] == 0) continue;
-          if (!mbar_wait_bounded(&ctl.stats_full[t], ph_st[t], abort_flag, LIM)) { ok = false; break; }
-          ph_st[t] ^= 1;
-          l[t] = ctl.stat_l[t][row];
-          m[t] = ctl.stat_m[t][row];
+      for (int s = 0; s < 2; ++s) {
+        if (key && s == 1) break;
+        const int n = s == 0 ? n0 : n1, nj = key ? n1 : 0;  // nj > 0: stage 1 is joined
+        const int rows = w->rows[s] - (wq << 5);            // of the tile, from this warp's first on
+        float m = -INFINITY, l = 0.0f, f0 = 1.0f, f1 = 0.0f;
+        if (n > 0) {
+          if (!wait_bounded(&ctl.stats_full[s], (ph_st >> s) & 1, abort_flag, LIM)) { ok = false; break; }
+          ph_st ^= 1u << s;
+          l = ctl.stat_l[s][row];
+          m = ctl.stat_m[s][row];
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.stats_empty[t]);
-          if (!mbar_wait_bounded(&ctl.o_full[t], ph_of[t], abort_flag, LIM)) { ok = false; break; }
-          ph_of[t] ^= 1;
+          if (lane == 0) mbar_arrive(&ctl.stats_empty[s]);
         }
-        if (!ok) break;
-        tc_fence_after();
-        // join: weights of the two stages' O (a stage without tiles has m = -inf, l = 0)
-        const float mj = fmaxf(m[0], m[1]), mu = mj == -INFINITY ? 0.0f : mj;
-        const float w0 = m[0] == -INFINITY ? 0.0f : ex2_mufu(m[0] - mu);
-        const float w1 = m[1] == -INFINITY ? 0.0f : ex2_mufu(m[1] - mu);
-        const float lj = l[0] * w0 + l[1] * w1;
-        const float inv = part ? 1.0f : lj == 0.0f ? 0.0f : 1.0f / lj;
-        const bool has0 = x.n[0] > 0 && s == 0, has1 = x.n[1] > 0 && s1 == 1;
-        const float f0 = w0 * inv, f1 = w1 * inv;
-        if ((wq << 5) < x.rows[s]) {
-          // columns [16 c, 16 c + 16) of the joined O (inv is 1 for a part)
+        if (nj > 0) {
+          if (!wait_bounded(&ctl.stats_full[1], (ph_st >> 1) & 1, abort_flag, LIM)) { ok = false; break; }
+          ph_st ^= 2u;
+          const float l1 = ctl.stat_l[1][row], m1 = ctl.stat_m[1][row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.stats_empty[1]);
+          const float mj = fmaxf(m, m1), mu = mj == -INFINITY ? 0.0f : mj;
+          f0 = ex2_mufu(m - mu);  // (0 for a stage that saw no key)
+          f1 = ex2_mufu(m1 - mu);
+          l = l * f0 + l1 * f1;
+          m = mj;
+        }
+        const float inv = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        f0 *= inv;
+        f1 *= inv;
+        if (n > 0) {
+          if (!wait_bounded(&ctl.o_full[s], (ph_of >> s) & 1, abort_flag, LIM)) { ok = false; break; }
+          ph_of ^= 1u << s;
+          if (nj > 0) {
+            if (!wait_bounded(&ctl.o_full[1], (ph_of >> 1) & 1, abort_flag, LIM)) { ok = false; break; }
+            ph_of ^= 2u;
+          }
+          tc_fence_after();
+        }
+        if (rows > 0) {
+          const bool valid = lane < rows;
+          const int token = q0 + s * p.tok + row_tok, head = kvh * p.group + row_head;
+          // columns [16 c, 16 c + 16) of the (joined) O
           auto columns = [&](int c, float (&f)[16]) {
-            uint32_t v[16], u[16];
-            if (has0) tmem_ld16(t_lane + c * 16, v);
-            if (has1) tmem_ld16(t_lane + D + c * 16, u);
-            tmem_wait_ld();
+            uint32_t v[16];
+            if (n > 0) {
+              tmem_ld16(t_lane + s * D + c * 16, v);
+              if (nj > 0) {
+                uint32_t u[16];
+                tmem_ld16(t_lane + D + c * 16, u);
+                tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              f[i] = (has0 ? u2f(v[i]) * f0 : 0.0f) + (has1 ? u2f(u[i]) * f1 : 0.0f);
+                for (int e = 0; e < 16; ++e) f[e] = fmaf(u2f(u[e]), f1, u2f(v[e]) * f0);
+              } else {
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) f[e] = u2f(v[e]) * f0;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) f[e] = 0.0f;
+            }
           };
           if (part) {
-            const size_t at = size_t(slot) * 256 + s * 128 + row;
-            if (valid) p.part_ml[at] = make_float2(mj, lj);
-            float* dst = p.part_o + at * D;
+            const size_t at = size_t(2 * int(blockIdx.x) + ((w->flags & kCont) ? 0 : 1)) * 256 + s * 128 + row;
+            if (valid) p.part_ml[at] = make_float2(m, l);
+            float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               float f[16];
               columns(c, f);
               if (valid) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                  *reinterpret_cast<float4*>(dst + c * 16 + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                for (int e = 0; e < 4; ++e) dst[c * 4 + e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
               }
             }
           } else {
-            uint8_t* stg = sStg + wq * 4096;
+            // 32 rows x 64 columns at a time through a staging buffer
+            // (128-byte swizzle): by one TMA store where the warp's rows are
+            // whole tokens of the sequence, else by plain stores of whole rows
+            const bool tma = p.o_box != 0 && rows >= 32;
             const int orow = valid ? token * p.Hq + head : -1;
 #pragma unroll 1
             for (int hf = 0; hf < D / 64; ++hf) {
-              __syncwarp();  // the previous half has been read
+              if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
+              __syncwarp();
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 float f[16];
                 columns(hf * 4 + c, f);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  *reinterpret_cast<uint4*>(stg + lane * 128 + (((c * 2 + i) ^ (lane & 7)) << 4)) =
-                      make_uint4(pack_bf16x2(f[8 * i], f[8 * i + 1]), pack_bf16x2(f[8 * i + 2], f[8 * i + 3]),
-                                 pack_bf16x2(f[8 * i + 4], f[8 * i + 5]), pack_bf16x2(f[8 * i + 6], f[8 * i + 7]));
+                for (int e = 0; e < 2; ++e)
+                  *reinterpret_cast<uint4*>(stg + lane * 128 + (((c * 2 + e) ^ (lane & 7)) << 4)) =
+                      make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
+                                 pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
               }
-              __syncwarp();
-              // 8 lanes write a row's 128 bytes, 4 rows at a time
+              if (tma) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  tma_store_4d(&tmO, stg, hf * 64, 0, q0 + s * p.tok + wq * p.o_box, kvh);
+                  bulk_commit();
+                }
+              } else {
+                __syncwarp();
+                // 8 lanes write a row's 128 bytes, 4 rows at a time
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = i * 4 + (lane >> 3);
-                const int to = __shfl_sync(0xffffffffu, orow, r);
-                const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                if (to >= 0) *reinterpret_cast<uint4*>(p.o + size_t(to) * D + hf * 64 + (lane & 7) * 8) = w;
+                for (int e = 0; e < 8; ++e) {
+                  const int rr = e * 4 + (lane >> 3);
+                  const int to = __shfl_sync(0xffffffffu, orow, rr);
+                  const uint4 x = *reinterpret_cast<const uint4*>(stg + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                  if (to >= 0) *reinterpret_cast<uint4*>(p.o + size_t(to) * D + hf * 64 + (lane & 7) * 8) = x;
+                }
+                __syncwarp();
               }
             }
             if (valid)
-              p.lse[size_t(head) * p.total_q + token] = lj == 0.0f ? -INFINITY : (mu + __log2f(lj)) * 0.69314718055994531f;
+              p.lse[size_t(head) * p.total_q + token] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
           }
         }
-        tc_fence_before();
+        if (n > 0) {  // the next item's products may overwrite O
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl.p_full[s]);
+            if (nj > 0) mbar_arrive(&ctl.p_full[1]);
+          }
+        }
+        if (row == 0) trace_stamp(p.trace, step0 - 1, 12 + s);
       }
+      __syncwarp();
+      if (lane == 0) release(i);
     }
+    if (lane == 0) bulk_wait_all();  // stores complete (and staging reads done) before the CTA exits
   } else {
     setmaxnreg_dec<80>();
   }
   if (warp == 12) {
     // ------------------------------------------------------- TMA producer
-    uint32_t kv_it = 0, ph_qe = 0;
-    bool first = true, ok = true, injected = false;
+    uint32_t kv_it = 0, q_uses[2] = {0, 0}, key_items = 0;
+    bool ok = true, injected = false;
     const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
+    const uint32_t q_bytes = uint32_t(p.tok * p.group * D * 2);
     // paged: lane -> (box of the tile, 64-column chunk)
     const int n_box = PAGED ? 128 / p.box_rows : 1;
     const int box = lane % n_box, chunk = lane / n_box;
-    while (ok && walk_next(p, wk, x)) {
-      const int nt = x.it.nt;
-      if (nt == 0) continue;
-      if (!first) {
-        ok = mbar_wait_bounded(&ctl.q_empty, ph_qe, abort_flag, LIM);
-        ok = __all_sync(0xffffffffu, ok);
+    for (int i = 0; ok; ++i) {
+      const Work* const w = item(i);
+      if (w == nullptr) break;
+      const int nt = w->nt, kvh = w->kvh, kt = w->kt, kbase = w->kbase, klen = w->klen;
+      const bool key = (w->flags & kKeyMode) != 0;
+      // Q: key mode takes the two buffers in turn, else stage s takes buffer s
+      for (int s = 0; s < 2 && ok; ++s) {
+        if (w->n[s] == 0 || (key && s == 1)) continue;
+        const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
+        ok = __all_sync(0xffffffffu, wait_bounded(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1,
+                                                        abort_flag, LIM));
         if (!ok) break;
-        ph_qe ^= 1;
-      }
-      first = false;
-      if (lane == 0) {
-        const uint32_t q_bytes = uint32_t(p.tok * p.group * D * 2);
-        for (int s = 0; s < 2; ++s) {
-          if (x.n[s] == 0 || (s == 1 && x.key)) continue;
-          mbar_arrive_expect_tx(&ctl.q_full[s], q_bytes);
+        if (b == 0) {
+          ++q_uses[0];
+        } else {
+          ++q_uses[1];
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&ctl.q_full[b], q_bytes);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d_hint(sQ + s * C::kTileBytes + c * 16384, &tmQ, &ctl.q_full[s], c * 64, 0, x.it.q0 + s * p.tok,
-                             x.it.kvh, pol_q);
+            tma_load_4d_hint(sQ + b * C::kTileBytes + c * 16384, &tmQ, &ctl.q_full[b], c * 64, 0,
+                             w->q0 + (key ? 0 : s * p.tok), kvh, pol_q);
         }
       }
-      // K runs d tiles ahead of V: K(0..d-1), then V(t), K(t + d)
-      const int d = x.key ? 2 : 1;
-      auto load = [&](const CUtensorMap* m, int t) -> bool {
-        const uint32_t slot = kv_it % C::kSlots;
-        const bool r = __all_sync(0xffffffffu, mbar_wait_bounded(&ctl.kv_empty[slot], ((kv_it / C::kSlots) & 1) ^ 1,
-                                                                  abort_flag, LIM));
-        if (!r) return false;
-        ++kv_it;
-        if (p.inject == 1 && !injected) {  // test hook: never deliver this tile
-          injected = true;
-          return true;
+      // The next item's Q and first K and V tile into L2, a lane to each box:
+      // its loads wait for buffers that this item still uses, and would
+      // then wait for device memory too.
+      if (const Work* const w2 = item(i + 1); w2 != nullptr && w2->nt > 0) {
+        const int c = lane % C::kChunks * 64, what = lane / C::kChunks;
+        if (what < 2) {
+          if (w2->n[what] > 0 && !(what == 1 && (w2->flags & kKeyMode)))
+            tma_prefetch_l2_4d(&tmQ, c, 0, w2->q0 + what * p.tok, w2->kvh);
+        } else if (!PAGED && what < 4) {
+          tma_prefetch_l2_4d(what == 2 ? &tmK : &tmV, c, w2->kvh, w2->kbase + w2->kt * 128, 0);
         }
+      }
+      // K runs d tiles ahead of V: K(0..d-1), then V(t), K(t + d) in turn, then the last V
+      const int d = min(key ? 2 : 1, nt), turns = 2 * (nt - d);
+#pragma unroll 1
+      for (int e = 0; e < 2 * nt; ++e) {
+        const int r = e - d;
+        const bool is_v = r >= 0 && (r >= turns || (r & 1) == 0);
+        const int t = r < 0 ? e : r >= turns ? r - (nt - d) : is_v ? r >> 1 : d + (r >> 1);
+        const CUtensorMap* m = is_v ? &tmV : &tmK;
+        const uint32_t slot = kv_it % C::kSlots;
+        const int key0 = (kt + t) * 128;
         uint8_t* dst = sKV + slot * C::kTileBytes;
-        const int key0 = (x.it.kt + t) * 128;
+        int boxes = 1, page = 0, in_page = 0;
         if constexpr (PAGED) {
-          // boxes that begin before the sequence's end
-          const int boxes = min(n_box, (x.it.klen - key0 + p.box_rows - 1) / p.box_rows);
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(boxes * p.box_rows * D * 2));
-          __syncwarp();
+          // boxes that begin before the sequence's end; the page is looked up
+          // before the wait for the slot
+          boxes = min(n_box, (klen - key0 + p.box_rows - 1) / p.box_rows);
           if (chunk < C::kChunks && box < boxes) {
-            const int key = key0 + box * p.box_rows;
-            const int pg = key / p.page_size;
-            int page = p.table[size_t(x.it.kbase) * p.max_pages + pg];
+            const int k = key0 + box * p.box_rows, pg = k / p.page_size;
+            page = p.table[size_t(kbase) * p.max_pages + pg];
+            in_page = k - pg * p.page_size;
             if (page < 0 || page >= p.num_pages) {  // no such page: its keys read as zeros, and the caller is told
               atomicOr(p.status, kDevBadArg);
               page = p.num_pages;
             }
-            tma_load_4d_hint(dst + chunk * 16384 + box * p.box_rows * 128, m, &ctl.kv_full[slot], chunk * 64, x.it.kvh,
-                             key - pg * p.page_size, page, pol_kv);
           }
+        }
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded(&ctl.kv_empty[slot], ((kv_it / C::kSlots) & 1) ^ 1, abort_flag, LIM));
+        if (!ok) break;
+        ++kv_it;
+        if (p.inject == 1 && !injected) {  // test hook: never deliver this tile
+          injected = true;
+          continue;
+        }
+        if constexpr (PAGED) {
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(boxes * p.box_rows * D * 2));
+          __syncwarp();
+          if (chunk < C::kChunks && box < boxes)
+            tma_load_4d_hint(dst + chunk * 16384 + box * p.box_rows * 128, m, &ctl.kv_full[slot], chunk * 64, kvh, in_page,
+                             page, pol_kv);
         } else if (lane == 0) {
           mbar_arrive_expect_tx(&ctl.kv_full[slot], C::kTileBytes);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d_hint(dst + c * 16384, m, &ctl.kv_full[slot], c * 64, x.it.kvh, x.it.kbase + key0, 0, pol_kv);
+            tma_load_4d_hint(dst + c * 16384, m, &ctl.kv_full[slot], c * 64, kvh, kbase + key0, 0, pol_kv);
         }
-        return true;
-      };
-      for (int t = 0; t < d && t < nt && ok; ++t) ok = load(&tmK, t);
-      for (int t = 0; t < nt && ok; ++t) {
-        ok = load(&tmV, t);
-        if (ok && t + d < nt) ok = load(&tmK, t + d);
+        // (the last entry is the last V)
+        if (e == 2 * nt - 1 && w->fill != 0 && lane == 0) mbar_arrive(&ctl.tail_req[slot]);
       }
+      __syncwarp();
+      if (lane == 0) release(i);
     }
     if (*abort_flag) {
       // let copies already in flight land before shared memory is released
@@ -530,116 +676,131 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idPV = idesc_bf16_f32(128, D, 0, 1);
       const uint32_t dq = sdesc_lo(smem_u32(sQ), 16), dk = sdesc_lo(smem_u32(sKV), 16),
                      dv = sdesc_lo(smem_u32(sKV), 16384);
-      uint32_t kv_it = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_o[2] = {0, 0};
+      // Phases of the barriers of each stage (or slot), a bit each: arrays
+      // indexed by the stage would be kept in memory.
+      uint32_t phases = 0, tail_phases = 0;
+      uint32_t E = 0, key_items = 0;  // ring entry that follows
       bool ok = true;
-      auto wait_kv = [&](uint32_t& slot) -> bool {
-        slot = kv_it % C::kSlots;
-        const bool r = mbar_wait_bounded(&ctl.kv_full[slot], (kv_it / C::kSlots) & 1, abort_flag, LIM);
-        ++kv_it;
+      auto wait_phase = [&](uint64_t* bar, int bit) -> bool {
+        const bool r = wait_bounded(bar, (phases >> bit) & 1, abort_flag, LIM);
+        phases ^= 1u << bit;
         return r;
       };
-      // S of stage s = Q (tile qt) K^T
-      auto issue_s = [&](int s, int qt, uint32_t kslot) {
-        const uint32_t a0 = sdesc_step(dq, qt * C::kTileBytes), b0 = sdesc_step(dk, kslot * C::kTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ko = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_ss_lo(tmem + uint32_t(s * 128), sdesc_step(a0, ko), sdesc_step(b0, ko), idS, kk > 0);
-        }
-        mma_commit(&ctl.s_full[s]);
+      // the next ring entry, loaded
+      auto wait_kv = [&](uint32_t& slot) -> bool {
+        slot = E % C::kSlots;
+        const uint32_t phase = (E / C::kSlots) & 1;
+        ++E;
+        return wait_bounded(&ctl.kv_full[slot], phase, abort_flag, LIM);
       };
-      // O of stage s (+)= P V
-      auto issue_pv = [&](int s, uint32_t vslot, bool acc) {
-        const uint32_t b0 = sdesc_step(dv, vslot * C::kTileBytes);
+      // rows of a V tile past the sequence's end zeroed
+      auto wait_tail = [&](uint32_t slot) -> bool {
+        const uint32_t phase = (tail_phases >> slot) & 1;
+        tail_phases ^= 1u << slot;
+        return wait_bounded(&ctl.tail_done[slot], phase, abort_flag, LIM);
+      };
+      // O of stage s (+)= P V; S of stage s = Q (buffer b) K^T
+      auto issue_pv = [&](int s, uint32_t slot, bool acc) {
+        tc_fence_after();
+        const uint32_t b0 = sdesc_step(dv, slot * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts_lo(tmem + kOCol0 + uint32_t(s * D), tmem + uint32_t(s * 128) + kk * 8, sdesc_step(b0, kk * 2048), idPV,
                     (acc || kk > 0) ? 1u : 0u);
       };
-      auto wait_po = [&](int s) -> bool {
-        if (!mbar_wait_bounded(&ctl.p_full[s], ph_p[s], abort_flag, LIM)) return false;
-        ph_p[s] ^= 1;
-        if (!mbar_wait_bounded(&ctl.o_ready[s], ph_o[s], abort_flag, LIM)) return false;
-        ph_o[s] ^= 1;
+      auto issue_s = [&](int s, uint32_t b, uint32_t slot) {
         tc_fence_after();
-        return true;
+        const uint32_t q0 = sdesc_step(dq, b * C::kTileBytes), b0 = sdesc_step(dk, slot * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t ko = (kk >> 2) * 16384 + (kk & 3) * 32;
+          mma_ss_lo(tmem + uint32_t(s * 128), sdesc_step(q0, ko), sdesc_step(b0, ko), idS, kk > 0);
+        }
+        mma_commit(&ctl.s_full[s]);
       };
-      while (ok && walk_next(p, wk, x)) {
-        const int nt = x.it.nt;
-        if (nt == 0) continue;
-        // the sequence's last key tile, if partly filled, has V rows to be zeroed first
-        const bool tail = (x.it.klen & 127) != 0 && x.it.kt + nt - 1 == (x.it.klen - 1) >> 7;
-        uint32_t kslot = 0, vslot = 0, v_phase = 0;
-        auto wait_v = [&](int t) -> bool {
-          v_phase = (kv_it / C::kSlots) & 1;
-          if (!wait_kv(vslot)) return false;
-          if (!tail || t != nt - 1) return true;
-          // (every tile passes the tail warp, so this slot's count of phases is the ring's)
-          return mbar_wait_bounded(&ctl.seen[vslot], v_phase, abort_flag, LIM);
-        };
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (x.n[s] == 0 || (s == 1 && x.key)) continue;
-          ok = mbar_wait_bounded(&ctl.q_full[s], ph_q[s], abort_flag, LIM);
-          ph_q[s] ^= 1;
-        }
-        if (!ok) break;
-        if (x.key) {
-          for (int t = 0; t < 2 && t < nt && ok; ++t) {
-            ok = wait_kv(kslot);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(t, 0, kslot);
-            mma_commit(&ctl.kv_empty[kslot]);
-          }
-          if (nt <= 2) mma_commit(&ctl.q_empty);
-          for (int t = 0; t < nt && ok; ++t) {
+      // Both loops begin one step (key mode: two tiles) before the item, with
+      // its first S alone: one copy of each product's instructions, since
+      // code that runs once per item is not in the instruction cache (a
+      // prologue and a general step at the items' ends cost some 5 us each).
+      int step0 = 0;
+      for (int i = 0; ok; ++i) {
+        const Work* const w = item(i);
+        if (w == nullptr) break;
+        const int nt = w->nt;
+        const bool fill = w->fill != 0;
+        if (nt > 0 && (w->flags & kKeyMode)) {
+          const uint32_t b = key_items++ & 1;
+          ok = wait_phase(&ctl.q_full[b], kPhQ + int(b));
+          for (int t = -2; t < nt && ok; ++t) {  // V(t) and K(t + 2), of stage t & 1
             const int s = t & 1;
-            ok = wait_v(t) && wait_po(s);
-            if (!ok) break;
-            issue_pv(s, vslot, t > 1);
-            if (t + 2 >= nt) mma_commit(&ctl.o_full[s]);
-            mma_commit(&ctl.kv_empty[vslot]);
+            uint32_t slot;
+            if (t >= 0) {
+              ok = wait_kv(slot) && (!fill || t < nt - 1 || wait_tail(slot)) && wait_phase(&ctl.p_full[s], kPhP + s);
+              if (!ok) break;
+              if (s == 0) trace_stamp(p.trace, step0 + (t >> 1), 0);
+              issue_pv(s, slot, t > 1);
+              if (t + 2 >= nt) mma_commit(&ctl.o_full[s]);
+              mma_commit(&ctl.kv_empty[slot]);
+            }
             if (t + 2 < nt) {
-              ok = wait_kv(kslot);
+              ok = wait_kv(slot);
               if (!ok) break;
-              tc_fence_after();
-              issue_s(s, 0, kslot);
-              mma_commit(&ctl.kv_empty[kslot]);
-              if (t + 3 == nt) mma_commit(&ctl.q_empty);
+              issue_s(s, b, slot);
+              mma_commit(&ctl.kv_empty[slot]);
+              if (t + 3 == nt) mma_commit(&ctl.q_empty[b]);
             }
           }
-          continue;
-        }
-        auto active = [&](int s, int t) { return t >= x.a[s] && t < x.a[s] + x.n[s]; };
-        ok = wait_kv(kslot);
-        if (!ok) break;
-        tc_fence_after();
-        for (int s = 0; s < 2; ++s)
-          if (active(s, 0)) issue_s(s, s, kslot);
-        mma_commit(&ctl.kv_empty[kslot]);
-        if (nt == 1) mma_commit(&ctl.q_empty);
-        for (int t = 0; t < nt && ok; ++t) {
-          const bool nxt = t + 1 < nt;
-          ok = wait_v(t) && (!nxt || wait_kv(kslot));
-          if (!ok) break;
-          const int last_v = active(1, t) ? 1 : 0;  // the last stage that reads V(t)
-          for (int s = 0; s < 2; ++s) {
-            if (active(s, t)) {
-              ok = wait_po(s);
+          step0 += (nt + 1) >> 1;
+        } else if (nt > 0) {
+          const int n0 = w->n[0], n1 = w->n[1], a0 = w->a[0], a1 = w->a[1];
+          for (int s = 0; s < 2 && ok; ++s)
+            if ((s == 0 ? n0 : n1) > 0) ok = wait_phase(&ctl.q_full[s], kPhQ + s);
+          for (int t = -1; t < nt && ok; ++t) {  // V(t) and K(t + 1), of both stages
+            const bool v = t >= 0, k = t + 1 < nt;
+            // tile t (or t + 1) among a stage's: below n unsigned
+            const uint32_t u0 = uint32_t(t - a0), u1 = uint32_t(t - a1);
+            uint32_t vs = 0, ks = 0;
+            if (v) {
+              ok = wait_kv(vs) && (!fill || k || wait_tail(vs));
               if (!ok) break;
-              issue_pv(s, vslot, t > x.a[s]);
-              if (t == x.a[s] + x.n[s] - 1) mma_commit(&ctl.o_full[s]);
-              if (s == last_v) mma_commit(&ctl.kv_empty[vslot]);
+              trace_stamp(p.trace, step0 + t, 0);
+              if (u0 < uint32_t(n0)) {
+                ok = wait_phase(&ctl.p_full[0], kPhP);
+                if (!ok) break;
+                issue_pv(0, vs, u0 > 0);
+                trace_stamp(p.trace, step0 + t, 1);
+                if (u0 + 1 == uint32_t(n0)) mma_commit(&ctl.o_full[0]);
+                if (u1 >= uint32_t(n1)) mma_commit(&ctl.kv_empty[vs]);
+              }
             }
-            if (nxt && active(s, t + 1)) {
-              tc_fence_after();
-              issue_s(s, s, kslot);
+            if (k) {
+              ok = wait_kv(ks);
+              if (!ok) break;
+              if (u0 + 1 < uint32_t(n0)) {
+                issue_s(0, 0, ks);
+                if (u0 + 2 == uint32_t(n0)) mma_commit(&ctl.q_empty[0]);
+              }
             }
+            if (v && u1 < uint32_t(n1)) {
+              ok = wait_phase(&ctl.p_full[1], kPhP + 1);
+              if (!ok) break;
+              issue_pv(1, vs, u1 > 0);
+              trace_stamp(p.trace, step0 + t, 2);
+              if (u1 + 1 == uint32_t(n1)) mma_commit(&ctl.o_full[1]);
+              mma_commit(&ctl.kv_empty[vs]);
+            }
+            if (k) {
+              if (u1 + 1 < uint32_t(n1)) {
+                issue_s(1, 1, ks);
+                if (u1 + 2 == uint32_t(n1)) mma_commit(&ctl.q_empty[1]);
+              }
+              mma_commit(&ctl.kv_empty[ks]);
+            }
+            if (v) trace_stamp(p.trace, step0 + t, 3);
           }
-          if (!ok) break;
-          if (nxt) mma_commit(&ctl.kv_empty[kslot]);
-          if (t + 2 == nt) mma_commit(&ctl.q_empty);
+          step0 += nt;
         }
+        if (ok) release(i);
       }
       if (*abort_flag) {
         // drain the tensor pipe before TMEM is released
@@ -651,32 +812,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 14) {
     // ---------------------------------------------------------- V tail rows
-    // (follows every ring slot, so that it cannot lose count of their phases)
-    uint32_t kv_it = 0;
+    uint32_t kv_it = 0, req_phases = 0;
     bool ok = true;
-    while (ok && walk_next(p, wk, x)) {
-      const int nt = x.it.nt;
-      const int fill = x.it.klen & 127;
-      const bool tail = fill != 0 && x.it.kt + nt - 1 == (x.it.klen - 1) >> 7;
-      for (int e = 0; e < 2 * nt; ++e, ++kv_it) {
-        const uint32_t slot = kv_it % C::kSlots;
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&ctl.kv_full[slot], (kv_it / C::kSlots) & 1, abort_flag, LIM));
+    for (int i = 0; ok; ++i) {
+      const Work* const w = item(i);
+      if (w == nullptr) break;
+      const int fill = w->fill;
+      kv_it += 2 * w->nt;
+      if (fill != 0) {
+        // An item's last ring entry is its last V tile. The slot holds no
+        // other tile from the request until the products have read this one.
+        const uint32_t e = kv_it - 1, slot = e % C::kSlots;
+        ok = wait_bounded(&ctl.tail_req[slot], (req_phases >> slot) & 1, abort_flag, LIM) &&
+             wait_bounded(&ctl.kv_full[slot], (e / C::kSlots) & 1, abort_flag, LIM);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (tail && e == 2 * nt - 1) {  // an item's last ring entry is its last V tile
-          uint8_t* dst = sKV + slot * C::kTileBytes;
-          // a row is 128 bytes of each chunk (the swizzle stays within it)
-          for (int i = fill * 8 + lane; i < 128 * 8; i += 32)
+        req_phases ^= 1u << slot;
+        uint8_t* dst = sKV + slot * C::kTileBytes;
+        // a row is 128 bytes of each chunk (the swizzle stays within it)
+        for (int k = fill * 8 + lane; k < 128 * 8; k += 32)
 #pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-              *reinterpret_cast<uint4*>(dst + c * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-        }
+          for (int c = 0; c < C::kChunks; ++c)
+            *reinterpret_cast<uint4*>(dst + c * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl.seen[slot]);
-          mbar_arrive(&ctl.kv_empty[slot]);
+        if (lane == 0) mbar_arrive(&ctl.tail_done[slot]);
+      }
+      __syncwarp();
+      if (lane == 0) release(i);
+    }
+  } else if (warp == 15) {
+    // --------------------------------------------------------- work items
+    if (lane == 0) {
+      Walk wk = walk_begin(p.head, p.first, p.last);
+      for (int i = 0;; ++i) {
+        const bool more = wk.i <= wk.last;
+        Work x;
+        x.flags = -1;
+        if (more) {
+          x = work_of(p, p.items + wk.i);
+          walk_step(wk);
         }
+        if (!wait_bounded(&ctl.it_empty[i % kItems], ((i / kItems) & 1) ^ 1, abort_flag, LIM)) break;
+        ctl.it[i % kItems] = x;
+        mbar_arrive(&ctl.it_full[i % kItems]);
+        if (!more) break;
       }
     }
   }
@@ -691,8 +871,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The parts of the rows whose keys were divided between workers, joined in
-// the workers' order: O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
-// Block (c, y): cut c, every gridDim.y-th group of rows; a warp per row.
+// the workers' order: O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i. Block
+// (c, y): cut c, every gridDim.y-th group of rows; a warp per row. The
+// lanes read the parts' (m, l) first, so that the reads of O are independent.
 template <int D>
 __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
   grid_dep_wait();
@@ -700,32 +881,49 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
   const Cut k = p.cuts[blockIdx.x];
   if (k.c1 < 0) return;
   const int lane = threadIdx.x & 31;
-  const int ntok = k.count, rows = ntok * p.group;
-  const int per_stage = p.tok * p.group;
+  const int rows = k.count * p.group, per_stage = p.tok * p.group;
   constexpr int V = D / 32;  // columns per lane
   for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
     const int s = r >= per_stage ? 1 : 0;
     const size_t at = size_t(s) * 128 + (r - s * per_stage);
     float m = -INFINITY, l = 0.0f, o[V] = {};
-    for (int c = k.c0; c <= k.c1; ++c) {
-      if (p.last[c] < 0) continue;  // a worker without a share (fewer key tiles than workers)
-      const size_t i = size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * 256 + at;
-      const float2 ml = p.part_ml[i];
-      if (ml.y == 0.0f) continue;  // no key of this part is visible to the row: its O was not written
-      const float mn = fmaxf(m, ml.x);
-      const float wa = m == -INFINITY ? 0.0f : ex2_mufu(m - mn), wb = ex2_mufu(ml.x - mn);
-      float f[V];
-      if constexpr (V == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(p.part_o + i * D + lane * V);
-        f[0] = t.x; f[1] = t.y; f[2] = t.z; f[3] = t.w;
-      } else {
-        const float2 t = *reinterpret_cast<const float2*>(p.part_o + i * D + lane * V);
-        f[0] = t.x; f[1] = t.y;
-      }
+    for (int c0 = k.c0; c0 <= k.c1; c0 += 32) {  // 32 parts at a time
+      const int c = c0 + lane;
+      const size_t mine = size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * 256 + at;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (c <= k.c1 && p.last[c] >= 0) ml = p.part_ml[mine];  // (a worker without a share has no part)
+      float mn = fmaxf(m, ml.x);
 #pragma unroll
-      for (int e = 0; e < V; ++e) o[e] = o[e] * wa + f[e] * wb;
-      l = l * wa + ml.y * wb;
+      for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+      const float mu = mn == -INFINITY ? 0.0f : mn;
+      const float wa = ex2_mufu(m - mu);  // (0 for m = -inf)
+      const float wb = ex2_mufu(ml.x - mu);
+      float ls = ml.y * wb;
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+      l = l * wa + ls;
       m = mn;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] *= wa;
+      const int n = min(32, k.c1 - c0 + 1);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, wb, i), li = __shfl_sync(0xffffffffu, ml.y, i);
+        const int ci = c0 + i;
+        if (li == 0.0f) continue;  // no key of this part is visible to the row: its O may not have been written
+        const float* src = p.part_o + (size_t(ci == k.c0 ? 2 * ci + 1 : 2 * ci) * 256 + at) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 t = *reinterpret_cast<const float4*>(src);
+          o[0] = fmaf(t.x, wi, o[0]);
+          o[1] = fmaf(t.y, wi, o[1]);
+          o[2] = fmaf(t.z, wi, o[2]);
+          o[3] = fmaf(t.w, wi, o[3]);
+        } else {
+          const float2 t = *reinterpret_cast<const float2*>(src);
+          o[0] = fmaf(t.x, wi, o[0]);
+          o[1] = fmaf(t.y, wi, o[1]);
+        }
+      }
     }
     const int tok = r / p.group, head = k.kvh * p.group + (r - tok * p.group), token = k.row0 + tok;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -766,7 +964,7 @@ Space carve(uint8_t* base, const SeqProblem& pb, int G, int tok) {
 template <int D, bool PAGED>
 cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t stream) {
   using C = Tiles<D>;
-  const int G = num_sms();
+  const int G = std::min(num_sms(), seq::kMaxWorkers);
   const int group = pb.Hq / pb.Hkv, tok = 128 / group;
   Params p{};
   // q: rows (token, head of the group), `tok` tokens to a tile
@@ -776,6 +974,16 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
     const uint64_t strides[3] = {uint64_t(D) * 2, uint64_t(pb.q_stride) * 2, uint64_t(group) * D * 2};
     const uint32_t box[4] = {64, uint32_t(group), uint32_t(tok), 1};
     if (!encode_tiled(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pb.q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  // o: the 32 rows of a warp, where they are whole tokens
+  CUtensorMap mo = mq;
+  if (32 % group == 0) {
+    p.o_box = 32 / group;
+    const uint64_t dims[4] = {uint64_t(D), uint64_t(group), uint64_t(pb.total_q), uint64_t(pb.Hkv)};
+    const uint64_t strides[3] = {uint64_t(D) * 2, uint64_t(pb.Hq) * D * 2, uint64_t(group) * D * 2};
+    const uint32_t box[4] = {64, uint32_t(group), uint32_t(p.o_box), 1};
+    if (!encode_tiled(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, o, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
   if constexpr (PAGED) {
@@ -841,6 +1049,7 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   const DebugCfg dc = debug_cfg();
   p.wait_limit_ns = dc.wait_limit_ns;
   p.inject = dc.inject;
+  p.trace = dc.trace;
   plan_kernel<FwdSide><<<1, kPlanThreads, 0, stream>>>(a);
   e = cudaGetLastError();
   // the kernels after it start while the one before ends, and wait for it
@@ -855,7 +1064,7 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   lc.attrs = pdl;
   lc.numAttrs = 1;
   if (dc.ev_begin) cudaEventRecord(dc.ev_begin, stream);
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&lc, kern, mq, mk, mv, p);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&lc, kern, mq, mk, mv, mo, p);
   if (dc.ev_end) cudaEventRecord(dc.ev_end, stream);
   if (e == cudaSuccess) {
     lc.gridDim = dim3(G, 8);

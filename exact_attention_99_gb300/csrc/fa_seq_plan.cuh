@@ -23,7 +23,8 @@ namespace fa {
 namespace seq {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 2048;  // of the sort by n; units of more tiles sort as equal
+constexpr int kBuckets = 1024;    // of the sort by n; units of more tiles sort as equal
+constexpr int kMaxWorkers = 256;  // CTAs of a main kernel
 
 // An item is a unit, or a part of one, for one kv head.
 struct __align__(16) FwdItem {
@@ -218,11 +219,11 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 }
 
 // the last b in [0, B) with start[b] * scale <= x
-__device__ __forceinline__ int find_seq(const int* start, int B, int scale, long long x) {
+__device__ __forceinline__ int find_seq(const int* start, int B, int scale, int x) {
   int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (1LL * start[mid] * scale <= x) {
+    if (start[mid] * scale <= x) {
       lo = mid;
     } else {
       hi = mid;
@@ -231,16 +232,36 @@ __device__ __forceinline__ int find_seq(const int* start, int B, int scale, long
   return lo;
 }
 
+// What the planning block keeps at hand; larger batches than that are read
+// from device memory.
+constexpr int kNearSeqs = 512, kNearUnits = 2048;
+
 template <class Side>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side> a) {
   using Item = typename Side::Item;
   __shared__ long long sums[32];
   __shared__ int hist[kBuckets];
+  __shared__ long long share[kMaxWorkers + 1];
+  __shared__ Seq near_seq[kNearSeqs];
+  __shared__ int near_ustart[kNearSeqs + 1];
+  __shared__ long long near_cost[kNearUnits + 1];
+  __shared__ int near_order[kNearUnits];
   __shared__ unsigned long long worst;
   __shared__ int bad;
   const int tid = threadIdx.x;
-  const int B = a.L.B, G = a.G;
+  const int B = a.L.B, G = a.G, Hkv = a.Hkv;
   const Plan<Item>& P = a.P;
+  const bool near_b = B <= kNearSeqs;
+  int* const ustart = near_b ? near_ustart : P.ustart;
+  auto seq_of = [&](int b) {
+    Seq s;
+    if (near_b) {
+      s = near_seq[b];
+    } else {
+      seq_at(a.L, b, s);
+    }
+    return s;
+  };
   if (tid == 0) {
     bad = 0;
     worst = 0;
@@ -265,10 +286,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
       } else {
         bad = 1;
       }
+      if (near_b) near_seq[b] = s;
     }
     const long long end = block_scan(n, sums, sum) + n_units;
     if (b < B) {
-      P.ustart[b] = int((end - n) & 0x7fffffff);
+      ustart[b] = int((end - n) & 0x7fffffff);
       P.tstart[b] = int((end - n) >> 32);
     }
     n_units += sum;
@@ -285,9 +307,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   }
   const int U = int(n_units & 0xffffffffll);
   if (tid == 0) {
-    P.ustart[B] = U;
+    ustart[B] = U;
     P.tstart[B] = int(n_units >> 32);
   }
+  long long* const cost = U <= kNearUnits ? near_cost : P.cost;
+  int* const order = U <= kNearUnits ? near_order : P.order;
   __syncthreads();
   // n of each unit: running sum and histogram
   long long T = 0;
@@ -295,17 +319,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     const int u = u0 + tid;
     int n = 0;
     if (u < U) {
-      Seq s;
-      const int b = find_seq(P.ustart, B, 1, u);
-      seq_at(a.L, b, s);
-      n = a.side.range(s, u - P.ustart[b]).n;
+      const int b = find_seq(ustart, B, 1, u);
+      n = a.side.range(seq_of(b), u - ustart[b]).n;
       atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1);
     }
     const long long end = block_scan(n, sums, sum) + T;
-    if (u < U) P.cost[u] = end - n;
+    if (u < U) cost[u] = end - n;
     T += sum;
   }
-  if (tid == 0) P.cost[U] = T;
+  if (tid == 0) cost[U] = T;
+  const long long Ttot = T * Hkv;
+  for (int c = tid; c <= G; c += kPlanThreads) share[c] = Ttot * c / G;
   __syncthreads();
   // sorted order (arbitrary within a bucket, which changes no result)
   long long base = 0;
@@ -317,74 +341,74 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   }
   __syncthreads();
   for (int u = tid; u < U; u += kPlanThreads) {
-    const int n = int(P.cost[u + 1] - P.cost[u]);
-    P.order[atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1)] = u;
+    const int n = int(cost[u + 1] - cost[u]);
+    order[atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1)] = u;
   }
   __syncthreads();
   // The busiest worker in sorted order against an equal division, in half
   // tile products: an item costs half a product more than it has; dividing
   // costs part_cost (the parts' stores and the last kernel).
-  const long long n_items = 1LL * U * a.Hkv;
+  const int n_items = U * Hkv;
   for (int c = tid; c < G; c += kPlanThreads) {
     unsigned long long t = 0;
-    for (long long r = 0; r * G < n_items; ++r) {
-      const long long i = r * G + ((r & 1) ? G - 1 - c : c);
+    for (int r = 0; r * G < n_items; ++r) {
+      const int i = r * G + ((r & 1) ? G - 1 - c : c);
       if (i < n_items) {
-        const int u = P.order[i / a.Hkv];
-        t += 2 * (P.cost[u + 1] - P.cost[u]) + 1;
+        const int u = order[i / Hkv];
+        t += 2 * (cost[u + 1] - cost[u]) + 1;
       }
     }
     atomicMax(&worst, t);
   }
   __syncthreads();
-  const long long Ttot = T * a.Hkv;
   const bool split = Ttot > 0 && static_cast<long long>(worst) > 2 * ((Ttot + G - 1) / G) + a.part_cost;
-  if (tid == 0) *P.head = PlanHead{int(n_items), split ? 1 : 0, 0, 0};
-  auto share = [&](int c) -> long long { return Ttot * c / G; };
-  for (long long i = tid; i < n_items; i += kPlanThreads) {
-    Seq s;
-    if (!split) {
-      const int u = P.order[i / a.Hkv], b = find_seq(P.ustart, B, 1, u);
-      seq_at(a.L, b, s);
-      const Range r = a.side.range(s, u - P.ustart[b]);
-      Item it = a.side.item(s, b, u - P.ustart[b], int(i % a.Hkv), P.tstart[b]);
+  if (tid == 0) *P.head = PlanHead{n_items, split ? 1 : 0, 0, 0};
+  if (!split) {
+    for (int i = tid; i < n_items; i += kPlanThreads) {
+      const int u = order[i / Hkv], b = find_seq(ustart, B, 1, u);
+      const Seq s = seq_of(b);
+      const Range r = a.side.range(s, u - ustart[b]);
+      Item it = a.side.item(s, b, u - ustart[b], i % Hkv, P.tstart[b]);
       Side::set_range(it, r.first, r.n);
       P.items[i] = it;
-      continue;
     }
+    return;
+  }
+  const float per_worker = float(G) / float(Ttot);
+  for (int i = tid; i < n_items; i += kPlanThreads) {
     // order (sequence, kv head, unit): the place [x0, x1) of item i among all
     // tile products; worker c has [share(c), share(c + 1))
-    const int b = find_seq(P.ustart, B, a.Hkv, i);
-    seq_at(a.L, b, s);
-    const int us = P.ustart[b], per = P.ustart[b + 1] - us;
-    const int j = int(i - 1LL * us * a.Hkv), kvh = j / per, ju = j - kvh * per;
+    const int b = find_seq(ustart, B, Hkv, i);
+    const Seq s = seq_of(b);
+    const int us = ustart[b], per = ustart[b + 1] - us;
+    const int j = i - us * Hkv, kvh = j / per, ju = j - kvh * per;
     const Range r = a.side.range(s, ju);
-    const long long of_seq = P.cost[us + per] - P.cost[us];
-    const long long x0 = P.cost[us] * a.Hkv + kvh * of_seq + (P.cost[us + ju] - P.cost[us]), x1 = x0 + r.n;
+    const long long of_seq = cost[us + per] - cost[us];
+    const long long x0 = cost[us] * Hkv + kvh * of_seq + (cost[us + ju] - cost[us]), x1 = x0 + r.n;
     Item it = a.side.item(s, b, ju, kvh, P.tstart[b]);
     const int count = it.count;
     // the worker that has product x0 (fewer products than workers: the last
-    // of those whose share begins there)
-    int c = int(min(x0 * G / Ttot, 1LL * G - 1));
-    while (c > 0 && share(c) > x0) --c;
-    while (c + 1 < G && share(c + 1) <= x0) ++c;
+    // of those whose share begins there), from a guess
+    int c = max(0, min(int(float(x0) * per_worker), G - 1));
+    while (c > 0 && share[c] > x0) --c;
+    while (c + 1 < G && share[c + 1] <= x0) ++c;
     const int c0 = c;
     long long x = x0;
     do {
-      const long long e = c + 1 < G ? min(x1, share(c + 1)) : x1;
+      const long long e = c + 1 < G ? min(x1, share[c + 1]) : x1;
       const bool part = x > x0 || e < x1;
       it.count = count | (part ? kPart : 0) | (x > x0 ? kCont : 0);
       Side::set_range(it, r.first + int(x - x0), int(e - x));
       // one entry per (item, worker), in order: no two have the same sum, and
       // a worker's entries follow one another
-      const int at = int(i) + c;
+      const int at = i + c;
       P.items[at] = it;
       atomicMin(&P.first[c], at);
       atomicMax(&P.last[c], at);
       x = e;
       if (x < x1)
         do ++c;
-        while (c + 1 < G && share(c + 1) <= x);
+        while (c + 1 < G && share[c + 1] <= x);
     } while (x < x1);
     if (c > c0) {
       Cut& k = P.cuts[c0 + 1];

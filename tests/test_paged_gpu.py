@@ -54,6 +54,15 @@ def test_mixed_chunks(fa):
     run(fa, [1, 33, 1, 200, 0, 64, 1, 300], [900, 33, 4000, 200, 50, 640, 1, 1111], 8, 2, 64, 16, seed=11, fused=True)
 
 
+@pytest.mark.parametrize("hq,hk,d", [(16, 8, 128), (32, 8, 64)])
+def test_many_items_per_cta(fa, hq, hk, d):
+    # chunks and single tokens, several work items to a CTA
+    g = torch.Generator().manual_seed(hq)
+    new = [1 if i % 3 else int(n) for i, n in enumerate(torch.randint(1, 300, (48,), generator=g))]
+    keys = [n + int(m) for n, m in zip(new, torch.randint(0, 500, (48,), generator=g))]
+    run(fa, new, keys, hq, hk, d, 16, seed=hq)
+
+
 @pytest.mark.parametrize("causal,window", [(True, (100, 0)), (False, (40, 7)), (False, None), (True, (0, 0))])
 def test_masks(fa, causal, window):
     run(fa, [1, 70, 9, 5], [500, 333, 9, 2], 4, 2, 128, 64, seed=12, causal=causal, window=window)

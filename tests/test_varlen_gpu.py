@@ -95,6 +95,14 @@ def test_many_sequences(fa):
     run(fa, n, n, 2, 1, 64, seed=6)
 
 
+@pytest.mark.parametrize("hq,hk,d", [(16, 8, 128), (24, 8, 64), (20, 20, 128)])
+def test_many_items_per_cta(fa, hq, hk, d):
+    # long and short units mixed, several to a CTA
+    rng = torch.Generator().manual_seed(hq)
+    n = torch.randint(0, 420, (36,), generator=rng).tolist()
+    run(fa, n, n, hq, hk, d, seed=hq)
+
+
 def test_group_of_128(fa):
     run(fa, [5, 3], [300, 3], 128, 1, 64, seed=7)
 
