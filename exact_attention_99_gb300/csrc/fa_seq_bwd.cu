@@ -874,7 +874,6 @@ cudaError_t launch_t(const SeqProblem& pb, const void* o, const float* lse, cons
   a.side = seq::BwdSide{tok, pb.window_left, pb.window_right};
   a.Hkv = pb.Hkv;
   a.G = G;
-  a.part_cost = 8;
   a.status = status;
   Params p{};
   p.dk = static_cast<__nv_bfloat16*>(dk);

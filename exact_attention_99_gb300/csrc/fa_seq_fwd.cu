@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (wg <= 1) {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<176>();
+    setmaxnreg_inc<168>();
     const int s = wg, wq = warp & 3;
     const int row = (wq << 5) + lane;
     const uint32_t t_s = tmem + (uint32_t(wq) << 21) + uint32_t(s * 128);  // lane quarter + S columns
@@ -296,9 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
             if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
             const uint32_t span = uint32_t(max(hi - lo, 0));
+            // only the blocks of 32 columns that some row of the warp does not
+            // see whole: code that runs once per item is slow to fetch
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+            for (int b = 0; b < 128; b += 32) {
+              if (lo <= b && hi >= b + 32) continue;
+#pragma unroll
+              for (int c = b; c < b + 32; ++c)
+                if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+            }
           }
           float mA = -INFINITY, mB = -INFINITY, mC = -INFINITY, mD = -INFINITY;
 #pragma unroll
@@ -368,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (wg == 2) {
     // ------------------------------------------------ correction + epilogue
-    setmaxnreg_dec<80>();
+    setmaxnreg_dec<104>();
     const int wq = warp & 3;
     const int row = (wq << 5) + lane;
     const uint32_t t_lane = tmem + (uint32_t(wq) << 21) + kOCol0;
@@ -471,82 +477,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rows > 0) {
           const bool valid = lane < rows;
           const int token = q0 + s * p.tok + row_tok, head = kvh * p.group + row_head;
-          // columns [16 c, 16 c + 16) of the (joined) O
-          auto columns = [&](int c, float (&f)[16]) {
-            uint32_t v[16];
-            if (n > 0) {
-              tmem_ld16(t_lane + s * D + c * 16, v);
-              if (nj > 0) {
-                uint32_t u[16];
-                tmem_ld16(t_lane + D + c * 16, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) f[e] = fmaf(u2f(u[e]), f1, u2f(v[e]) * f0);
-              } else {
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) f[e] = u2f(v[e]) * f0;
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) f[e] = 0.0f;
-            }
-          };
-          if (part) {
-            const size_t at = size_t(2 * int(blockIdx.x) + ((w->flags & kCont) ? 0 : 1)) * 256 + s * 128 + row;
-            if (valid) p.part_ml[at] = make_float2(m, l);
-            float4* dst = reinterpret_cast<float4*>(p.part_o + at * D);
+          // 32 columns at a time, the next ones on their way from tensor
+          // memory. A part's rows go to its slot as they are. Else 32 rows x
+          // 64 columns go through a staging buffer (128-byte swizzle), and out
+          // by one TMA store where the warp's rows are whole tokens of the
+          // sequence, or by plain stores of whole rows.
+          const size_t at = size_t(2 * int(blockIdx.x) + ((w->flags & kCont) ? 0 : 1)) * 256 + s * 128 + row;
+          const bool tma = p.o_box != 0 && rows >= 32;
+          uint32_t v[32], x[32];
+          if (n > 0) tmem_ld32(t_lane + s * D, x);
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              float f[16];
-              columns(c, f);
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = n > 0 ? f2u(u2f(x[e]) * f0) : 0u;
+            if (nj > 0) {
+              tmem_ld32(t_lane + D + c * 32, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = f2u(fmaf(u2f(x[e]), f1, u2f(v[e])));
+            }
+            if (n > 0 && c + 1 < D / 32) tmem_ld32(t_lane + s * D + (c + 1) * 32, x);
+            if (part) {
               if (valid) {
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + c * 32);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[c * 4 + e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                for (int e = 0; e < 8; ++e) dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
               }
+              continue;
             }
-          } else {
-            // 32 rows x 64 columns at a time through a staging buffer
-            // (128-byte swizzle): by one TMA store where the warp's rows are
-            // whole tokens of the sequence, else by plain stores of whole rows
-            const bool tma = p.o_box != 0 && rows >= 32;
-            const int orow = valid ? token * p.Hq + head : -1;
-#pragma unroll 1
-            for (int hf = 0; hf < D / 64; ++hf) {
+            if ((c & 1) == 0) {
               if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
               __syncwarp();
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                float f[16];
-                columns(hf * 4 + c, f);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  *reinterpret_cast<uint4*>(stg + lane * 128 + (((c * 2 + e) ^ (lane & 7)) << 4)) =
-                      make_uint4(pack_bf16x2(f[8 * e], f[8 * e + 1]), pack_bf16x2(f[8 * e + 2], f[8 * e + 3]),
-                                 pack_bf16x2(f[8 * e + 4], f[8 * e + 5]), pack_bf16x2(f[8 * e + 6], f[8 * e + 7]));
-              }
-              if (tma) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                  tma_store_4d(&tmO, stg, hf * 64, 0, q0 + s * p.tok + wq * p.o_box, kvh);
-                  bulk_commit();
-                }
-              } else {
-                __syncwarp();
-                // 8 lanes write a row's 128 bytes, 4 rows at a time
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int rr = e * 4 + (lane >> 3);
-                  const int to = __shfl_sync(0xffffffffu, orow, rr);
-                  const uint4 x = *reinterpret_cast<const uint4*>(stg + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-                  if (to >= 0) *reinterpret_cast<uint4*>(p.o + size_t(to) * D + hf * 64 + (lane & 7) * 8) = x;
-                }
-                __syncwarp();
-              }
             }
-            if (valid)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t* y = &v[8 * e];
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((((c & 1) * 4 + e) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(u2f(y[0]), u2f(y[1])), pack_bf16x2(u2f(y[2]), u2f(y[3])),
+                             pack_bf16x2(u2f(y[4]), u2f(y[5])), pack_bf16x2(u2f(y[6]), u2f(y[7])));
+            }
+            if ((c & 1) == 0) continue;
+            if (tma) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                tma_store_4d(&tmO, stg, (c >> 1) * 64, 0, q0 + s * p.tok + wq * p.o_box, kvh);
+                bulk_commit();
+              }
+            } else {
+              __syncwarp();
+              // 8 lanes write a row's 128 bytes, 4 rows at a time
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e) {
+                const int rr = e * 4 + (lane >> 3);
+                const int to = __shfl_sync(0xffffffffu, valid ? token * p.Hq + head : -1, rr);
+                const uint4 y = *reinterpret_cast<const uint4*>(stg + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                if (to >= 0) *reinterpret_cast<uint4*>(p.o + size_t(to) * D + (c >> 1) * 64 + (lane & 7) * 8) = y;
+              }
+              __syncwarp();
+            }
+          }
+          if (valid) {
+            if (part) {
+              p.part_ml[at] = make_float2(m, l);
+            } else {
               p.lse[size_t(head) * p.total_q + token] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+            }
           }
         }
         if (n > 0) {  // the next item's products may overwrite O
@@ -564,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) bulk_wait_all();  // stores complete (and staging reads done) before the CTA exits
   } else {
-    setmaxnreg_dec<80>();
+    setmaxnreg_dec<72>();
   }
   if (warp == 12) {
     // ------------------------------------------------------- TMA producer
@@ -598,18 +595,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_4d_hint(sQ + b * C::kTileBytes + c * 16384, &tmQ, &ctl.q_full[b], c * 64, 0,
                              w->q0 + (key ? 0 : s * p.tok), kvh, pol_q);
-        }
-      }
-      // The next item's Q and first K and V tile into L2, a lane to each box:
-      // its loads wait for buffers that this item still uses, and would
-      // then wait for device memory too.
-      if (const Work* const w2 = item(i + 1); w2 != nullptr && w2->nt > 0) {
-        const int c = lane % C::kChunks * 64, what = lane / C::kChunks;
-        if (what < 2) {
-          if (w2->n[what] > 0 && !(what == 1 && (w2->flags & kKeyMode)))
-            tma_prefetch_l2_4d(&tmQ, c, 0, w2->q0 + what * p.tok, w2->kvh);
-        } else if (!PAGED && what < 4) {
-          tma_prefetch_l2_4d(what == 2 ? &tmK : &tmV, c, w2->kvh, w2->kbase + w2->kt * 128, 0);
         }
       }
       // K runs d tiles ahead of V: K(0..d-1), then V(t), K(t + d) in turn, then the last V
@@ -843,21 +828,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 15) {
     // --------------------------------------------------------- work items
-    if (lane == 0) {
-      Walk wk = walk_begin(p.head, p.first, p.last);
-      for (int i = 0;; ++i) {
-        const bool more = wk.i <= wk.last;
-        Work x;
-        x.flags = -1;
-        if (more) {
-          x = work_of(p, p.items + wk.i);
-          walk_step(wk);
+    Walk wk = walk_begin(p.head, p.first, p.last);
+    for (int i = 0;; ++i) {
+      const bool more = wk.i <= wk.last;
+      Work x;
+      x.flags = -1;
+      if (more) {
+        x = work_of(p, p.items + wk.i);
+        walk_step(wk);
+        // Its Q and its first K and V tile into L2, a lane to each box: the
+        // loads wait for buffers that items before still use, and would then
+        // wait for device memory too.
+        const int c = lane % C::kChunks * 64, what = lane / C::kChunks;
+        if (x.nt > 0) {
+          if (what < 2) {
+            if ((what == 0 ? x.n[0] : x.n[1]) > 0 && !(what == 1 && (x.flags & kKeyMode)))
+              tma_prefetch_l2_4d(&tmQ, c, 0, x.q0 + what * p.tok, x.kvh);
+          } else if (!PAGED && what < 4) {
+            tma_prefetch_l2_4d(what == 2 ? &tmK : &tmV, c, x.kvh, x.kbase + x.kt * 128, 0);
+          }
         }
-        if (!wait_bounded(&ctl.it_empty[i % kItems], ((i / kItems) & 1) ^ 1, abort_flag, LIM)) break;
+      }
+      const bool ok = wait_bounded(&ctl.it_empty[i % kItems], ((i / kItems) & 1) ^ 1, abort_flag, LIM);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
         ctl.it[i % kItems] = x;
         mbar_arrive(&ctl.it_full[i % kItems]);
-        if (!more) break;
       }
+      if (!more) break;
     }
   }
 
@@ -1023,7 +1021,6 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   a.side = FwdSide{tok, pb.window_left, pb.window_right, pb.page_table != nullptr ? 1 : 0};
   a.Hkv = pb.Hkv;
   a.G = G;
-  a.part_cost = 8;
   a.status = p.status;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;

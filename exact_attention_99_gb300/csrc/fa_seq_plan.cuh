@@ -12,9 +12,11 @@
 //   split : all tile products laid end to end (sequence, kv head, unit), an
 //           equal share to each CTA. A unit that a boundary falls into is
 //           done in parts, and a last kernel joins them in the CTAs' order.
-// Sorted order leaves no parts and ends within its shortest units where there
-// are many; few units (a chunk of new tokens over long caches) would leave
-// CTAs idle, and are split.
+// Sorted order leaves no parts, ends within its shortest units where there
+// are many, and lets the CTAs walk the same keys at the same time; few units
+// (a chunk of new tokens over long caches) would leave CTAs idle, and are
+// split. Every unit costs kItemCost products beside its own: Q's load, the
+// first S that nothing overlaps, the epilogue.
 #pragma once
 #include "fa_seq.cuh"
 #include "sm103_ptx.cuh"
@@ -25,6 +27,7 @@ namespace seq {
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;    // of the sort by n; units of more tiles sort as equal
 constexpr int kMaxWorkers = 256;  // CTAs of a main kernel
+constexpr int kItemCost = 2;
 
 // An item is a unit, or a part of one, for one kv head.
 struct __align__(16) FwdItem {
@@ -82,7 +85,7 @@ struct Plan {
   Cut* cuts;        // [G]
   int* ustart;      // [B + 1] first unit of each sequence
   int* tstart;      // [B + 1] first row tile of each sequence
-  long long* cost;  // [units + 1] tile products of the units before
+  long long* cost;  // [units + 1] cost of the units before
   int* order;       // [units] longest first
   Item* items;      // [units * Hkv + G]
   int max_units;
@@ -189,7 +192,6 @@ struct PlanArgs {
   Plan<typename Side::Item> P;
   Side side;
   int Hkv, G;
-  int part_cost;  // what dividing units costs, in half tile products
   unsigned* status;
 };
 
@@ -323,6 +325,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
       n = a.side.range(seq_of(b), u - ustart[b]).n;
       atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1);
     }
+    n = u < U ? n + kItemCost : 0;
     const long long end = block_scan(n, sums, sum) + T;
     if (u < U) cost[u] = end - n;
     T += sum;
@@ -341,13 +344,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   }
   __syncthreads();
   for (int u = tid; u < U; u += kPlanThreads) {
-    const int n = int(cost[u + 1] - cost[u]);
+    const int n = int(cost[u + 1] - cost[u]) - kItemCost;
     order[atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1)] = u;
   }
   __syncthreads();
-  // The busiest worker in sorted order against an equal division, in half
-  // tile products: an item costs half a product more than it has; dividing
-  // costs part_cost (the parts' stores and the last kernel).
+  // The busiest worker in sorted order against an equal division, which has
+  // to win by more than what the parts' stores and the last kernel cost (6
+  // products) and what CTAs at different keys cost: one causal sequence of
+  // 16384 tokens (32 query heads, 8 kv heads) took 1.80 ms sorted and 1.91 ms
+  // split at 1 % less imbalance; packed prompts 0.41 and 0.59 ms.
   const int n_items = U * Hkv;
   for (int c = tid; c < G; c += kPlanThreads) {
     unsigned long long t = 0;
@@ -355,13 +360,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
       const int i = r * G + ((r & 1) ? G - 1 - c : c);
       if (i < n_items) {
         const int u = order[i / Hkv];
-        t += 2 * (cost[u + 1] - cost[u]) + 1;
+        t += cost[u + 1] - cost[u];
       }
     }
     atomicMax(&worst, t);
   }
   __syncthreads();
-  const bool split = Ttot > 0 && static_cast<long long>(worst) > 2 * ((Ttot + G - 1) / G) + a.part_cost;
+  const bool split = static_cast<long long>(worst) > Ttot / G + Ttot / (8 * G) + 6;
   if (tid == 0) *P.head = PlanHead{n_items, split ? 1 : 0, 0, 0};
   if (!split) {
     for (int i = tid; i < n_items; i += kPlanThreads) {
@@ -376,15 +381,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   }
   const float per_worker = float(G) / float(Ttot);
   for (int i = tid; i < n_items; i += kPlanThreads) {
-    // order (sequence, kv head, unit): the place [x0, x1) of item i among all
-    // tile products; worker c has [share(c), share(c + 1))
+    // order (sequence, kv head, unit): the place [x0, x1) of item i's products
+    // among all costs; worker c has those in [share(c), share(c + 1))
     const int b = find_seq(ustart, B, Hkv, i);
     const Seq s = seq_of(b);
     const int us = ustart[b], per = ustart[b + 1] - us;
     const int j = i - us * Hkv, kvh = j / per, ju = j - kvh * per;
     const Range r = a.side.range(s, ju);
     const long long of_seq = cost[us + per] - cost[us];
-    const long long x0 = cost[us] * Hkv + kvh * of_seq + (cost[us + ju] - cost[us]), x1 = x0 + r.n;
+    // (its own cost comes first, and is nobody's)
+    const long long x0 = cost[us] * Hkv + kvh * of_seq + (cost[us + ju] - cost[us]) + kItemCost, x1 = x0 + r.n;
     Item it = a.side.item(s, b, ju, kvh, P.tstart[b]);
     const int count = it.count;
     // the worker that has product x0 (fewer products than workers: the last
