@@ -104,10 +104,25 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = _get_device = None
+
+
+def _current_stream() -> int:
+    """The current stream's handle (without building a Stream object, which
+    takes longer than a small call's checks)."""
+    global _raw_stream, _get_device
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _raw_stream(_get_device())
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -314,37 +329,54 @@ def fa_cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, B, Hkv, to
                                  v_stride, _stream(stream))
 
 
-def _tokens(name, t, device=None, shape=None):
-    """Checks a packed [total, H, d] tensor; returns its elements between tokens."""
+_bf16 = _i32 = _f32 = _empty = None
+
+
+def _types():
+    global _bf16, _i32, _f32, _empty
     import torch
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or not t.is_cuda or t.shape[1] < 1:
-        raise ValueError(f"{name} must be a CUDA bf16 tensor of shape [tokens, heads, d]")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, q is on {device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have the shape {shape}")
-    n, h, d = t.shape
-    s = t.stride()
+    _bf16, _i32, _f32, _empty = torch.bfloat16, torch.int32, torch.float32, torch.empty
+
+
+def _tokens(name, t, device, shape):
+    """Checks a packed [total, H, d] tensor; returns its elements between tokens."""
+    if t.dtype != _bf16 or t.shape != shape or t.device != device:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on {device}")
+    n, h, d = shape
+    s0, s1, s2 = t.stride()
     if n <= 1:  # the stride of an axis of one has no meaning
-        s = (h * d, s[1], s[2])
-    if s[2] != 1 or (h > 1 and s[1] != d) or s[0] < h * d:
+        s0 = h * d
+    if s2 != 1 or (s1 != d and h > 1) or s0 < h * d:
         raise ValueError(f"{name}: the heads of a token must be contiguous, and tokens must not overlap")
-    return s[0]
+    return s0
+
+
+def _first(name, t):
+    """The device of a call's first tensor, after a check of its form."""
+    if _bf16 is None:
+        _types()
+    if t.dim() != 3 or not t.is_cuda or t.shape[1] < 1:
+        raise ValueError(f"{name} must be a CUDA bf16 tensor of shape [tokens, heads, d]")
+    return t.device
 
 
 def _ints(name, t, shape, device):
-    import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype != _i32 or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
 
 
+def _packed(name, t, shape, device, dtype=None):
+    if t.shape != shape or t.dtype != (dtype or _bf16) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype or _bf16} tensor of shape {tuple(shape)} on {device}")
+
+
 def _pages(k_pages, v_pages, hkv, d, device):
-    import torch
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if (t.dtype != torch.bfloat16 or t.dim() != 4 or t.shape != k_pages.shape or tuple(t.shape[2:]) != (hkv, d)
-                or not t.is_contiguous() or t.device != device):
-            raise ValueError(f"{name} must be a contiguous bf16 tensor of shape [pages, page_size, {hkv}, {d}] on {device}")
-    return k_pages.shape[0], k_pages.shape[1]
+    shape = k_pages.shape
+    if len(shape) != 4 or shape[2] != hkv or shape[3] != d:
+        raise ValueError(f"k_pages must have the shape [pages, page_size, {hkv}, {d}]")
+    _packed("k_pages", k_pages, shape, device)
+    _packed("v_pages", v_pages, shape, device)
+    return shape[0], shape[1]
 
 
 class _on:
@@ -371,24 +403,54 @@ class _on:
             g.__exit__(*exc)
 
 
-def _packed(name, t, shape, device):
-    import torch
-    if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous bf16 tensor of shape {shape} on {device}")
+def _there(device, stream, call, *args):
+    """call(stream handle, *args) where the tensors are: at once on the current
+    device and stream, else with those made current."""
+    if stream is None:
+        here = _current_stream()
+        if device.index == _get_device():
+            return call(here, *args)
+    with _on(device, stream):
+        return call(_current_stream(), *args)
 
 
-def _seq_out(q, out):
+def _seq_out(q, shape, out):
     """The given (o, lse) after a check, or new ones."""
-    import torch
-    total, hq, d = q.shape
+    total, hq, _ = shape
     if out is None:
-        return (torch.empty((total, hq, d), device=q.device, dtype=torch.bfloat16),
-                torch.empty((hq, total), device=q.device, dtype=torch.float32))
+        return _empty(shape, dtype=_bf16, device=q.device), _empty((hq, total), dtype=_f32, device=q.device)
     o, lse = out
-    _packed("o", o, (total, hq, d), q.device)
-    if tuple(lse.shape) != (hq, total) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != q.device:
-        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(hq, total)} on {q.device}")
+    _packed("o", o, shape, q.device)
+    _packed("lse", lse, (hq, total), q.device, _f32)
     return o, lse
+
+
+def _fwd_varlen(stream, q, k, v, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr):
+    o, lse = _seq_out(q, shape, out)
+    total_q, hq, d = shape
+    total_k, hkv, _ = kshape
+    st = lib().fa_fwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_q.data_ptr(),
+                             cu_k.data_ptr(), cu_q.shape[0] - 1, hq, hkv, total_q, total_k, d, *strides, scale, wl, wr,
+                             stream)
+    if st != 0:
+        raise FAError(st, "fa_fwd_varlen")
+    return o, lse
+
+
+def _varlen_args(q, k, v, cu_q, cu_k):
+    """Checks shared by forward_varlen and backward_varlen: device, shapes, token strides."""
+    device = _first("q", q)
+    shape, kshape = q.shape, k.shape
+    if len(kshape) != 3 or kshape[2] != shape[2] or kshape[1] < 1:
+        raise ValueError(f"k must have the shape [tokens, kv heads, {shape[2]}]")
+    strides = _tokens("q", q, device, shape), _tokens("k", k, device, kshape), _tokens("v", v, device, kshape)
+    n = cu_q.shape
+    _ints("cu_q", cu_q, n, device)
+    if cu_k is not cu_q:
+        _ints("cu_k", cu_k, n, device)
+    if len(n) != 1 or n[0] < 2:
+        raise ValueError("cu_q must hold the row offsets of one sequence at least")
+    return device, shape, kshape, strides
 
 
 def forward_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | None = None, out=None, stream=None,
@@ -397,21 +459,28 @@ def forward_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | Non
     [total_q, Hq, d], k/v [total_k, Hkv, d] (bf16, CUDA; tokens may be strided),
     cu_q, cu_k int32 [B + 1] row offsets on the device (see fa.h fa_fwd_varlen).
     Rows outside every sequence are left as they are (unset in new outputs)."""
-    qs = _tokens("q", q)
-    total_q, hq, d = q.shape
-    total_k, hkv = k.shape[0], k.shape[1]
-    ks, vs = _tokens("k", k, q.device, (total_k, hkv, d)), _tokens("v", v, q.device, (total_k, hkv, d))
-    B = cu_q.shape[0] - 1
-    _ints("cu_q", cu_q, (B + 1,), q.device)
-    _ints("cu_k", cu_k, (B + 1,), q.device)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _on(q.device, stream):
-        o, lse = _seq_out(q, out)
-        st = fa_fwd_varlen(q, k, v, o, lse, cu_q, cu_k, B, hq, hkv, total_q, total_k, d, qs, ks, vs, scale,
-                           *_window_args(causal, window))
+    device, shape, kshape, strides = _varlen_args(q, k, v, cu_q, cu_k)
+    scale = 1.0 / math.sqrt(shape[2]) if scale is None else scale
+    return _there(device, stream, _fwd_varlen, q, k, v, cu_q, cu_k, out, shape, kshape, strides, scale,
+                  *_window_args(causal, window))
+
+
+def _bwd_varlen(stream, q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr):
+    total_q, hq, d = shape
+    total_k, hkv, _ = kshape
+    if out is None:
+        dq, dk, dv = (_empty(x, dtype=_bf16, device=q.device) for x in (shape, kshape, kshape))
+    else:
+        dq, dk, dv = out
+        _packed("dq", dq, shape, q.device)
+        _packed("dk", dk, kshape, q.device)
+        _packed("dv", dv, kshape, q.device)
+    st = lib().fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+                             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
+                             cu_q.shape[0] - 1, hq, hkv, total_q, total_k, d, *strides, scale, wl, wr, stream)
     if st != 0:
-        raise FAError(st, "fa_fwd_varlen")
-    return o, lse
+        raise FAError(st, "fa_bwd_varlen")
+    return dq, dk, dv
 
 
 def backward_varlen(q, k, v, o, lse, dout, cu_q, cu_k, causal: bool = False, scale: float | None = None, out=None,
@@ -419,31 +488,37 @@ def backward_varlen(q, k, v, o, lse, dout, cu_q, cu_k, causal: bool = False, sca
     """dQ [total_q, Hq, d], dK, dV [total_k, Hkv, d] for the forward_varlen
     that gave o and lse (same offsets, mask and scale); dout [total_q, Hq, d].
     Rows outside every sequence are left as they are (unset in new outputs)."""
-    import torch
-    qs = _tokens("q", q)
-    total_q, hq, d = q.shape
-    total_k, hkv = k.shape[0], k.shape[1]
-    ks, vs = _tokens("k", k, q.device, (total_k, hkv, d)), _tokens("v", v, q.device, (total_k, hkv, d))
-    B = cu_q.shape[0] - 1
-    _ints("cu_q", cu_q, (B + 1,), q.device)
-    _ints("cu_k", cu_k, (B + 1,), q.device)
-    _seq_out(q, (o, lse))
-    _packed("dout", dout, (total_q, hq, d), q.device)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _on(q.device, stream):
-        if out is None:
-            dq, dk, dv = (torch.empty(s, device=q.device, dtype=torch.bfloat16)
-                          for s in ((total_q, hq, d), (total_k, hkv, d), (total_k, hkv, d)))
-        else:
-            dq, dk, dv = out
-            _packed("dq", dq, (total_q, hq, d), q.device)
-            _packed("dk", dk, (total_k, hkv, d), q.device)
-            _packed("dv", dv, (total_k, hkv, d), q.device)
-        st = fa_bwd_varlen(q, k, v, o, lse, dout, dq, dk, dv, cu_q, cu_k, B, hq, hkv, total_q, total_k, d, qs, ks, vs,
-                           scale, *_window_args(causal, window))
+    device, shape, kshape, strides = _varlen_args(q, k, v, cu_q, cu_k)
+    _seq_out(q, shape, (o, lse))
+    _packed("dout", dout, shape, device)
+    scale = 1.0 / math.sqrt(shape[2]) if scale is None else scale
+    return _there(device, stream, _bwd_varlen, q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, strides, scale,
+                  *_window_args(causal, window))
+
+
+def _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, d, device):
+    """Checks shared by forward_paged and cache_append: B, pages, page size, pages of a sequence."""
+    num_pages, page_size = _pages(k_pages, v_pages, hkv, d, device)
+    shape = page_table.shape
+    if len(shape) != 2:
+        raise ValueError("page_table must have the shape [sequences, pages]")
+    B, max_pages = shape
+    _ints("cu_q", cu_q, (B + 1,), device)
+    _ints("lens_k", lens_k, (B,), device)
+    _ints("page_table", page_table, shape, device)
+    return B, num_pages, page_size, max_pages
+
+
+def _fwd_paged(stream, q, k_pages, v_pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes, scale, wl, wr):
+    o, lse = _seq_out(q, shape, out)
+    total_q, hq, d = shape
+    B, num_pages, page_size, max_pages = sizes
+    st = lib().fa_fwd_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                            cu_q.data_ptr(), lens_k.data_ptr(), page_table.data_ptr(), B, hq, hkv, total_q, num_pages,
+                            page_size, max_pages, d, qs, scale, wl, wr, stream)
     if st != 0:
-        raise FAError(st, "fa_bwd_varlen")
-    return dq, dk, dv
+        raise FAError(st, "fa_fwd_paged")
+    return o, lse
 
 
 def forward_paged(q, k_pages, v_pages, cu_q, lens_k, page_table, causal: bool = True, scale: float | None = None,
@@ -452,40 +527,32 @@ def forward_paged(q, k_pages, v_pages, cu_q, lens_k, page_table, causal: bool = 
     (bf16, CUDA; tokens may be strided) over a cache of pages [num_pages,
     page_size, Hkv, d]; cu_q [B + 1], lens_k [B] and page_table [B, max_pages]
     are int32 on the device (see fa.h fa_fwd_paged)."""
-    qs = _tokens("q", q)
-    total_q, hq, d = q.shape
+    device = _first("q", q)
+    shape = q.shape
+    qs = _tokens("q", q, device, shape)
     hkv = k_pages.shape[2] if k_pages.dim() == 4 else 0
-    num_pages, page_size = _pages(k_pages, v_pages, hkv, d, q.device)
-    B = cu_q.shape[0] - 1
-    max_pages = page_table.shape[-1]
-    _ints("cu_q", cu_q, (B + 1,), q.device)
-    _ints("lens_k", lens_k, (B,), q.device)
-    _ints("page_table", page_table, (B, max_pages), q.device)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _on(q.device, stream):
-        o, lse = _seq_out(q, out)
-        st = fa_fwd_paged(q, k_pages, v_pages, o, lse, cu_q, lens_k, page_table, B, hq, hkv, total_q, num_pages,
-                          page_size, max_pages, d, qs, scale, *_window_args(causal, window))
+    sizes = _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, shape[2], device)
+    scale = 1.0 / math.sqrt(shape[2]) if scale is None else scale
+    return _there(device, stream, _fwd_paged, q, k_pages, v_pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes,
+                  scale, *_window_args(causal, window))
+
+
+def _append(stream, k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes):
+    total, hkv, d = shape
+    B, num_pages, page_size, max_pages = sizes
+    st = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), cu_q.data_ptr(),
+                               lens_k.data_ptr(), page_table.data_ptr(), B, hkv, total, num_pages, page_size, max_pages,
+                               d, ks, vs, stream)
     if st != 0:
-        raise FAError(st, "fa_fwd_paged")
-    return o, lse
+        raise FAError(st, "fa_cache_append")
 
 
 def cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, stream=None) -> None:
     """k, v [total_q, Hkv, d] of new tokens (bf16, CUDA; tokens may be strided)
     into the pages, in place; lens_k are the lengths with the new tokens (see
     fa.h fa_cache_append)."""
-    ks = _tokens("k", k)
-    total, hkv, d = k.shape
-    vs = _tokens("v", v, k.device, (total, hkv, d))
-    num_pages, page_size = _pages(k_pages, v_pages, hkv, d, k.device)
-    B = cu_q.shape[0] - 1
-    max_pages = page_table.shape[-1]
-    _ints("cu_q", cu_q, (B + 1,), k.device)
-    _ints("lens_k", lens_k, (B,), k.device)
-    _ints("page_table", page_table, (B, max_pages), k.device)
-    with _on(k.device, stream):
-        st = fa_cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, B, hkv, total, num_pages, page_size,
-                             max_pages, d, ks, vs)
-    if st != 0:
-        raise FAError(st, "fa_cache_append")
+    device = _first("k", k)
+    shape = k.shape
+    ks, vs = _tokens("k", k, device, shape), _tokens("v", v, device, shape)
+    sizes = _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, shape[1], shape[2], device)
+    _there(device, stream, _append, k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -95,10 +96,14 @@ int check_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int 
 int check_device() {
   const int dev = current_device();
   if (dev < 0) return FA_ERR_NO_DEVICE;
+  // a device found usable stays so: its attributes are asked for once
+  static std::atomic<bool> usable[kMaxDevices];
+  if (usable[dev].load(std::memory_order_relaxed)) return FA_OK;
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return FA_ERR_NO_DEVICE;
   if (cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) return FA_ERR_NO_DEVICE;
   if (major != 10 || minor != 3) return FA_ERR_NO_DEVICE;
+  usable[dev].store(true, std::memory_order_relaxed);
   return FA_OK;
 }
 

@@ -819,7 +819,8 @@ cudaError_t launch_t(const SeqProblem& pb, const void* o, const float* lse, cons
   auto kern = seq_bwd_kernel<D>;
   constexpr int smem = C::kOffCtl + int(sizeof(Ctl));
   static_assert(smem <= 232448, "shared memory of a CTA");
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static seq::SmemLimit limit;
+  cudaError_t e = limit.set(kern, smem);
   if (e != cudaSuccess) return e;
   void* ws = nullptr;
   cudaMemPool_t pool = workspace_pool();

@@ -56,11 +56,14 @@ constexpr float kTau = 8.0f;  // rescale threshold (log2 units), as in the dense
 struct Params {
   __nv_bfloat16* o;
   float* lse;          // [Hq, total_q]
-  const PlanHead* head;
+  PlanHead* head;
   const int* first;
-  const int* last;
-  const FwdItem* items;
-  const Cut* cuts;
+  int* last;
+  const FwdItem* items;  // null: few items, every CTA finds its own (self_plan)
+  Cut* cuts;
+  Lens L;              // for self-planning CTAs
+  FwdSide side;
+  int Hkv, max_units;
   float* part_o;       // [2 G][2 * 128][D] partial O
   float2* part_ml;     // [2 G][2 * 128] their (m, l)
   const int* table;    // paged: [B, max_pages]
@@ -127,7 +130,14 @@ struct Work {
   int fill;     // keys of the last tile if the sequence ends inside it, else 0
 };
 
-struct __align__(8) Ctl {
+// Few items (kFewUnits units at most, no more items than CTAs): the planning
+// kernel would take as long as the work, so the item warp of every CTA lays
+// the work out by itself.
+constexpr int kFewUnits = 160;
+
+struct __align__(16) Ctl {
+  FwdItem unit[kFewUnits];
+  int cost[kFewUnits + 1];  // cost of the units before
   Work it[kItems];
   uint64_t it_full[kItems], it_empty[kItems];
   uint64_t q_full[2], q_empty[2];
@@ -146,19 +156,18 @@ struct __align__(8) Ctl {
   uint32_t abort;
 };
 
-// The laid-out form of the item at `src`.
-__device__ __forceinline__ Work work_of(const Params& p, const FwdItem* src) {
-  const int4 u = reinterpret_cast<const int4*>(src)[0], v = reinterpret_cast<const int4*>(src)[1];
+// The laid-out form of an item: key tiles [kt, kt + nt) of the unit at `src`.
+__device__ __forceinline__ Work work_of(const Params& p, const FwdItem* src, int kvh, int flags, int kt, int nt) {
   Work x;
-  x.q0 = u.x;
-  x.ntok = u.y & 0xffff;
-  x.flags = u.y & ~0xffff;
-  x.kvh = u.z;
-  x.kbase = u.w;
-  x.klen = v.x;
-  x.pos = v.y;
-  x.kt = v.z;
-  x.nt = v.w;
+  x.q0 = src->q0;
+  x.ntok = src->ntok();
+  x.flags = flags;
+  x.kvh = kvh;
+  x.kbase = src->kbase;
+  x.klen = src->klen;
+  x.pos = src->pos;
+  x.kt = kt;
+  x.nt = nt;
   const int end = x.klen & 127;
   x.fill = x.nt > 0 && x.kt + x.nt - 1 == (x.klen - 1) >> 7 ? end : 0;
   if (x.flags & kKeyMode) {
@@ -828,14 +837,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 15) {
     // --------------------------------------------------------- work items
-    Walk wk = walk_begin(p.head, p.first, p.last);
-    for (int i = 0;; ++i) {
-      const bool more = wk.i <= wk.last;
+    int n_done = 0;
+    // hands an item to the other roles (null: there are no more); false when
+    // a wait ran out
+    auto hand_out = [&](const FwdItem* src, int kvh, int flags, int kt, int nt) -> bool {
       Work x;
       x.flags = -1;
-      if (more) {
-        x = work_of(p, p.items + wk.i);
-        walk_step(wk);
+      if (src != nullptr) {
+        x = work_of(p, src, kvh, flags, kt, nt);
         // Its Q and its first K and V tile into L2, a lane to each box: the
         // loads wait for buffers that items before still use, and would then
         // wait for device memory too.
@@ -849,14 +858,116 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      const int i = n_done++;
       const bool ok = wait_bounded(&ctl.it_empty[i % kItems], ((i / kItems) & 1) ^ 1, abort_flag, LIM);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!__all_sync(0xffffffffu, ok)) return false;
       if (lane == 0) {
         ctl.it[i % kItems] = x;
         mbar_arrive(&ctl.it_full[i % kItems]);
       }
-      if (!more) break;
+      return true;
+    };
+    bool ok = true;
+    if (p.items != nullptr) {
+      for (Walk wk = walk_begin(p.head, p.first, p.last); ok && wk.i <= wk.last; walk_step(wk)) {
+        const FwdItem* src = p.items + wk.i;
+        ok = hand_out(src, src->kvh, src->count & ~0xffff, src->kt, src->nt);
+      }
+    } else {
+      // units, 32 sequences at a time
+      int U = 0, bad = 0;
+      for (int b0 = 0; b0 < p.L.B; b0 += 32) {
+        const int b = b0 + lane;
+        Seq q;
+        int n = 0;
+        if (b < p.L.B) {
+          if (seq_at(p.L, b, q)) {
+            n = p.side.units(q);
+          } else {
+            bad = 1;
+          }
+        }
+        int at = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, at, m);
+          if (lane >= m) at += o;
+        }
+        const int sum = __shfl_sync(0xffffffffu, at, 31);
+        at += U - n;
+        for (int j = 0; j < n && at + j < p.max_units; ++j) {
+          const Range r = p.side.range(q, j);
+          FwdItem x = p.side.item(q, b, j, 0, 0);
+          FwdSide::set_range(x, r.first, r.n);
+          ctl.unit[at + j] = x;
+        }
+        U = min(U + sum, p.max_units + 1);
+      }
+      bad = __any_sync(0xffffffffu, bad != 0) || U > p.max_units;
+      if (bad) U = 0;  // lengths that the tensors cannot hold: nothing is computed
+      __syncwarp();
+      int T = 0, most = 0;
+      for (int u0 = 0; u0 < U; u0 += 32) {
+        const int n = u0 + lane < U ? ctl.unit[u0 + lane].nt + kItemCost : 0;
+        int at = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, at, m);
+          if (lane >= m) at += o;
+        }
+        if (u0 + lane < U) ctl.cost[u0 + lane] = T + at - n;
+        T += __shfl_sync(0xffffffffu, at, 31);
+        most = max(most, __reduce_max_sync(0xffffffffu, n));
+      }
+      __syncwarp();
+      // the plan kernel's rule, and its shares, in the order (kv head, unit)
+      const int G = int(gridDim.x), me = int(blockIdx.x), n_items = U * p.Hkv;
+      const long long all = 1LL * T * p.Hkv;
+      const bool split = most > all / G + all / (8 * G) + 6;
+      const long long lo = all * me / G, hi = all * (me + 1) / G;
+      Cut cut;
+      cut.c1 = -1;
+      bool any = false;
+      for (int i0 = 0; ok && i0 < n_items; i0 += 32) {
+        const int i = i0 + lane, kvh = i / U, u = i - kvh * U;
+        const long long x0 = i < n_items ? 1LL * kvh * T + ctl.cost[u] + kItemCost : 0, x1 = i < n_items ? x0 + ctl.unit[u].nt : 0;
+        const bool mine = i < n_items && (!split ? i == me
+                                          : x0 == x1 ? x0 >= lo && (x0 < hi || me == G - 1) : x1 > lo && x0 < hi);
+        for (unsigned left = __ballot_sync(0xffffffffu, mine); ok && left != 0; left &= left - 1) {
+          const int k = i0 + __ffs(left) - 1, kk = k / U, ku = k - kk * U;
+          const FwdItem* src = &ctl.unit[ku];
+          int flags = src->count & ~0xffff, kt = src->kt, nt = src->nt;
+          if (split && nt > 0) {
+            const long long y0 = 1LL * kk * T + ctl.cost[ku] + kItemCost, y1 = y0 + nt;
+            const long long z0 = max(y0, lo), z1 = min(y1, hi);
+            kt += int(z0 - y0);
+            nt = int(z1 - z0);
+            if (z0 > y0 || z1 < y1) flags |= kPart;
+            if (z0 > y0) flags |= kCont;
+            if (z0 == y0 && z1 < y1) {  // the first of a divided unit's parts: its last is in worker c1
+              cut.row0 = src->q0;
+              cut.count = src->ntok();
+              cut.kvh = kk;
+              cut.c0 = me;
+              cut.c1 = me + 1;
+              while (all * (cut.c1 + 1) / G < y1) ++cut.c1;
+            }
+          }
+          any = true;
+          ok = hand_out(src, kk, flags, kt, nt);
+        }
+      }
+      if (lane == 0) {  // for the last kernel
+        if (me + 1 < G) p.cuts[me + 1] = cut;
+        p.last[me] = any ? 0 : -1;
+        if (me == 0) {
+          p.cuts[0].c1 = -1;
+          *p.head = PlanHead{n_items, split ? 1 : 0, bad, 0};
+          if (bad) atomicOr(p.status, kDevBadArg);
+        }
+      }
     }
+    if (ok) hand_out(nullptr, 0, 0, 0, 0);
   }
 
   // ------------------------------------------------------------- teardown
@@ -1008,7 +1119,8 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   p.status = status_word();
   if (p.status == nullptr) return cudaErrorLaunchFailure;
   auto kern = seq_fwd_kernel<D, PAGED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemDyn);
+  static SmemLimit limit;
+  cudaError_t e = limit.set(kern, C::kSmemDyn);
   if (e != cudaSuccess) return e;
   void* ws = nullptr;
   cudaMemPool_t pool = workspace_pool();
@@ -1027,7 +1139,13 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   p.head = sp.plan.head;
   p.first = sp.plan.first;
   p.last = sp.plan.last;
-  p.items = sp.plan.items;
+  p.L = a.L;
+  p.side = a.side;
+  p.Hkv = pb.Hkv;
+  p.max_units = sp.plan.max_units;
+  // few items: 13.6 instead of 10.4 us with the planning kernel (77 tokens, 2 heads)
+  const bool few = p.max_units <= kFewUnits && 1LL * p.max_units * pb.Hkv <= G;
+  p.items = few ? nullptr : sp.plan.items;
   p.cuts = sp.plan.cuts;
   p.part_o = sp.part_o;
   p.part_ml = sp.part_ml;
@@ -1047,8 +1165,10 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   p.wait_limit_ns = dc.wait_limit_ns;
   p.inject = dc.inject;
   p.trace = dc.trace;
-  plan_kernel<FwdSide><<<1, kPlanThreads, 0, stream>>>(a);
-  e = cudaGetLastError();
+  if (!few) {
+    plan_kernel<FwdSide><<<1, kPlanThreads, 0, stream>>>(a);
+    e = cudaGetLastError();
+  }
   // the kernels after it start while the one before ends, and wait for it
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1059,11 +1179,12 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   lc.dynamicSmemBytes = C::kSmemDyn;
   lc.stream = stream;
   lc.attrs = pdl;
-  lc.numAttrs = 1;
+  lc.numAttrs = few ? 0 : 1;
   if (dc.ev_begin) cudaEventRecord(dc.ev_begin, stream);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&lc, kern, mq, mk, mv, mo, p);
   if (dc.ev_end) cudaEventRecord(dc.ev_end, stream);
   if (e == cudaSuccess) {
+    lc.numAttrs = 1;
     lc.gridDim = dim3(G, 8);
     lc.blockDim = dim3(256);
     lc.dynamicSmemBytes = 0;

@@ -18,6 +18,8 @@
 // split. Every unit costs kItemCost products beside its own: Q's load, the
 // first S that nothing overlaps, the epilogue.
 #pragma once
+#include <atomic>
+
 #include "fa_seq.cuh"
 #include "sm103_ptx.cuh"
 
@@ -89,6 +91,23 @@ struct Plan {
   int* order;       // [units] longest first
   Item* items;      // [units * Hkv + G]
   int max_units;
+};
+
+// A kernel's dynamic shared memory limit, set on each device's first launch
+// (one object per kernel).
+struct SmemLimit {
+  std::atomic<bool> done[64] = {};
+  template <class Kernel>
+  cudaError_t set(Kernel kernel, int bytes) {
+    int dev = -1;
+    const cudaError_t g = cudaGetDevice(&dev);
+    if (g != cudaSuccess) return g;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+  }
 };
 
 // Takes pieces of a workspace, 256-byte aligned (base null: sizes alone).
