@@ -928,7 +928,7 @@ cudaError_t launch_t(const SeqProblem& pb, const void* o, const float* lse, cons
   }
   if (dc.ev_end) cudaEventRecord(dc.ev_end, stream);
   if (e == cudaSuccess) {
-    lc.gridDim = dim3(wide);
+    lc.gridDim = dim3(unsigned(8 * G));  // the parts' sums want warps where there are few rows
     lc.blockDim = dim3(256);
     lc.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&lc, seq_post_kernel<D>, static_cast<const float*>(sp.acc), static_cast<const float*>(sp.part),

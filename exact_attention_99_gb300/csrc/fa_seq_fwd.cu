@@ -986,7 +986,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
   grid_dep_wait();
-  if (p.head->n_items == 0 || p.head->split == 0) return;
   const Cut k = p.cuts[blockIdx.x];
   if (k.c1 < 0) return;
   const int lane = threadIdx.x & 31;
@@ -1000,7 +999,11 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
       const int c = c0 + lane;
       const size_t mine = size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * 256 + at;
       float2 ml = make_float2(-INFINITY, 0.0f);
-      if (c <= k.c1 && p.last[c] >= 0) ml = p.part_ml[mine];  // (a worker without a share has no part)
+      if (c <= k.c1) {
+        const bool has = p.last[c] >= 0;  // a worker without a share has no part: what its slot holds is not used
+        const float2 x = p.part_ml[mine];
+        if (has) ml = x;
+      }
       float mn = fmaxf(m, ml.x);
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
@@ -1185,7 +1188,7 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   if (dc.ev_end) cudaEventRecord(dc.ev_end, stream);
   if (e == cudaSuccess) {
     lc.numAttrs = 1;
-    lc.gridDim = dim3(G, 8);
+    lc.gridDim = dim3(G, unsigned(std::max(1LL, std::min(16LL, (1LL * pb.total_q * group + 7) / 8))));
     lc.blockDim = dim3(256);
     lc.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&lc, seq_join_kernel<D>, p);
