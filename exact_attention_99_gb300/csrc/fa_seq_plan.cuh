@@ -446,6 +446,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   }
 }
 
+// Bounded wait of a whole converged warp on an mbarrier phase: true in every
+// lane, or false in every lane when the CTA's abort word is set or limit_ns
+// passed (the abort word is then set here). All lanes take the same way, so
+// the caller may go on with warp-wide instructions either way. Short, since the
+// roles of a kernel, with some fifty waits, share the instruction cache.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                          uint64_t limit_ns) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !__all_sync(0xffffffffu, mbar_try_wait(addr, parity)); ++n) {
+    if ((n & 31) != 0) continue;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    const bool late = t - t0 > limit_ns;
+    if (late) *abort_flag = 1u;
+    if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return false;
+  }
+  return true;
+}
+
 // A worker's walk over its items.
 struct Walk {
   int i, r, last;

@@ -345,6 +345,16 @@ __device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// 1 in one lane of the (converged) warp. A role that the whole warp walks and
+// whose MMAs one elected lane issues keeps descriptors and addresses in
+// uniform registers; walked by one lane alone, each MMA first has to move
+// them there.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Arrive (once) on the mbarrier when all previously issued tcgen05 async
 // operations of this thread have completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
