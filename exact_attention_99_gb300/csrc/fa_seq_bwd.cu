@@ -114,19 +114,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 }
 
 // the next item of this CTA into the warp's shared slot; false at the end
-// (one_lane: the role is run by lane 0 alone)
-template <bool ONE_LANE>
 __device__ __forceinline__ bool next_item(const Params& p, seq::Walk& w, BwdItem* slot, int lane) {
   if (w.i > w.last) return false;
-  if (!ONE_LANE) __syncwarp();  // the previous item has been read
-  if (lane == 0) {
-    const int4* src = reinterpret_cast<const int4*>(p.items + w.i);
-    int4* dst = reinterpret_cast<int4*>(slot);
-    dst[0] = src[0];
-    dst[1] = src[1];
-    dst[2] = src[2];
-  }
-  if (!ONE_LANE) __syncwarp();
+  __syncwarp();  // the previous item has been read
+  if (lane < 3) reinterpret_cast<int4*>(slot)[lane] = reinterpret_cast<const int4*>(p.items + w.i)[lane];
+  __syncwarp();
   seq::walk_step(w);
   return true;
 }
@@ -139,7 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Ctl& ctl = *reinterpret_cast<Ctl*>(smem + C::kOffCtl);
-  const int warp = threadIdx.x >> 5;
+  // (by a shuffle, so that the compiler knows the warp's index to be uniform)
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   const int wg = warp >> 2;
   const uint64_t LIM = p.wait_limit_ns;
@@ -211,15 +204,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ph_s = 0, ph_dp = 0;
     bool ok = true;
     int g = 0;  // step counter across items
-    while (ok && next_item<false>(p, wk, &ctl.cur[warp], lane)) {
+    while (ok && next_item(p, wk, &ctl.cur[warp], lane)) {
       const bool kvalid = row < I.nkey();  // keys past the sequence's end: P = 0
       for (int st = 0; st < I.n && ok; ++st, ++g) {
         const int t0 = (I.i0 + st) * p.tok;  // first token of the row tile
         const int vs = g & 1;
         const float* lse2 = sVec + vs * 256 + c0;
         const float* dlt = sVec + vs * 256 + 128 + c0;
-        if (!mbar_wait_bounded(&ctl.vec_full[vs], (g >> 1) & 1, abort_flag, LIM)) { ok = false; break; }
-        if (!mbar_wait_bounded(&ctl.s_full, ph_s, abort_flag, LIM)) { ok = false; break; }
+        if (!seq::warp_wait(&ctl.vec_full[vs], (g >> 1) & 1, abort_flag, LIM)) { ok = false; break; }
+        if (!seq::warp_wait(&ctl.s_full, ph_s, abort_flag, LIM)) { ok = false; break; }
         ph_s ^= 1;
         tc_fence_after();
         float pv[64];
@@ -272,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ctl.p_full);
 
         // dS^T = P^T o (dP^T - D), 32 columns per TMEM load
-        if (!mbar_wait_bounded(&ctl.dp_full, ph_dp, abort_flag, LIM)) { ok = false; break; }
+        if (!seq::warp_wait(&ctl.dp_full, ph_dp, abort_flag, LIM)) { ok = false; break; }
         ph_dp ^= 1;
         tc_fence_after();
 #pragma unroll
@@ -315,10 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* stg = smem + C::kOffStg + wq * 8192;
     uint32_t ph_dq = 0, nacc = 0;
     bool ok = true;
-    while (ok && next_item<false>(p, wk, &ctl.cur[warp], lane)) {
+    while (ok && next_item(p, wk, &ctl.cur[warp], lane)) {
       for (int st = 0; st < I.n && ok; ++st) {
         const int arow = (I.kvh * p.tile_cap + I.tiles + I.i0 + st) * 128 + wq * 32;  // this warp's accumulator rows
-        if (!mbar_wait_bounded(&ctl.dq_full, ph_dq, abort_flag, LIM)) { ok = false; break; }
+        if (!seq::warp_wait(&ctl.dq_full, ph_dq, abort_flag, LIM)) { ok = false; break; }
         ph_dq ^= 1;
         tc_fence_after();
         // dQ: lane = query row of the tile, column = d. Staged as
@@ -368,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             reinterpret_cast<uint4*>(rows[c & 1] + row_off)[c >> 1] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      if (!mbar_wait_bounded(&ctl.acc_full, nacc & 1, abort_flag, LIM)) { ok = false; break; }
+      if (!seq::warp_wait(&ctl.acc_full, nacc & 1, abort_flag, LIM)) { ok = false; break; }
       ++nacc;
       tc_fence_after();
       const bool part = (I.count & seq::kPart) != 0;
@@ -444,120 +437,134 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 12) {
     // ------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      bool ok = true;
-      int g = 0, nkv = 0;
-      const uint32_t row_bytes = uint32_t(p.tok * p.group * D * 2);
-      while (ok && next_item<true>(p, wk, &ctl.cur[warp], 0)) {
-        if (I.n == 0) continue;
-        if (!mbar_wait_bounded(&ctl.kv_empty, (nkv & 1) ^ 1, abort_flag, LIM)) { ok = false; break; }
-        ++nkv;
+    bool ok = true;
+    int g = 0, nkv = 0;
+    const uint32_t row_bytes = uint32_t(p.tok * p.group * D * 2);
+    while (ok && next_item(p, wk, &ctl.cur[warp], lane)) {
+      const int n = I.n;
+      if (n == 0) continue;
+      ok = seq::warp_wait(&ctl.kv_empty, (nkv & 1) ^ 1, abort_flag, LIM);
+      if (!ok) break;
+      ++nkv;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&ctl.kv_full, 2 * C::kTile);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
           tma_load_4d(sK + c * 16384, &tmK, &ctl.kv_full, c * 64, I.kvh, I.krow, 0);
           tma_load_4d(sV + c * 16384, &tmV, &ctl.kv_full, c * 64, I.kvh, I.krow, 0);
         }
-        for (int st = 0; st < I.n && ok; ++st, ++g) {
-          const int it = I.i0 + st;
-          const int qs = g & 1;
-          if (!mbar_wait_bounded(&ctl.q_empty[qs], ((g >> 1) & 1) ^ 1, abort_flag, LIM)) { ok = false; break; }
+      }
+      const int kvh = I.kvh, token0 = I.q0 + I.i0 * p.tok;
+      const size_t row0 = (size_t(kvh) * p.tile_cap + I.tiles + I.i0) * 128;
+      for (int st = 0; st < n; ++st, ++g) {
+        const int qs = g & 1, token = token0 + st * p.tok;
+        ok = seq::warp_wait(&ctl.q_empty[qs], ((g >> 1) & 1) ^ 1, abort_flag, LIM);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&ctl.q_full[qs], row_bytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sQ + qs * C::kTile + c * 16384, &tmQ, &ctl.q_full[qs], c * 64, 0, I.q0 + it * p.tok, I.kvh);
-          // LSE/D rows before dO: the compute warps need them as soon as S is
-          // ready, while dO (one slot) waits for the previous dV
-          if (!mbar_wait_bounded(&ctl.vec_empty[qs], ((g >> 1) & 1) ^ 1, abort_flag, LIM)) { ok = false; break; }
+            tma_load_4d(sQ + qs * C::kTile + c * 16384, &tmQ, &ctl.q_full[qs], c * 64, 0, token, kvh);
+        }
+        // LSE/D rows before dO: the compute warps need them as soon as S is
+        // ready, while dO (one slot) waits for the previous dV
+        ok = seq::warp_wait(&ctl.vec_empty[qs], ((g >> 1) & 1) ^ 1, abort_flag, LIM);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&ctl.vec_full[qs], 1024);
-          const size_t roff = (size_t(I.kvh) * p.tile_cap + I.tiles + it) * 128;
-          bulk_load(sVec + qs * 256, p.lse2 + roff, 512, &ctl.vec_full[qs]);
-          bulk_load(sVec + qs * 256 + 128, p.delta + roff, 512, &ctl.vec_full[qs]);
-          if (!mbar_wait_bounded(&ctl.do_empty, (g & 1) ^ 1, abort_flag, LIM)) { ok = false; break; }
+          bulk_load(sVec + qs * 256, p.lse2 + row0 + size_t(st) * 128, 512, &ctl.vec_full[qs]);
+          bulk_load(sVec + qs * 256 + 128, p.delta + row0 + size_t(st) * 128, 512, &ctl.vec_full[qs]);
+        }
+        ok = seq::warp_wait(&ctl.do_empty, (g & 1) ^ 1, abort_flag, LIM);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&ctl.do_full, row_bytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(sDO + c * 16384, &tmDO, &ctl.do_full, c * 64, 0, I.q0 + it * p.tok, I.kvh);
+            tma_load_4d(sDO + c * 16384, &tmDO, &ctl.do_full, c * 64, 0, token, kvh);
         }
       }
-      if (*abort_flag) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
-      }
+    }
+    if (*abort_flag) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
   } else if (warp == 13) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idSS = idesc_bf16_f32(128, 128, 0, 0);  // S^T, dP^T
-      constexpr uint32_t idAcc = idesc_bf16_f32(128, D, 0, 1);   // dV, dK
-      constexpr uint32_t idDQ = idesc_bf16_f32(128, D, 1, 1);
-      const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aQ = smem_u32(sQ), aDO = smem_u32(sDO),
-                     aDs = smem_u32(sDs);
-      bool ok = true;
-      uint32_t ph_p = 0, ph_ds = 0, ph_dqe = 0;
-      int g = 0, nkv = 0;
-      const uint32_t kK = sdesc_lo(aK, 16), kV = sdesc_lo(aV, 16), kQ = sdesc_lo(aQ, 16);  // K-major
-      const uint32_t kDO = sdesc_lo(aDO, 16), kDs = sdesc_lo(aDs, 16);
-      const uint32_t mQ = sdesc_lo(aQ, 16384), mDO = sdesc_lo(aDO, 16384);  // MN-major
-      const uint32_t mK = sdesc_lo(aK, 16384), mDs = sdesc_lo(aDs, 16384);
-      auto issue_kmajor = [&](uint32_t d_col, uint32_t a0, uint32_t b0) {  // [128 x 128] = A B^T, K = D
+    // The whole warp walks the role and an elected lane issues.
+    constexpr uint32_t idSS = idesc_bf16_f32(128, 128, 0, 0);  // S^T, dP^T
+    constexpr uint32_t idAcc = idesc_bf16_f32(128, D, 0, 1);   // dV, dK
+    constexpr uint32_t idDQ = idesc_bf16_f32(128, D, 1, 1);
+    const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aQ = smem_u32(sQ), aDO = smem_u32(sDO), aDs = smem_u32(sDs);
+    bool ok = true;
+    uint32_t ph_p = 0, ph_ds = 0, ph_dqe = 0;
+    int g = 0, nkv = 0;
+    const uint32_t kK = sdesc_lo(aK, 16), kV = sdesc_lo(aV, 16), kQ = sdesc_lo(aQ, 16);  // K-major
+    const uint32_t kDO = sdesc_lo(aDO, 16), kDs = sdesc_lo(aDs, 16);
+    const uint32_t mQ = sdesc_lo(aQ, 16384), mDO = sdesc_lo(aDO, 16384);  // MN-major
+    const uint32_t mK = sdesc_lo(aK, 16384), mDs = sdesc_lo(aDs, 16384);
+    auto wait = [&](uint64_t* bar, uint32_t phase) -> bool { return seq::warp_wait(bar, phase, abort_flag, LIM); };
+    // [128 x 128] = A B^T, K = D
+    auto issue_kmajor = [&](uint32_t d_col, uint32_t a0, uint32_t b0, uint64_t* done) {
+      tc_fence_after();
+      if (!elect_one()) return;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ko = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_ss_lo(tmem + d_col, sdesc_step(a0, ko), sdesc_step(b0, ko), idSS, kk > 0);
-        }
-      };
-      // Q of step g (its rows past the sequence's end zeroed, if it has such)
-      auto wait_q = [&](int step, bool tail) -> bool {
-        return mbar_wait_bounded(&ctl.q_full[step & 1], (step >> 1) & 1, abort_flag, LIM) &&
-               (!tail || mbar_wait_bounded(&ctl.q_seen[step & 1], (step >> 1) & 1, abort_flag, LIM));
-      };
-      while (ok && next_item<true>(p, wk, &ctl.cur[warp], 0)) {
-        if (I.n == 0) continue;
-        // the step with rows past the sequence's end, if any
-        const int tail_st = I.qlen % p.tok != 0 ? I.qlen / p.tok - I.i0 : -1;
-        ok = mbar_wait_bounded(&ctl.kv_full, nkv & 1, abort_flag, LIM);
-        if (ok && I.nkey() < 128) ok = mbar_wait_bounded(&ctl.kv_seen, nkv & 1, abort_flag, LIM);
-        if (ok) ok = wait_q(g, tail_st == 0);
-        if (!ok) break;
-        ++nkv;
-        tc_fence_after();
-        issue_kmajor(C::kColS, kK, sdesc_step(kQ, (g & 1) * C::kTile));  // S^T = K Q^T for the item's first step
-        mma_commit(&ctl.s_full);
-        for (int st = 0; st < I.n && ok; ++st, ++g) {
-          const uint32_t mQcur = sdesc_step(mQ, (g & 1) * C::kTile);
-          if (!mbar_wait_bounded(&ctl.do_full, g & 1, abort_flag, LIM)) { ok = false; break; }
-          if (st == tail_st && !mbar_wait_bounded(&ctl.do_seen, g & 1, abort_flag, LIM)) { ok = false; break; }
-          if (g > 0) {
-            if (!mbar_wait_bounded(&ctl.dq_empty, ph_dqe, abort_flag, LIM)) { ok = false; break; }
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t ko = (kk >> 2) * 16384 + (kk & 3) * 32;
+        mma_ss_lo(tmem + d_col, sdesc_step(a0, ko), sdesc_step(b0, ko), idSS, kk > 0);
+      }
+      mma_commit(done);
+    };
+    // Q of a step (its rows past the sequence's end zeroed, if it has such)
+    auto wait_q = [&](int step, bool tail) -> bool {
+      return wait(&ctl.q_full[step & 1], (step >> 1) & 1) && (!tail || wait(&ctl.q_seen[step & 1], (step >> 1) & 1));
+    };
+    while (ok && next_item(p, wk, &ctl.cur[warp], lane)) {
+      const int n = I.n;
+      if (n == 0) continue;
+      // the step with rows past the sequence's end, if any
+      const int tail_st = I.qlen % p.tok != 0 ? I.qlen / p.tok - I.i0 : -1;
+      ok = wait(&ctl.kv_full, nkv & 1) && (I.nkey() == 128 || wait(&ctl.kv_seen, nkv & 1));
+      if (!ok) break;
+      ++nkv;
+      // step st issues S^T of step st + 1; the item begins a step early, with its first S^T alone
+      for (int st = -1; st < n; ++st) {
+        if (st >= 0) {
+          ok = wait(&ctl.do_full, g & 1) && (st != tail_st || wait(&ctl.do_seen, g & 1));
+          if (ok && g > 0) {
+            ok = wait(&ctl.dq_empty, ph_dqe);
             ph_dqe ^= 1;
           }
-          tc_fence_after();
-          issue_kmajor(C::kColDP, kV, kDO);  // dP^T = V dO^T
-          mma_commit(&ctl.dp_full);
-          if (!mbar_wait_bounded(&ctl.p_full, ph_p, abort_flag, LIM)) { ok = false; break; }
+          if (!ok) break;
+          issue_kmajor(C::kColDP, kV, kDO, &ctl.dp_full);  // dP^T = V dO^T
+          ok = wait(&ctl.p_full, ph_p);
           ph_p ^= 1;
           // before the first dV of a later item overwrites the accumulators,
           // the previous item's dK/dV must have been read out of TMEM
-          if (st == 0 && nkv > 1 && !mbar_wait_bounded(&ctl.acc_empty, (nkv - 2) & 1, abort_flag, LIM)) {
-            ok = false;
-            break;
-          }
+          if (ok && st == 0 && nkv > 1) ok = wait(&ctl.acc_empty, (nkv - 2) & 1);
+          if (!ok) break;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)  // dV += P^T dO   (P^T in TMEM, dO MN-major)
-            mma_ts_lo(tmem + C::kColDV, tmem + C::kColS + kk * 8, sdesc_step(mDO, kk * 2048), idAcc,
-                      (st > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&ctl.do_empty);
-          if (st + 1 < I.n) {
-            if (!wait_q(g + 1, st + 1 == tail_st)) { ok = false; break; }
-            tc_fence_after();
-            issue_kmajor(C::kColS, kK, sdesc_step(kQ, ((g + 1) & 1) * C::kTile));  // S^T for the next step
-            mma_commit(&ctl.s_full);
+            for (int kk = 0; kk < 8; ++kk)  // dV += P^T dO   (P^T in TMEM, dO MN-major)
+              mma_ts_lo(tmem + C::kColDV, tmem + C::kColS + kk * 8, sdesc_step(mDO, kk * 2048), idAcc,
+                        (st > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&ctl.do_empty);
           }
-          if (!mbar_wait_bounded(&ctl.ds_full, ph_ds, abort_flag, LIM)) { ok = false; break; }
-          ph_ds ^= 1;
-          tc_fence_after();
+        }
+        if (st + 1 < n) {
+          const int nx = st < 0 ? g : g + 1;
+          ok = wait_q(nx, st + 1 == tail_st);
+          if (!ok) break;
+          issue_kmajor(C::kColS, kK, sdesc_step(kQ, (nx & 1) * C::kTile), &ctl.s_full);  // S^T = K Q^T
+        }
+        if (st < 0) continue;
+        ok = wait(&ctl.ds_full, ph_ds);
+        ph_ds ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t mQcur = sdesc_step(mQ, (g & 1) * C::kTile);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {  // dK += dS^T Q   (dS^T K-major, Q MN-major)
             const uint32_t ko = (kk >> 2) * 16384 + (kk & 3) * 32;
@@ -569,17 +576,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < 8; ++kk)  // dQ = dS K  (both MN-major): lane = query row, column = d
             mma_ss_lo(tmem + C::kColDP, sdesc_step(mDs, kk * 2048), sdesc_step(mK, kk * 2048), idDQ, kk > 0);
           mma_commit(&ctl.dq_full);
+          if (st + 1 == n) {
+            mma_commit(&ctl.acc_full);  // dK, dV of this item are complete
+            mma_commit(&ctl.kv_empty);  // K, V of this item no longer read
+          }
         }
-        if (!ok) break;
-        mma_commit(&ctl.acc_full);  // dK, dV of this item are complete
-        mma_commit(&ctl.kv_empty);  // K, V of this item no longer read
+        ++g;
       }
-      if (*abort_flag) {
-        mma_commit(&ctl.drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer_ns() - t0 < 100000000ull) {
-        }
+    }
+    if (*abort_flag) {
+      if (elect_one()) mma_commit(&ctl.drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer_ns() - t0 < 100000000ull) {
       }
+      __syncwarp();
     }
   } else if (warp == 14) {
     // ----------------------------------------------------------- tail rows
@@ -591,9 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) *reinterpret_cast<uint4*>(tile + c * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
     };
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, LIM));
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return seq::warp_wait(bar, parity, abort_flag, LIM); };
     auto done = [&](uint64_t* seen, uint64_t* empty) {
       __syncwarp();
       if (lane == 0) {
@@ -603,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     int g = 0, nkv = 0;
-    while (ok && next_item<false>(p, wk, &ctl.cur[warp], lane)) {
+    while (ok && next_item(p, wk, &ctl.cur[warp], lane)) {
       if (I.n == 0) continue;
       ok = wait(&ctl.kv_full, nkv & 1);
       if (!ok) break;
