@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(256)
                        pack_bf16x2(v[i][1].x * scale, v[i][1].y * scale), pack_bf16x2(v[i][1].z * scale, v[i][1].w * scale));
     }
   }
-  if (head->split == 0) return;
+  if (head->step != 1) return;  // no unit is divided
   // a warp pass: RPP rows of one cut's dV or dK
   const long long n_pass = 1LL * G * 2 * (128 / RPP);
   for (long long i = warp; i < n_pass; i += n_warps) {

@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the plan kernel's rule, and its shares, in the order (kv head, unit)
       const int G = int(gridDim.x), me = int(blockIdx.x), n_items = U * p.Hkv;
       const long long all = 1LL * T * p.Hkv;
-      const bool split = most > all / G + all / (8 * G) + 6;
+      const bool split = most > all / G * FwdSide::kSplitGain / 8 + 6;
       const long long lo = all * me / G, hi = all * (me + 1) / G;
       Cut cut;
       cut.c1 = -1;
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         p.last[me] = any ? 0 : -1;
         if (me == 0) {
           p.cuts[0].c1 = -1;
-          *p.head = PlanHead{n_items, split ? 1 : 0, bad, 0};
+          *p.head = PlanHead{n_items, 1, bad, 0};
           if (bad) atomicOr(p.status, kDevBadArg);
         }
       }

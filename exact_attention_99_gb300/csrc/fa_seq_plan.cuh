@@ -8,7 +8,8 @@
 // (row = token * group + head), so that they share the key tiles.
 //
 // Two divisions, whichever promises the earlier end:
-//   sorted: the units by n, longest first, over the CTAs in snake order;
+//   sorted: the units by n, longest first, in rounds of one to each CTA, in
+//           each round the longest to the CTA that has least so far;
 //   split : all tile products laid end to end (sequence, kv head, unit), an
 //           equal share to each CTA. A unit that a boundary falls into is
 //           done in parts, and a last kernel joins them in the CTAs' order.
@@ -73,8 +74,8 @@ struct Cut {
 };
 
 struct PlanHead {
-  int n_items;  // sorted: worker c takes items c, 2G-1-c, 2G+c, ...
-  int split;    // 1: worker c takes items [first[c], last[c]] instead
+  int n_items;
+  int step;     // worker c takes items first[c], first[c] + step, ... up to last[c]
   int bad;      // the lengths say something that the tensors cannot hold
   int pad;
 };
@@ -145,6 +146,10 @@ struct Range {
 
 struct FwdSide {
   using Item = FwdItem;
+  // One causal sequence of 16384 tokens (32 query heads, 8 kv heads) took 6 %
+  // longer split, packed prompts of 16 to 4096 tokens 44 % (at 2 % less in the count).
+  static constexpr int kSplitGain = 9;
+  static constexpr int kRanked = 2;  // many units of few tiles: back and forth is even enough
   int tok, wl, wr, paged;
   __device__ __forceinline__ int units(const Seq& s) const { return (s.qlen + 2 * tok - 1) / (2 * tok); }
   __device__ __forceinline__ int row_tiles(const Seq&) const { return 0; }
@@ -176,6 +181,12 @@ struct FwdSide {
 
 struct BwdSide {
   using Item = BwdItem;
+  // Split, the CTAs of a sequence add into dQ rows far apart: one causal
+  // sequence of 16384 tokens took 5.8 instead of 3.9 ms.
+  static constexpr int kSplitGain = 12;
+  // Units of many tiles: the documents of a packed training step are 6 % from
+  // even back and forth, 1 % ranked (step 1.68 -> 1.53 ms).
+  static constexpr int kRanked = 12;
   int tok, wl, wr;
   __device__ __forceinline__ int units(const Seq& s) const { return (s.klen + 127) >> 7; }
   __device__ __forceinline__ int row_tiles(const Seq& s) const { return (s.qlen + tok - 1) / tok; }
@@ -215,7 +226,7 @@ struct PlanArgs {
 };
 
 // inclusive scan over the block (kPlanThreads threads); total in `sum`
-__device__ __forceinline__ long long block_scan(long long v, long long* warp_sums, long long& sum) {
+static __device__ __noinline__ long long block_scan(long long v, long long* warp_sums, long long& sum) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
@@ -255,7 +266,7 @@ __device__ __forceinline__ int find_seq(const int* start, int B, int scale, int 
 
 // What the planning block keeps at hand; larger batches than that are read
 // from device memory.
-constexpr int kNearSeqs = 512, kNearUnits = 2048;
+constexpr int kNearSeqs = 512, kNearUnits = 1024;
 
 template <class Side>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side> a) {
@@ -267,8 +278,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   __shared__ int near_ustart[kNearSeqs + 1];
   __shared__ long long near_cost[kNearUnits + 1];
   __shared__ int near_order[kNearUnits];
+  __shared__ __align__(16) unsigned load[kMaxWorkers];
+  __shared__ int rank[kMaxWorkers], taken[Side::kRanked * kMaxWorkers];
   __shared__ unsigned long long worst;
   __shared__ int bad;
+  // (no loop is unrolled: the kernel runs once per call, and fetching its code
+  // takes longer than most of what it does)
   const int tid = threadIdx.x;
   const int B = a.L.B, G = a.G, Hkv = a.Hkv;
   const Plan<Item>& P = a.P;
@@ -287,16 +302,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     bad = 0;
     worst = 0;
   }
+#pragma unroll 1
   for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+#pragma unroll 1
   for (int c = tid; c < G; c += kPlanThreads) {
     P.first[c] = 0x7fffffff;
     P.last[c] = -1;
     P.cuts[c].c1 = -1;
   }
+#pragma unroll 1
+  for (int c = tid; c < kMaxWorkers; c += kPlanThreads) rank[c] = 0;
   grid_dep_launch();  // the next kernel may start its set-up meanwhile
   __syncthreads();
   // units (low half) and row tiles (high half) of the sequences before each
   long long n_units = 0, sum;
+#pragma unroll 1
   for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     long long n = 0;
@@ -321,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   // by their sum): nothing is computed
   if (bad || (n_units & 0xffffffffll) > P.max_units) {
     if (tid == 0) {
-      *P.head = PlanHead{0, 0, 1, 0};
+      *P.head = PlanHead{0, 1, 1, 0};
       atomicOr(a.status, kDevBadArg);
     }
     return;
@@ -336,6 +356,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   __syncthreads();
   // n of each unit: running sum and histogram
   long long T = 0;
+#pragma unroll 1
   for (int u0 = 0; u0 < U; u0 += kPlanThreads) {
     const int u = u0 + tid;
     int n = 0;
@@ -351,10 +372,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   }
   if (tid == 0) cost[U] = T;
   const long long Ttot = T * Hkv;
+#pragma unroll 1
   for (int c = tid; c <= G; c += kPlanThreads) share[c] = Ttot * c / G;
   __syncthreads();
   // sorted order (arbitrary within a bucket, which changes no result)
   long long base = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < kBuckets; i0 += kPlanThreads) {
     const int n = hist[i0 + tid];
     const long long end = block_scan(n, sums, sum) + base;
@@ -362,43 +385,89 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     base += sum;
   }
   __syncthreads();
+#pragma unroll 1
   for (int u = tid; u < U; u += kPlanThreads) {
     const int n = int(cost[u + 1] - cost[u]) - kItemCost;
     order[atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1)] = u;
   }
   __syncthreads();
-  // The busiest worker in sorted order against an equal division, which has
-  // to win by more than what the parts' stores and the last kernel cost (6
-  // products) and what CTAs at different keys cost: one causal sequence of
-  // 16384 tokens (32 query heads, 8 kv heads) took 1.80 ms sorted and 1.91 ms
-  // split at 1 % less imbalance; packed prompts 0.41 and 0.59 ms.
   const int n_items = U * Hkv;
-  for (int c = tid; c < G; c += kPlanThreads) {
-    unsigned long long t = 0;
-    for (int r = 0; r * G < n_items; ++r) {
-      const int i = r * G + ((r & 1) ? G - 1 - c : c);
-      if (i < n_items) {
-        const int u = order[i / Hkv];
-        t += cost[u + 1] - cost[u];
-      }
-    }
-    atomicMax(&worst, t);
+  auto cost_of = [&](int i) {
+    const int u = order[i / Hkv];
+    return int(cost[u + 1] - cost[u]);
+  };
+  // Rounds of G items, worker c's at place r * G + c. The last Side::kRanked rounds
+  // rank the workers by their load; rounds before them, which leave enough to
+  // even out, go back and forth over the workers.
+  const int rounds = (n_items + G - 1) / G, early = max(0, rounds - Side::kRanked);
+  int mine = tid < G && early > 0 ? tid + (early - 1) * G : -1;  // worker tid's last place
+  int own = 0;  // worker tid's load
+  auto publish = [&]() {  // as a key that orders equal loads by worker
+    load[tid] = tid < G ? (unsigned(min(own, 0x7ffffe)) << 8) | unsigned(tid) : 0xffffffffu;
+  };
+  if (tid < kMaxWorkers) {
+    if (tid < G)
+#pragma unroll 1
+      for (int r = 0; r < early; ++r) own += cost_of(r * G + ((r & 1) ? G - 1 - tid : tid));
+    publish();
   }
   __syncthreads();
-  const bool split = static_cast<long long>(worst) > Ttot / G + Ttot / (8 * G) + 6;
-  if (tid == 0) *P.head = PlanHead{n_items, split ? 1 : 0, 0, 0};
+  // thread (c, part): how many of the part's workers come before worker c
+  const int wide = (G + 31) & ~31, parts = kPlanThreads / wide, per_part = ((G + parts - 1) / parts + 3) & ~3;
+  const int c = tid % wide, c0 = tid / wide * per_part, c1 = min(c0 + per_part, kMaxWorkers);
+#pragma unroll 1
+  for (int r = early; r < rounds; ++r) {
+    if (c < G && c0 < G) {
+      const unsigned key = load[c];
+      int before = 0;
+#pragma unroll 1
+      for (int x = c0; x < c1; x += 4) {
+        const uint4 y = *reinterpret_cast<const uint4*>(&load[x]);
+        before += (y.x < key) + (y.y < key) + (y.z < key) + (y.w < key);
+      }
+      if (before > 0) atomicAdd(&rank[c], before);
+    }
+    __syncthreads();
+    if (tid < G) {
+      const int i = r * G + rank[tid];
+      rank[tid] = 0;
+      taken[(r - early) * kMaxWorkers + tid] = i;
+      if (i < n_items) {
+        mine = r * G + tid;
+        own += cost_of(i);
+        publish();
+      }
+    }
+    __syncthreads();
+  }
+  // The busiest worker against an equal division, which has to win by more
+  // than what the parts' stores and the last kernel cost (6 products) and what
+  // CTAs at different places cost (Side::kSplitGain, in eighths).
+  if (tid < G) atomicMax(&worst, static_cast<unsigned long long>(own));
+  __syncthreads();
+  const bool split = static_cast<long long>(worst) > Ttot / G * Side::kSplitGain / 8 + 6;
+  if (tid == 0) *P.head = PlanHead{n_items, split ? 1 : G, 0, 0};
   if (!split) {
-    for (int i = tid; i < n_items; i += kPlanThreads) {
+    if (tid < G) {
+      P.first[tid] = tid;
+      P.last[tid] = mine;
+    }
+#pragma unroll 1
+    for (int at = tid; at < rounds * G; at += kPlanThreads) {
+      const int r = at / G, c = at - r * G;
+      const int i = r < early ? r * G + ((r & 1) ? G - 1 - c : c) : taken[(r - early) * kMaxWorkers + c];
+      if (i >= n_items) continue;
       const int u = order[i / Hkv], b = find_seq(ustart, B, 1, u);
       const Seq s = seq_of(b);
-      const Range r = a.side.range(s, u - ustart[b]);
+      const Range x = a.side.range(s, u - ustart[b]);
       Item it = a.side.item(s, b, u - ustart[b], i % Hkv, P.tstart[b]);
-      Side::set_range(it, r.first, r.n);
-      P.items[i] = it;
+      Side::set_range(it, x.first, x.n);
+      P.items[at] = it;
     }
     return;
   }
   const float per_worker = float(G) / float(Ttot);
+#pragma unroll 1
   for (int i = tid; i < n_items; i += kPlanThreads) {
     // order (sequence, kv head, unit): the place [x0, x1) of item i's products
     // among all costs; worker c has those in [share(c), share(c + 1))
@@ -466,27 +535,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
-// A worker's walk over its items.
+// A worker's walk over its items: i, i + step, ... up to last.
 struct Walk {
-  int i, r, last;
-  bool split;
+  int i, step, last;
 };
 __device__ __forceinline__ Walk walk_begin(const PlanHead* head, const int* first, const int* last) {
-  Walk w;
-  w.split = head->split != 0;
-  w.r = 0;
-  w.i = w.split ? first[blockIdx.x] : int(blockIdx.x);
-  w.last = w.split ? last[blockIdx.x] : head->n_items - 1;
-  return w;
+  return Walk{first[blockIdx.x], head->step, last[blockIdx.x]};
 }
-__device__ __forceinline__ void walk_step(Walk& w) {
-  if (w.split) {
-    ++w.i;
-  } else {
-    ++w.r;
-    w.i = w.r * int(gridDim.x) + ((w.r & 1) ? int(gridDim.x) - 1 - int(blockIdx.x) : int(blockIdx.x));
-  }
-}
+__device__ __forceinline__ void walk_step(Walk& w) { w.i += w.step; }
 
 #endif  // __CUDACC__
 
