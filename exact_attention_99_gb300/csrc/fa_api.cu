@@ -96,6 +96,13 @@ int check_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int 
 int check_device() {
   const int dev = current_device();
   if (dev < 0) return FA_ERR_NO_DEVICE;
+  // a thread's first call may come before anything made the device's context
+  // current in it, and the tensor maps are encoded by the driver
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return FA_ERR_NO_DEVICE;
+    bound = dev;
+  }
   // a device found usable stays so: its attributes are asked for once
   static std::atomic<bool> usable[kMaxDevices];
   if (usable[dev].load(std::memory_order_relaxed)) return FA_OK;
