@@ -56,7 +56,7 @@ constexpr float kTau = 8.0f;  // rescale threshold (log2 units), as in the dense
 struct Params {
   __nv_bfloat16* o;
   float* lse;          // [Hq, total_q]
-  PlanHead* head;
+  const PlanHead* head;
   const int* first;
   int* last;
   const FwdItem* items;  // null: few items, every CTA finds its own (self_plan)
@@ -113,7 +113,8 @@ struct Work {
 
 // Few items (kFewUnits units at most, no more items than CTAs): the planning
 // kernel would take as long as the work, so the item warp of every CTA lays
-// the work out by itself.
+// the work out by itself (77 tokens, 2 heads: 13.7 -> 10.1 us; one token of 32
+// heads over 1000 keys: 22 -> 15 us).
 constexpr int kFewUnits = 160;
 
 struct __align__(16) Ctl {
@@ -915,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the plan kernel's rule, and its shares, in the order (kv head, unit)
       const int G = int(gridDim.x), me = int(blockIdx.x), n_items = U * p.Hkv;
       const long long all = 1LL * T * p.Hkv;
-      const bool split = most > all / G * FwdSide::kSplitGain / 8 + 6;
+      const bool split = most > all / G * FwdSide::kSplitGain / 8 + kPartsCost;
       const long long lo = all * me / G, hi = all * (me + 1) / G;
       Cut cut;
       cut.c1 = -1;
@@ -949,14 +950,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = hand_out(src, kk, flags, kt, nt);
         }
       }
-      if (lane == 0) {  // for the last kernel
-        if (me + 1 < G) p.cuts[me + 1] = cut;
-        p.last[me] = any ? 0 : -1;
-        if (me == 0) {
-          p.cuts[0].c1 = -1;
-          *p.head = PlanHead{n_items, 1, bad, 0};
-          if (bad) atomicOr(p.status, kDevBadArg);
+      if (lane == 0) {
+        if (p.cuts != nullptr) {  // for the last kernel
+          if (me + 1 < G) p.cuts[me + 1] = cut;
+          p.last[me] = any ? 0 : -1;
+          if (me == 0) p.cuts[0].c1 = -1;
         }
+        if (me == 0 && bad) atomicOr(p.status, kDevBadArg);
       }
     }
     if (ok) hand_out(nullptr, 0, 0, 0, 0);
@@ -1052,12 +1052,9 @@ struct Space {
   float2* part_ml;
   size_t bytes;
 };
-Space carve(uint8_t* base, const SeqProblem& pb, int G, int tok) {
+Space carve(uint8_t* base, const SeqProblem& pb, int G, long long units) {
   Space s{};
   Carver c{base, 0};
-  // a sequence of n tokens has ceil(n / (2 tok)) units
-  long long units = pb.total_q / (2 * tok) + pb.B;
-  if (units > pb.total_q) units = pb.total_q;
   s.plan = carve_plan<FwdItem>(c, pb.B, units, pb.Hkv, G);
   s.part_ml = c.take<float2>(size_t(2) * G * 256);
   s.part_o = c.take<float>(size_t(2) * G * 256 * pb.d);
@@ -1117,11 +1114,23 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   static SmemLimit limit;
   cudaError_t e = limit.set(kern, C::kSmemDyn);
   if (e != cudaSuccess) return e;
+  // a sequence of n tokens has ceil(n / (2 tok)) units
+  long long units = pb.total_q / (2 * tok) + pb.B;
+  if (units > pb.total_q) units = pb.total_q;
+  const bool few = units <= kFewUnits && units * pb.Hkv <= G;
+  // Few items of few key tiles are never divided: no workspace, no last kernel.
+  long long keys = pb.page_table != nullptr ? 1LL * pb.max_pages * pb.page_size : pb.total_k;
+  if (pb.window_left >= 0 && pb.window_right >= 0)  // and whole tiles around those that a unit sees
+    keys = std::min(keys, 2LL * tok + pb.window_left + pb.window_right + 254);
+  const bool whole = few && (keys + 127) / 128 + kItemCost <= kPartsCost;
   void* ws = nullptr;
-  cudaMemPool_t pool = workspace_pool();
-  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr, pb, G, tok).bytes, pool, stream) != cudaSuccess)
-    return cudaErrorMemoryAllocation;
-  const Space sp = carve(static_cast<uint8_t*>(ws), pb, G, tok);
+  Space sp{};
+  if (!whole) {
+    cudaMemPool_t pool = workspace_pool();
+    if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr, pb, G, units).bytes, pool, stream) != cudaSuccess)
+      return cudaErrorMemoryAllocation;
+    sp = carve(static_cast<uint8_t*>(ws), pb, G, units);
+  }
   PlanArgs<FwdSide> a{};
   a.L = Lens{pb.cu_q, pb.cu_k, pb.lens_k, pb.B, pb.total_q, pb.total_k, 1LL * pb.max_pages * pb.page_size};
   a.P = sp.plan;
@@ -1137,9 +1146,7 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   p.L = a.L;
   p.side = a.side;
   p.Hkv = pb.Hkv;
-  p.max_units = sp.plan.max_units;
-  // few items: 13.6 instead of 10.4 us with the planning kernel (77 tokens, 2 heads)
-  const bool few = p.max_units <= kFewUnits && 1LL * p.max_units * pb.Hkv <= G;
+  p.max_units = int(units);
   p.items = few ? nullptr : sp.plan.items;
   p.cuts = sp.plan.cuts;
   p.part_o = sp.part_o;
@@ -1178,14 +1185,14 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   if (dc.ev_begin) cudaEventRecord(dc.ev_begin, stream);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&lc, kern, mq, mk, mv, mo, p);
   if (dc.ev_end) cudaEventRecord(dc.ev_end, stream);
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && !whole) {
     lc.numAttrs = 1;
     lc.gridDim = dim3(G, unsigned(std::max(1LL, std::min(16LL, (1LL * pb.total_q * group + 7) / 8))));
     lc.blockDim = dim3(256);
     lc.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&lc, seq_join_kernel<D>, p);
   }
-  const cudaError_t f = cudaFreeAsync(ws, stream);
+  const cudaError_t f = whole ? cudaSuccess : cudaFreeAsync(ws, stream);
   return e != cudaSuccess ? e : f;
 }
 

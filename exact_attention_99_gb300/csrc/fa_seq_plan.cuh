@@ -31,6 +31,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;    // of the sort by n; units of more tiles sort as equal
 constexpr int kMaxWorkers = 256;  // CTAs of a main kernel
 constexpr int kItemCost = 2;
+constexpr int kPartsCost = 6;  // of divided units: the parts' stores and the last kernel, in tile products
 
 // An item is a unit, or a part of one, for one kv head.
 struct __align__(16) FwdItem {
@@ -441,11 +442,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     __syncthreads();
   }
   // The busiest worker against an equal division, which has to win by more
-  // than what the parts' stores and the last kernel cost (6 products) and what
-  // CTAs at different places cost (Side::kSplitGain, in eighths).
+  // than kPartsCost and what CTAs at different places cost (Side::kSplitGain, in
+  // eighths).
   if (tid < G) atomicMax(&worst, static_cast<unsigned long long>(own));
   __syncthreads();
-  const bool split = static_cast<long long>(worst) > Ttot / G * Side::kSplitGain / 8 + 6;
+  const bool split = static_cast<long long>(worst) > Ttot / G * Side::kSplitGain / 8 + kPartsCost;
   if (tid == 0) *P.head = PlanHead{n_items, split ? 1 : G, 0, 0};
   if (!split) {
     if (tid < G) {

@@ -245,8 +245,10 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *              bits; v rows that only the window hides must be finite.
  *   Sizes    : B >= 1, total_q, total_k >= 0 (0: nothing, or no keys at all),
  *              Hq % Hkv == 0, Hq / Hkv <= 128, d in {64, 128}, any finite scale.
- *   Workspace: from the per-device pool that fa_bwd uses, on `stream` (about
- *              1 KB per SM and row of a tile: 80 MB at d = 128).
+ *   Workspace: from the per-device pool that fa_bwd uses, on `stream`: 40 MB
+ *              at d = 128 and 20 MB at d = 64 for the parts of divided work, and
+ *              about 40 bytes per block of 128 rows and kv head for the plan.
+ *              The smallest calls need none.
  *   Errors   : as above for what the host can see. Lengths or pages on the
  *              device that the tensors cannot hold set FA_ERR_INVALID_ARG in the
  *              status word (fa_get_status); bad lengths: the outputs stay as
@@ -271,7 +273,7 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
  *        rows of every sequence; other rows are left as they are.
  * dk and dv are sums over the query heads of a group, taken in a fixed order;
  * the additions into dq are not ordered (as in fa_bwd). Workspace: fp32 dQ
- * (about 4 * total_q * Hq * d bytes) and 80 MB at d = 128.
+ * (about 4 * total_q * Hq * d bytes) and 40 MB at d = 128 for parts.
  */
 int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
                   void* dq, void* dk, void* dv, const int* cu_q, const int* cu_k, int B, int Hq, int Hkv, int total_q,
