@@ -340,8 +340,8 @@ def _types():
 
 def _tokens(name, t, device, shape):
     """Checks a packed [total, H, d] tensor; returns its elements between tokens."""
-    if t.dtype != _bf16 or t.shape != shape or t.device != device:
-        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on {device}")
+    if t.dtype != _bf16 or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be a bf16 tensor of shape {tuple(shape)} on cuda:{device}")
     n, h, d = shape
     s0, s1, s2 = t.stride()
     if n <= 1:  # the stride of an axis of one has no meaning
@@ -352,22 +352,22 @@ def _tokens(name, t, device, shape):
 
 
 def _first(name, t):
-    """The device of a call's first tensor, after a check of its form."""
+    """The device index of a call's first tensor, after a check of its form."""
     if _bf16 is None:
         _types()
     if t.dim() != 3 or not t.is_cuda or t.shape[1] < 1:
         raise ValueError(f"{name} must be a CUDA bf16 tensor of shape [tokens, heads, d]")
-    return t.device
+    return t.get_device()
 
 
 def _ints(name, t, shape, device):
-    if t.dtype != _i32 or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+    if t.dtype != _i32 or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{device}")
 
 
 def _packed(name, t, shape, device, dtype=None):
-    if t.shape != shape or t.dtype != (dtype or _bf16) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype or _bf16} tensor of shape {tuple(shape)} on {device}")
+    if t.shape != shape or t.dtype != (dtype or _bf16) or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous {dtype or _bf16} tensor of shape {tuple(shape)} on cuda:{device}")
 
 
 def _pages(k_pages, v_pages, hkv, d, device):
@@ -387,11 +387,11 @@ class _on:
     def __init__(self, device, stream):
         import torch
         self.guards = []
-        if device.index != torch.cuda.current_device():
+        if device != torch.cuda.current_device():
             self.guards.append(torch.cuda.device(device))
         if stream is not None:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
+                stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", device))
             self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
@@ -403,15 +403,12 @@ class _on:
             g.__exit__(*exc)
 
 
-def _there(device, stream, call, *args):
-    """call(stream handle, *args) where the tensors are: at once on the current
-    device and stream, else with those made current."""
-    if stream is None:
-        here = _current_stream()
-        if device.index == _get_device():
-            return call(here, *args)
-    with _on(device, stream):
-        return call(_current_stream(), *args)
+def _here(device, stream):
+    """The current stream's handle if the call may be made as things are: its
+    tensors on the current device and no other stream asked for. Else None."""
+    if _raw_stream is None:
+        _current_stream()
+    return _raw_stream(device) if stream is None and device == _get_device() else None
 
 
 def _seq_out(q, shape, out):
@@ -420,8 +417,8 @@ def _seq_out(q, shape, out):
     if out is None:
         return _empty(shape, dtype=_bf16, device=q.device), _empty((hq, total), dtype=_f32, device=q.device)
     o, lse = out
-    _packed("o", o, shape, q.device)
-    _packed("lse", lse, (hq, total), q.device, _f32)
+    _packed("o", o, shape, q.get_device())
+    _packed("lse", lse, (hq, total), q.get_device(), _f32)
     return o, lse
 
 
@@ -461,8 +458,12 @@ def forward_varlen(q, k, v, cu_q, cu_k, causal: bool = False, scale: float | Non
     Rows outside every sequence are left as they are (unset in new outputs)."""
     device, shape, kshape, strides = _varlen_args(q, k, v, cu_q, cu_k)
     scale = 1.0 / math.sqrt(shape[2]) if scale is None else scale
-    return _there(device, stream, _fwd_varlen, q, k, v, cu_q, cu_k, out, shape, kshape, strides, scale,
-                  *_window_args(causal, window))
+    wl, wr = (-1, 0 if causal else -1) if window is None else _window_args(causal, window)
+    s = _here(device, stream)
+    if s is not None:
+        return _fwd_varlen(s, q, k, v, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr)
+    with _on(device, stream):
+        return _fwd_varlen(_current_stream(), q, k, v, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr)
 
 
 def _bwd_varlen(stream, q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr):
@@ -472,9 +473,10 @@ def _bwd_varlen(stream, q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, s
         dq, dk, dv = (_empty(x, dtype=_bf16, device=q.device) for x in (shape, kshape, kshape))
     else:
         dq, dk, dv = out
-        _packed("dq", dq, shape, q.device)
-        _packed("dk", dk, kshape, q.device)
-        _packed("dv", dv, kshape, q.device)
+        device = q.get_device()
+        _packed("dq", dq, shape, device)
+        _packed("dk", dk, kshape, device)
+        _packed("dv", dv, kshape, device)
     st = lib().fa_bwd_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(),
                              cu_q.shape[0] - 1, hq, hkv, total_q, total_k, d, *strides, scale, wl, wr, stream)
@@ -492,8 +494,12 @@ def backward_varlen(q, k, v, o, lse, dout, cu_q, cu_k, causal: bool = False, sca
     _seq_out(q, shape, (o, lse))
     _packed("dout", dout, shape, device)
     scale = 1.0 / math.sqrt(shape[2]) if scale is None else scale
-    return _there(device, stream, _bwd_varlen, q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, strides, scale,
-                  *_window_args(causal, window))
+    wl, wr = (-1, 0 if causal else -1) if window is None else _window_args(causal, window)
+    s = _here(device, stream)
+    if s is not None:
+        return _bwd_varlen(s, q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr)
+    with _on(device, stream):
+        return _bwd_varlen(_current_stream(), q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr)
 
 
 def _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, d, device):
@@ -533,8 +539,13 @@ def forward_paged(q, k_pages, v_pages, cu_q, lens_k, page_table, causal: bool = 
     hkv = k_pages.shape[2] if k_pages.dim() == 4 else 0
     sizes = _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, shape[2], device)
     scale = 1.0 / math.sqrt(shape[2]) if scale is None else scale
-    return _there(device, stream, _fwd_paged, q, k_pages, v_pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes,
-                  scale, *_window_args(causal, window))
+    wl, wr = (-1, 0 if causal else -1) if window is None else _window_args(causal, window)
+    s = _here(device, stream)
+    if s is not None:
+        return _fwd_paged(s, q, k_pages, v_pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes, scale, wl, wr)
+    with _on(device, stream):
+        return _fwd_paged(_current_stream(), q, k_pages, v_pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes,
+                          scale, wl, wr)
 
 
 def _append(stream, k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes):
@@ -555,4 +566,8 @@ def cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, stream=None) 
     shape = k.shape
     ks, vs = _tokens("k", k, device, shape), _tokens("v", v, device, shape)
     sizes = _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, shape[1], shape[2], device)
-    _there(device, stream, _append, k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)
+    s = _here(device, stream)
+    if s is not None:
+        return _append(s, k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)
+    with _on(device, stream):
+        _append(_current_stream(), k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)
