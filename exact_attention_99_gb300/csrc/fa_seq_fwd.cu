@@ -111,11 +111,14 @@ struct Work {
   int fill;     // keys of the last tile if the sequence ends inside it, else 0
 };
 
-// Few items (kFewUnits units at most, no more items than CTAs): the planning
-// kernel would take as long as the work, so the item warp of every CTA lays
-// the work out by itself (77 tokens, 2 heads: 13.7 -> 10.1 us; one token of 32
-// heads over 1000 keys: 22 -> 15 us).
-constexpr int kFewUnits = 160;
+// Few items: the planning kernel would take a good part of the call, so the
+// item warp of every CTA lays the work out by itself (77 tokens, 2 heads: 13.7
+// -> 10.1 us; one token of 32 heads over 1000 keys: 22 -> 15 us). Few are
+// kFewUnits units and no more items than CTAs, or, over a paged cache,
+// kFewRounds times as many, which are then always divided: sorting wants the
+// planning kernel, and gains where there are many units of as many keys as
+// rows (prompts), not where rows are few.
+constexpr int kFewUnits = 304, kFewRounds = 4;
 
 struct __align__(16) Ctl {
   FwdItem unit[kFewUnits];
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the plan kernel's rule, and its shares, in the order (kv head, unit)
       const int G = int(gridDim.x), me = int(blockIdx.x), n_items = U * p.Hkv;
       const long long all = 1LL * T * p.Hkv;
-      const bool split = most > all / G * FwdSide::kSplitGain / 8 + kPartsCost;
+      const bool split = n_items > G || most > all / G * FwdSide::kSplitGain / 8 + kPartsCost;
       const long long lo = all * me / G, hi = all * (me + 1) / G;
       Cut cut;
       cut.c1 = -1;
@@ -1117,12 +1120,12 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   // a sequence of n tokens has ceil(n / (2 tok)) units
   long long units = pb.total_q / (2 * tok) + pb.B;
   if (units > pb.total_q) units = pb.total_q;
-  const bool few = units <= kFewUnits && units * pb.Hkv <= G;
+  const bool few = units <= kFewUnits && units * pb.Hkv <= (PAGED ? kFewRounds : 1) * G;
   // Few items of few key tiles are never divided: no workspace, no last kernel.
   long long keys = pb.page_table != nullptr ? 1LL * pb.max_pages * pb.page_size : pb.total_k;
   if (pb.window_left >= 0 && pb.window_right >= 0)  // and whole tiles around those that a unit sees
     keys = std::min(keys, 2LL * tok + pb.window_left + pb.window_right + 254);
-  const bool whole = few && (keys + 127) / 128 + kItemCost <= kPartsCost;
+  const bool whole = few && units * pb.Hkv <= G && (keys + 127) / 128 + kItemCost <= kPartsCost;
   void* ws = nullptr;
   Space sp{};
   if (!whole) {
