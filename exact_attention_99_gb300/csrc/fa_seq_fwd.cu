@@ -177,6 +177,12 @@ __device__ __forceinline__ Work work_of(const Params& p, const FwdItem* src, int
   return x;
 }
 
+// A lane's box of a key tile in a paged cache.
+struct Place {
+  int page, in_page;
+  int boxes;  // of the tile
+};
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -572,6 +578,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w == nullptr) break;
       const int nt = w->nt, kvh = w->kvh, kt = w->kt, kbase = w->kbase, klen = w->klen;
       const bool key = (w->flags & kKeyMode) != 0;
+      // Where this lane's box of tile t is. The table is read one tile ahead
+      // of its K, and K's places serve V: a read takes as long as a product.
+      auto place = [&](int t) {
+        Place at{0, 0, 0};
+        if constexpr (PAGED) {
+          // boxes that begin before the sequence's end
+          const int key0 = (kt + t) * 128;
+          at.boxes = min(n_box, (klen - key0 + p.box_rows - 1) / p.box_rows);
+          if (t < nt && chunk < C::kChunks && box < at.boxes) {
+            const int k = key0 + box * p.box_rows, pg = k / p.page_size;
+            at.page = p.table[size_t(kbase) * p.max_pages + pg];
+            at.in_page = k - pg * p.page_size;
+          }
+        }
+        return at;
+      };
+      Place k_at = place(0);
       // Q: key mode takes the two buffers in turn, else stage s takes buffer s
       for (int s = 0; s < 2 && ok; ++s) {
         if (w->n[s] == 0 || (key && s == 1)) continue;
@@ -593,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // K runs d tiles ahead of V: K(0..d-1), then V(t), K(t + d) in turn, then the last V
       const int d = min(key ? 2 : 1, nt), turns = 2 * (nt - d);
+      Place v_at = k_at, v_next = k_at;  // of the next V tile and the one after: their K tiles' places
 #pragma unroll 1
       for (int e = 0; e < 2 * nt; ++e) {
         const int r = e - d;
@@ -600,23 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = r < 0 ? e : r >= turns ? r - (nt - d) : is_v ? r >> 1 : d + (r >> 1);
         const CUtensorMap* m = is_v ? &tmV : &tmK;
         const uint32_t slot = kv_it % C::kSlots;
-        const int key0 = (kt + t) * 128;
         uint8_t* dst = sKV + slot * C::kTileBytes;
-        int boxes = 1, page = 0, in_page = 0;
-        if constexpr (PAGED) {
-          // boxes that begin before the sequence's end; the page is looked up
-          // before the wait for the slot
-          boxes = min(n_box, (klen - key0 + p.box_rows - 1) / p.box_rows);
-          if (chunk < C::kChunks && box < boxes) {
-            const int k = key0 + box * p.box_rows, pg = k / p.page_size;
-            page = p.table[size_t(kbase) * p.max_pages + pg];
-            in_page = k - pg * p.page_size;
-            if (page < 0 || page >= p.num_pages) {  // no such page: its keys read as zeros, and the caller is told
-              atomicOr(p.status, kDevBadArg);
-              page = p.num_pages;
-            }
-          }
-        }
         ok = warp_wait(&ctl.kv_empty[slot], ((kv_it / C::kSlots) & 1) ^ 1, abort_flag, LIM);
         if (!ok) break;
         ++kv_it;
@@ -625,16 +633,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if constexpr (PAGED) {
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(boxes * p.box_rows * D * 2));
+          if (!is_v) {
+            if (k_at.page < 0 || k_at.page >= p.num_pages) {  // no such page: its keys read as zeros, and the caller is told
+              atomicOr(p.status, kDevBadArg);
+              k_at.page = p.num_pages;
+            }
+            if (d == 1 || t == 0) {
+              v_at = k_at;
+            } else {
+              v_next = k_at;
+            }
+          }
+          const Place at = is_v ? v_at : k_at;
+          if (is_v) {
+            v_at = v_next;
+          } else {
+            k_at = place(t + 1);
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(at.boxes * p.box_rows * D * 2));
           __syncwarp();
-          if (chunk < C::kChunks && box < boxes)
-            tma_load_4d_hint(dst + chunk * 16384 + box * p.box_rows * 128, m, &ctl.kv_full[slot], chunk * 64, kvh, in_page,
-                             page, pol_kv);
+          if (chunk < C::kChunks && box < at.boxes)
+            tma_load_4d_hint(dst + chunk * 16384 + box * p.box_rows * 128, m, &ctl.kv_full[slot], chunk * 64, kvh, at.in_page,
+                             at.page, pol_kv);
         } else if (lane == 0) {
           mbar_arrive_expect_tx(&ctl.kv_full[slot], C::kTileBytes);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            tma_load_4d_hint(dst + c * 16384, m, &ctl.kv_full[slot], c * 64, kvh, kbase + key0, 0, pol_kv);
+            tma_load_4d_hint(dst + c * 16384, m, &ctl.kv_full[slot], c * 64, kvh, kbase + (kt + t) * 128, 0, pol_kv);
         }
         // (the last entry is the last V)
         if (e == 2 * nt - 1 && w->fill != 0 && lane == 0) mbar_arrive(&ctl.tail_req[slot]);
