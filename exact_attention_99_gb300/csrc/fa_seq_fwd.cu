@@ -570,9 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, injected = false;
     const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
     const uint32_t q_bytes = uint32_t(p.tok * p.group * D * 2);
-    // paged: lane -> (box of the tile, 64-column chunk)
-    const int n_box = PAGED ? 128 / p.box_rows : 1;
-    const int box = lane % n_box, chunk = lane / n_box;
+    const int n_box = PAGED ? 128 / p.box_rows : 1;  // of a tile; lane i looks up box i
     for (int i = 0; ok; ++i) {
       const Work* const w = item(i);
       if (w == nullptr) break;
@@ -586,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // boxes that begin before the sequence's end
           const int key0 = (kt + t) * 128;
           at.boxes = min(n_box, (klen - key0 + p.box_rows - 1) / p.box_rows);
-          if (t < nt && chunk < C::kChunks && box < at.boxes) {
-            const int k = key0 + box * p.box_rows, pg = k / p.page_size;
+          if (t < nt && lane < at.boxes) {
+            const int k = key0 + lane * p.box_rows, pg = k / p.page_size;
             at.page = p.table[size_t(kbase) * p.max_pages + pg];
             at.in_page = k - pg * p.page_size;
           }
@@ -650,11 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             k_at = place(t + 1);
           }
-          if (lane == 0) mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(at.boxes * p.box_rows * D * 2));
-          __syncwarp();
-          if (chunk < C::kChunks && box < at.boxes)
-            tma_load_4d_hint(dst + chunk * 16384 + box * p.box_rows * 128, m, &ctl.kv_full[slot], chunk * 64, kvh, at.in_page,
-                             at.page, pol_kv);
+          // One lane issues the boxes, unrolled: a copy's operands are uniform
+          // registers, which lanes that issue a box each take turns to fill.
+          int page[8], in_page[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            page[x] = __shfl_sync(0xffffffffu, at.page, x);
+            in_page[x] = __shfl_sync(0xffffffffu, at.in_page, x);
+          }
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(at.boxes * p.box_rows * D * 2));
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              if (x >= at.boxes) break;
+#pragma unroll
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_4d_hint(dst + c * 16384 + x * p.box_rows * 128, m, &ctl.kv_full[slot], c * 64, kvh, in_page[x],
+                                 page[x], pol_kv);
+            }
+          }
         } else if (lane == 0) {
           mbar_arrive_expect_tx(&ctl.kv_full[slot], C::kTileBytes);
 #pragma unroll
