@@ -5,7 +5,8 @@
 // flight per thread. A block takes kRows tokens; its first threads find
 // where each goes (binary search of the token in cu_q, then the page of its
 // place in the sequence) while the others wait, and the rows are then copied
-// as runs of Hkv * d values.
+// as runs of Hkv * d values. 45 thousand tokens of 8 heads of 128: 57 us, 6.5
+// TB/s, 0.96 of the measured copy; 100 single tokens: 5 us, a launch.
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"

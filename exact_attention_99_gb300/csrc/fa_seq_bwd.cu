@@ -22,6 +22,15 @@
 //     memory by a warp of its own before any product reads them (another
 //     sequence's infinities would survive a multiplication by P = 0).
 //
+// What bounds it: shared memory. A step (a key tile and a tile of 128 rows,
+// d = 128) takes 2.2 us, in which the five products' operands, dS and the
+// staging of dQ are some 512 KB of shared-memory traffic; the tensor pipe is
+// 63 % busy, DRAM 26 % (2 sequences of 4096 tokens). One causal sequence of
+// 16384 tokens, 32 / 8 heads: 3.9 ms, as the dense backward; 8 of 2048:
+// 0.85 ms (dense 1.09, whose diagonals waste more). pre and post move their
+// bytes at the memory's rate (85 and 59 us of a step over 16 thousand packed
+// tokens of 1.5 ms).
+//
 // Kernels: plan, pre (D, LSE * log2 e, zeroed accumulator), main, post (dQ to
 // bf16, and the parts' sums).
 //   main: 512 threads, persistent, one CTA per SM

@@ -11,10 +11,10 @@
 //     tile: one new token of a group of 4 reads its cache once, not 4 times;
 //   * the lengths are on the device, so a planning kernel of one block lays
 //     out the work there: a list of items sorted by key tiles (longest first)
-//     that the CTAs take in snake order, or, where that would leave CTAs idle
+//     that the CTAs take in rounds, or, where that would leave CTAs idle
 //     (few rows over long caches), the same rows' key tiles laid end to end
 //     and divided evenly between the CTAs, whose partial results (m, l, O)
-//     a last kernel joins in a fixed order;
+//     a last kernel joins in a fixed order (fa_seq_plan.cuh);
 //   * an item of one row tile (one token, short chunks, a sequence's last
 //     rows) has no second row tile to overlap its softmax with: its two
 //     stages take alternate key tiles and are joined in the epilogue;
@@ -31,7 +31,21 @@
 //     warps 8-11       correction (O rescaled when a row's maximum grows) and epilogue
 //     warp 12 TMA producer, 13 MMA issuer, 14 V tail, 15 work items
 //   TMEM as in the dense forward: S/P of the stages at columns 0 and 128, O
-//   at 256 and 256 + d.
+//   at 256 and 256 + d. (At d = 64 there is room for a P apart from its S, so
+//   that S is issued a step ahead; measured slower, 16384 causal tokens 1.15
+//   -> 1.22 ms: the two stages' softmax then run in step.)
+//
+// What bounds it, measured:
+//   d = 128, long sequences: the tensor pipe. One causal sequence of 16384
+//     tokens, 32 query and 8 kv heads: 1.29 ms, 1710 TFLOP/s, 0.89 of the
+//     measured bf16 matrix product rate (the dense forward: 1.64 ms).
+//   d = 64: the softmax's latency. The same sequence takes 1.15 ms (dense 1.42);
+//     the schedulers issue in 42 % of the cycles, tensor pipe 35 %.
+//   single tokens: the cache's bytes. 64 sequences of 300 to 32000 keys, 8 kv
+//     heads of 128: 1.70 GB in 258 us, 6.6 TB/s, 0.97 of the measured copy.
+//   items of few tiles: 1.3 to 2.3 us between two items, most of it instruction
+//     fetch (code that runs once per item is not in the cache) and the first
+//     S; small calls: the launches (77 tokens: 8 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -117,7 +131,8 @@ struct Work {
 // kFewUnits units and no more items than CTAs, or, over a paged cache,
 // kFewRounds times as many, which are then always divided: sorting wants the
 // planning kernel, and gains where there are many units of as many keys as
-// rows (prompts), not where rows are few.
+// rows (prompts), not where rows are few (64 single tokens, 512 items: 279 us
+// planned and sorted, 259 us here).
 constexpr int kFewUnits = 304, kFewRounds = 4;
 
 struct __align__(16) Ctl {
@@ -577,7 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = w->nt, kvh = w->kvh, kt = w->kt, kbase = w->kbase, klen = w->klen;
       const bool key = (w->flags & kKeyMode) != 0;
       // Where this lane's box of tile t is. The table is read one tile ahead
-      // of its K, and K's places serve V: a read takes as long as a product.
+      // of its K, and K's places serve V: read for every load, as it was
+      // needed, the table set the pace (3 chunks of 512 tokens over long caches
+      // 228 -> 217 us, a mixed batch with pages of 16 68 -> 63 us).
       auto place = [&](int t) {
         Place at{0, 0, 0};
         if constexpr (PAGED) {
@@ -649,7 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             k_at = place(t + 1);
           }
           // One lane issues the boxes, unrolled: a copy's operands are uniform
-          // registers, which lanes that issue a box each take turns to fill.
+          // registers, which lanes that issue a box each take turns to fill
+          // (the mixed batch 62 -> 59 us; in a rolled loop 69 us).
           int page[8], in_page[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
@@ -686,8 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 13) {
     // ---------------------------------------------------------- MMA issuer
-    // The whole warp walks the role and an elected lane issues (1.78 -> 1.49 ms
-    // on one causal sequence of 16384 tokens, against one lane walking).
+    // The whole warp walks the role and an elected lane issues (with the
+    // producer's and all waits, 1.78 -> 1.29 ms on one causal sequence of 16384
+    // tokens, against one lane walking: MMA operands are uniform registers).
     {
       const uint32_t idS = idesc_bf16_f32(128, 128, 0, 0) | (p.neg_s << 13);
       constexpr uint32_t idPV = idesc_bf16_f32(128, D, 0, 1);

@@ -272,7 +272,9 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
  *   out: dq [total_q, Hq, d], dk, dv [total_k, Hkv, d] (bf16, contiguous): the
  *        rows of every sequence; other rows are left as they are.
  * dk and dv are sums over the query heads of a group, taken in a fixed order;
- * the additions into dq are not ordered (as in fa_bwd). Workspace: fp32 dQ
+ * the additions into dq are not ordered (as in fa_bwd). q, k, v and dout of a
+ * sequence's rows must be finite, also where only the window hides them
+ * (a hidden probability is 0, and 0 times them is added). Workspace: fp32 dQ
  * (about 4 * total_q * Hq * d bytes) and 40 MB at d = 128 for parts.
  */
 int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
