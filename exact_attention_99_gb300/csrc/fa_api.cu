@@ -363,7 +363,7 @@ int check_seq_sizes(int B, int Hq, int Hkv, int total, int d) {
 // elements between the tokens of a tensor of `heads` heads
 int check_stride(long long stride, int heads, int d, int total) {
   if (stride < 1LL * heads * d || stride % 8 != 0) return FA_ERR_INVALID_ARG;
-  if (stride >= (1LL << 38) || stride * 2 * (total > 0 ? total : 1) >= (1LL << 40)) return FA_ERR_UNSUPPORTED;
+  if (stride >= (1LL << 38) || 2.0 * stride * (total > 0 ? total : 1) >= double(1LL << 40)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 int check_pages(int num_pages, int page_size, int max_pages, int Hkv, int d) {

@@ -51,6 +51,13 @@ def test_bad_sizes(fa, name, bad, code):
     assert call(fa, name, **bad) == code
 
 
+@pytest.mark.parametrize("name,total,stride", [("fa_fwd_varlen", "total_q", "q_stride"), ("fa_fwd_varlen", "total_k", "v_stride"),
+                                               ("fa_bwd_varlen", "total_k", "k_stride"), ("fa_fwd_paged", "total_q", "q_stride"),
+                                               ("fa_cache_append", "total_q", "k_stride")])
+def test_bytes_that_pass_64_bits(fa, name, total, stride):
+    assert call(fa, name, **{total: 1 << 26, stride: 1 << 37}) == 2  # 2^64 bytes
+
+
 @pytest.mark.parametrize("name", list(CALLS))
 def test_bad_pointers(fa, name):
     for arg, v in CALLS[name].items():
