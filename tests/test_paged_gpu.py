@@ -79,6 +79,13 @@ def test_many_sequences(fa):
     run(fa, [1] * 1200, keys, 2, 1, 64, 16, seed=14)
 
 
+def test_many_empty_sequences(fa):
+    new, keys = [0] * 4000, [5] * 4000
+    new[7], new[2000], new[3999] = 40, 3, 1
+    keys[7], keys[3999] = 300, 900
+    run(fa, new, keys, 4, 2, 128, 16, seed=62)
+
+
 def test_append_then_attend(fa):
     hq, hk, d, page = 8, 2, 128, 16
     old, new = [0, 100, 31, 500], [40, 1, 17, 250]

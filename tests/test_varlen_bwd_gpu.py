@@ -82,6 +82,12 @@ def test_many_sequences(fa):
     run(fa, n, n, 2, 1, 64, seed=6)
 
 
+def test_many_empty_sequences(fa):
+    n = [0] * 4000
+    n[7], n[2000], n[3999] = 40, 3, 300
+    run(fa, n, n, 4, 2, 128, seed=61)
+
+
 @pytest.mark.parametrize("hq,hk,d", [(16, 8, 128), (24, 8, 64)])
 def test_many_items_per_cta(fa, hq, hk, d):
     rng = torch.Generator().manual_seed(hq)
