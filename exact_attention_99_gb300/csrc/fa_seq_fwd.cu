@@ -1003,8 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               cut.count = src->ntok();
               cut.kvh = kk;
               cut.c0 = me;
-              cut.c1 = me + 1;
-              while (all * (cut.c1 + 1) / G < y1) ++cut.c1;
+              cut.c1 = int((y1 * G - 1) / all);  // the last whose share begins before y1
             }
           }
           any = true;
