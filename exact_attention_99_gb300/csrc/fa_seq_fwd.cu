@@ -977,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the plan kernel's rule, and its shares, in the order (kv head, unit)
       const int G = int(gridDim.x), me = int(blockIdx.x), n_items = U * p.Hkv;
       const long long all = 1LL * T * p.Hkv;
-      const bool split = n_items > G || most > all / G * FwdSide::kSplitGain / 8 + kPartsCost;
+      const bool split = n_items > G || most > all / G * FwdSide::kSplitGain / 8 + FwdSide::kPartsCost;
       const long long lo = all * me / G, hi = all * (me + 1) / G;
       Cut cut;
       cut.c1 = -1;
@@ -1033,25 +1033,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The parts of the rows whose keys were divided between workers, joined in
 // the workers' order: O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i. Block
-// (c, y): cut c, every gridDim.y-th group of rows; a warp per row. The
-// lanes read the parts' (m, l) first, so that the reads of O are independent.
+// (c, y): cut c, every gridDim.y-th group of rows; a warp per row, or several
+// that take consecutive parts, where the rows are few and the parts many (the
+// parts' reads, one after the other, are what the kernel takes: one token over
+// 8000 keys 29 -> 16 us). The lanes read the parts' (m, l) first, so that the
+// reads of O are independent.
+constexpr int kJoinWarps = 8;  // (of 16 or 32, chunks over a cache took 4 and 10 us longer)
 template <int D>
-__global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) seq_join_kernel(const Params p) {
+  __shared__ float so[kJoinWarps][D];
+  __shared__ float2 sml[kJoinWarps];
   grid_dep_wait();
   const Cut k = p.cuts[blockIdx.x];
   if (k.c1 < 0) return;
-  const int lane = threadIdx.x & 31;
-  const int rows = k.count * p.group, per_stage = p.tok * p.group;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = k.count * p.group, per_stage = p.tok * p.group, parts = k.c1 - k.c0 + 1;
   constexpr int V = D / 32;  // columns per lane
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8) {
+  int per_row = kJoinWarps;  // no more than there are, and four parts to each
+  while (per_row > 1 && (per_row * rows > kJoinWarps * int(gridDim.y) || per_row * 4 > parts)) per_row >>= 1;
+  const int at_once = kJoinWarps / per_row, share = (parts + per_row - 1) / per_row;
+  const int first = k.c0 + warp % per_row * share, last = min(first + share - 1, k.c1);  // this warp's parts
+  for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
+    const int r = r0 + warp / per_row;
     const int s = r >= per_stage ? 1 : 0;
     const size_t at = size_t(s) * 128 + (r - s * per_stage);
     float m = -INFINITY, l = 0.0f, o[V] = {};
-    for (int c0 = k.c0; c0 <= k.c1; c0 += 32) {  // 32 parts at a time
+    for (int c0 = first; r < rows && c0 <= last; c0 += 32) {  // 32 parts at a time
       const int c = c0 + lane;
       const size_t mine = size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * 256 + at;
       float2 ml = make_float2(-INFINITY, 0.0f);
-      if (c <= k.c1) {
+      if (c <= last) {
         const bool has = p.last[c] >= 0;  // a worker without a share has no part: what its slot holds is not used
         const float2 x = p.part_ml[mine];
         if (has) ml = x;
@@ -1069,7 +1080,7 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
       m = mn;
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] *= wa;
-      const int n = min(32, k.c1 - c0 + 1);
+      const int n = min(32, last - c0 + 1);
 #pragma unroll 4
       for (int i = 0; i < n; ++i) {
         const float wi = __shfl_sync(0xffffffffu, wb, i), li = __shfl_sync(0xffffffffu, ml.y, i);
@@ -1089,6 +1100,26 @@ __global__ void __launch_bounds__(256) seq_join_kernel(const Params p) {
         }
       }
     }
+    if (per_row > 1) {  // the row's warps, in order
+      __syncthreads();  // the rows before have been read
+#pragma unroll
+      for (int e = 0; e < V; ++e) so[warp][lane * V + e] = o[e];
+      if (lane == 0) sml[warp] = make_float2(m, l);
+      __syncthreads();
+      if (warp % per_row != 0) continue;
+      for (int i = 1; i < per_row; ++i) m = fmaxf(m, sml[warp + i].x);
+      const float mu = m == -INFINITY ? 0.0f : m;
+      l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = 0.0f;
+      for (int i = 0; i < per_row; ++i) {
+        const float f = ex2_mufu(sml[warp + i].x - mu);
+        l = fmaf(sml[warp + i].y, f, l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(so[warp + i][lane * V + e], f, o[e]);
+      }
+    }
+    if (r >= rows) continue;
     const int tok = r / p.group, head = k.kvh * p.group + (r - tok * p.group), token = k.row0 + tok;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat16* dst = p.o + (size_t(token) * p.Hq + head) * D + lane * V;
@@ -1182,7 +1213,7 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   long long keys = pb.page_table != nullptr ? 1LL * pb.max_pages * pb.page_size : pb.total_k;
   if (pb.window_left >= 0 && pb.window_right >= 0)  // and whole tiles around those that a unit sees
     keys = std::min(keys, 2LL * tok + pb.window_left + pb.window_right + 254);
-  const bool whole = few && units * pb.Hkv <= G && (keys + 127) / 128 + kItemCost <= kPartsCost;
+  const bool whole = few && units * pb.Hkv <= G && (keys + 127) / 128 + kItemCost <= FwdSide::kPartsCost;
   void* ws = nullptr;
   Space sp{};
   if (!whole) {
@@ -1247,8 +1278,12 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   if (dc.ev_end) cudaEventRecord(dc.ev_end, stream);
   if (e == cudaSuccess && !whole) {
     lc.numAttrs = 1;
-    lc.gridDim = dim3(G, unsigned(std::max(1LL, std::min(16LL, (1LL * pb.total_q * group + 7) / 8))));
-    lc.blockDim = dim3(256);
+    // 256 rows of a cut at most. Units of some parts get a warp per row at once
+    // (64 tokens over 4000 keys 43 -> 32 us); of many units none has more than
+    // a few, if any are divided, and half as many blocks start 1 us sooner.
+    const long long high = (units * pb.Hkv * 4 < G ? 256 : 128) / kJoinWarps;
+    lc.gridDim = dim3(G, unsigned(std::min(high, 1LL * pb.total_q * group)));
+    lc.blockDim = dim3(kJoinWarps * 32);
     lc.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&lc, seq_join_kernel<D>, p);
   }

@@ -31,7 +31,6 @@ constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = 1024;    // of the sort by n; units of more tiles sort as equal
 constexpr int kMaxWorkers = 256;  // CTAs of a main kernel
 constexpr int kItemCost = 2;
-constexpr int kPartsCost = 6;  // of divided units: the parts' stores and the last kernel, in tile products
 
 // An item is a unit, or a part of one, for one kv head.
 struct __align__(16) FwdItem {
@@ -150,6 +149,10 @@ struct FwdSide {
   // One causal sequence of 16384 tokens (32 query heads, 8 kv heads) took 6 %
   // longer split, packed prompts of 16 to 4096 tokens 44 % (at 2 % less in the count).
   static constexpr int kSplitGain = 9;
+  // Of divided units: the parts' stores and the last kernel, in tile products.
+  // (40 tokens of 8 heads, 2 kv heads over 600 keys, 5 products: 20.6 us
+  // divided, 16.6 whole; over 1040, 9 products: 22.5 divided, about 23 whole.)
+  static constexpr int kPartsCost = 9;
   static constexpr int kRanked = 2;  // many units of few tiles: back and forth is even enough
   int tok, wl, wr, paged;
   __device__ __forceinline__ int units(const Seq& s) const { return (s.qlen + 2 * tok - 1) / (2 * tok); }
@@ -185,6 +188,7 @@ struct BwdSide {
   // Split, the CTAs of a sequence add into dQ rows far apart: one causal
   // sequence of 16384 tokens took 5.8 instead of 3.9 ms.
   static constexpr int kSplitGain = 12;
+  static constexpr int kPartsCost = 6;  // (at 9 a training step on 2115 tokens took 54 instead of 48 us)
   // Units of many tiles: the documents of a packed training step are 6 % from
   // even back and forth, 1 % ranked (step 1.68 -> 1.53 ms).
   static constexpr int kRanked = 12;
@@ -442,11 +446,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     __syncthreads();
   }
   // The busiest worker against an equal division, which has to win by more
-  // than kPartsCost and what CTAs at different places cost (Side::kSplitGain, in
+  // than Side::kPartsCost and what CTAs at different places cost (Side::kSplitGain, in
   // eighths).
   if (tid < G) atomicMax(&worst, static_cast<unsigned long long>(own));
   __syncthreads();
-  const bool split = static_cast<long long>(worst) > Ttot / G * Side::kSplitGain / 8 + kPartsCost;
+  const bool split = static_cast<long long>(worst) > Ttot / G * Side::kSplitGain / 8 + Side::kPartsCost;
   if (tid == 0) *P.head = PlanHead{n_items, split ? 1 : G, 0, 0};
   if (!split) {
     if (tid < G) {

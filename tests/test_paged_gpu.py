@@ -79,6 +79,13 @@ def test_many_sequences(fa):
     run(fa, [1] * 1200, keys, 2, 1, 64, 16, seed=14)
 
 
+@pytest.mark.parametrize("new,keys,window", [([1], [20011], None), ([3, 0, 1], [9000, 5, 1], None), ([64], [5000], None),
+                                             ([40], [7000], (2000, 0)), ([1], [20011], (300, 0)), ([17], [12], None)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 2, 128), (3, 1, 64)])
+def test_few_rows_in_many_parts(fa, new, keys, window, hq, hk, d):
+    run(fa, new, keys, hq, hk, d, 32, seed=63, window=window)
+
+
 def test_many_empty_sequences(fa):
     new, keys = [0] * 4000, [5] * 4000
     new[7], new[2000], new[3999] = 40, 3, 1
