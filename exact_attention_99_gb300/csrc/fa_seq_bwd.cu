@@ -680,14 +680,46 @@ __device__ __forceinline__ RowAt row_at(const int* cu_q, const int* tstart, int 
 // where a row is none or sees nothing, so that its probabilities recompute to
 // 0), and zeroes for the accumulator rows. A warp takes 16 rows of a row tile
 // at a time, 16 bytes of O and dO per lane and piece.
+// Up to kOwnSeqs sequences, every block finds the sequences' first row tiles by
+// itself, and the kernel runs beside the plan (a training step on 2115 tokens
+// 47.9 -> 45.3 us); the tiles of larger batches are the plan's.
+constexpr int kOwnSeqs = 256;
 template <int D>
 __global__ void __launch_bounds__(256)
-    seq_pre_kernel(const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse, const int* cu_q, const int* tstart,
-                   const PlanHead* head, float* lse2, float* delta, float* acc, int B, int Hkv, int group, int tok,
-                   int tile_cap, int total_q) {
-  grid_dep_wait();    // the plan
+    seq_pre_kernel(const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse, const seq::Lens L,
+                   const seq::BwdSide side, const int* plan_tstart, const PlanHead* head, float* lse2, float* delta,
+                   float* acc, int Hkv, int group, int tile_cap) {
+  __shared__ int own[kOwnSeqs + 1];
+  __shared__ int sums[8];
+  const int B = L.B, tok = side.tok, total_q = L.total_q;
+  const int* const cu_q = L.cu_q;
+  const int* tstart = own;
   grid_dep_launch();  // the main kernel may start its set-up meanwhile
-  if (head->bad) return;
+  if (B <= kOwnSeqs) {
+    const int b = threadIdx.x, w = b >> 5;
+    seq::Seq s;
+    const bool ok = b >= B || seq::seq_at(L, b, s);
+    int at = b < B && ok ? side.row_tiles(s) : 0;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, at, m);
+      if ((b & 31) >= m) at += x;
+    }
+    if ((b & 31) == 31) sums[w] = at;
+    const bool bad = __syncthreads_or(!ok);
+    for (int i = 0; i < w; ++i) at += sums[i];
+    own[b + 1] = at;
+    if (b == 0) own[0] = 0;
+    __syncthreads();
+    if (bad) {  // lengths that the tensors cannot hold
+      grid_dep_wait();
+      return;
+    }
+  } else {
+    grid_dep_wait();  // the plan
+    if (head->bad) return;
+    tstart = plan_tstart;
+  }
   constexpr int TPR = D / 8;          // lanes per row
   constexpr int RPP = 32 / TPR;       // rows per pass of the warp
   constexpr int kPass = 16 / RPP;     // passes per 16 rows
@@ -742,6 +774,7 @@ __global__ void __launch_bounds__(256)
       delta[arow + lane] = x.token >= 0 ? mine : 0.0f;
     }
   }
+  if (B <= kOwnSeqs) grid_dep_wait();  // the main kernel waits for this one, and needs the plan
 }
 
 // dq[token, head, :] = bf16(scale * accumulator row), then the sums of the
@@ -932,9 +965,9 @@ cudaError_t launch_t(const SeqProblem& pb, const void* o, const float* lse, cons
     lc.gridDim = dim3(wide);
     lc.blockDim = dim3(256);
     e = cudaLaunchKernelEx(&lc, seq_pre_kernel<D>, static_cast<const __nv_bfloat16*>(o),
-                           static_cast<const __nv_bfloat16*>(dout), lse, pb.cu_q, static_cast<const int*>(sp.plan.tstart),
-                           static_cast<const PlanHead*>(sp.plan.head), sp.lse2, sp.delta, sp.acc, pb.B, pb.Hkv, group,
-                           tok, sp.tile_cap, pb.total_q);
+                           static_cast<const __nv_bfloat16*>(dout), lse, a.L, a.side,
+                           static_cast<const int*>(sp.plan.tstart), static_cast<const PlanHead*>(sp.plan.head), sp.lse2,
+                           sp.delta, sp.acc, pb.Hkv, group, sp.tile_cap);
   }
   if (dc.ev_begin) cudaEventRecord(dc.ev_begin, stream);
   if (e == cudaSuccess) {

@@ -216,6 +216,24 @@ def test_wrong_lengths_change_nothing(fa, many):
     assert fa.fa_get_status() == 0
 
 
+def test_wrong_lengths_of_a_large_batch_change_nothing(fa):
+    n = [5] * 300
+    (q, k, v), cu, _, _ = case(n, n, 2, 2, 64, 19)
+    o, lse = torch.full_like(q, 3.0), torch.full((2, q.shape[0]), 3.0, device="cuda")
+    grads = [torch.full_like(t, 3.0) for t in (q, k, v)]
+    assert fa.fa_get_status() == 0
+    for at, value in ((299, 2), (300, sum(n) + 1), (0, -1)):
+        bad = cu.clone()
+        bad[at] = value
+        for cq, ck in ((bad.cuda(), cu.cuda()), (cu.cuda(), bad.cuda())):
+            fa.forward_varlen(q, k, v, cq, ck, out=(o, lse))
+            assert fa.fa_get_status() == FA_ERR_INVALID_ARG
+            fa.backward_varlen(q, k, v, o, lse, q, cq, ck, out=grads)
+            assert fa.fa_get_status() == FA_ERR_INVALID_ARG
+    for t in (o, lse, *grads):
+        assert (t == 3.0).all()
+
+
 def test_wrong_pages_and_cache_lengths(fa):
     hq, hk, d, page = 4, 2, 64, 16
     g = su.gen(10)

@@ -82,6 +82,13 @@ def test_many_sequences(fa):
     run(fa, n, n, 2, 1, 64, seed=6)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 255, 256, 257])
+def test_numbers_of_sequences(fa, B):
+    rng = torch.Generator().manual_seed(B)
+    n = torch.randint(0, 70, (B,), generator=rng).tolist()
+    run(fa, n, n, 3, 1, 64, seed=B)
+
+
 def test_many_empty_sequences(fa):
     n = [0] * 4000
     n[7], n[2000], n[3999] = 40, 3, 300
