@@ -20,16 +20,16 @@
 //     stages take alternate key tiles and are joined in the epilogue;
 //   * pages: a 128-key tile is 128 / box TMA boxes, each from the page that
 //     the table names, box the largest power of two dividing the page size
-//     (at most 128); lane i of the producer warp issues box i.
+//     (at most 128); lane i of a producer warp looks box i up.
 //   * the last key tile of a sequence reads on into what follows it (another
 //     sequence, a page's unused rows). Scores are masked by a select; V rows
-//     past the end are zeroed in shared memory by a warp of its own before
-//     the product reads them, as 0 * NaN would stay NaN.
+//     past the end are zeroed in shared memory, by the warp that loads V,
+//     before the product reads them, as 0 * NaN would stay NaN.
 //
 //   CTA = 512 threads, persistent (one per SM):
 //     warps 0-3 / 4-7  softmax of stage 0 / 1 (a thread per row)
 //     warps 8-11       correction (O rescaled when a row's maximum grows) and epilogue
-//     warp 12 TMA producer, 13 MMA issuer, 14 V tail, 15 work items
+//     warps 12 and 14 TMA producers (Q and K, V), 13 MMA issuer, 15 work items
 //   TMEM as in the dense forward: S/P of the stages at columns 0 and 128, O
 //   at 256 and 256 + d. (At d = 64 there is room for a P apart from its S, so
 //   that S is issued a step ahead; measured slower, 16384 causal tokens 1.15
@@ -144,8 +144,7 @@ struct __align__(16) Ctl {
   uint64_t it_full[kItems], it_empty[kItems];
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
-  // a V tile that the sequence ends in: loaded into the slot (being loaded), its rows past the end zeroed
-  uint64_t tail_req[kMaxSlots], tail_done[kMaxSlots];
+  uint64_t tail_done[kMaxSlots];  // a V tile that the sequence ends in: loaded, its rows past the end zeroed
   // p_full: P stored (4 softmax warps) and O corrected, or read by the epilogue
   // of the stage's item before (4 correction warps)
   uint64_t s_full[2], p_full[2], alpha_full[2], o_full[2];
@@ -236,7 +235,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&ctl.kv_full[i], 1);
       mbar_init(&ctl.kv_empty[i], 1);
-      mbar_init(&ctl.tail_req[i], 1);
       mbar_init(&ctl.tail_done[i], 1);
     }
     fence_mbar_init();
@@ -581,9 +579,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     setmaxnreg_dec<72>();
   }
-  if (warp == 12) {
-    // ------------------------------------------------------- TMA producer
-    uint32_t kv_it = 0, q_uses[2] = {0, 0}, key_items = 0;
+  if (warp == 12 || warp == 14) {
+    // ------------------------------------------------------ TMA producers
+    // Warp 12 loads Q and K, warp 14 V: a paged tile takes a warp some 0.5 us
+    // to look up and issue, and one warp for both set the pace of single tokens
+    // at d = 64 (256 of them over 1000 to 4000 keys, pages of 16: 375 -> 270 us).
+    // The ring holds K and V in the order in which the products take them.
+    const bool is_v = warp == 14;
+    const CUtensorMap* const m = is_v ? &tmV : &tmK;
+    uint32_t base = 0, q_uses[2] = {0, 0}, key_items = 0;  // ring entries of the items before
     bool ok = true, injected = false;
     const uint64_t pol_q = l2_policy_evict_first(), pol_kv = l2_policy_evict_last();
     const uint32_t q_bytes = uint32_t(p.tok * p.group * D * 2);
@@ -593,10 +597,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w == nullptr) break;
       const int nt = w->nt, kvh = w->kvh, kt = w->kt, kbase = w->kbase, klen = w->klen;
       const bool key = (w->flags & kKeyMode) != 0;
-      // Where this lane's box of tile t is. The table is read one tile ahead
-      // of its K, and K's places serve V: read for every load, as it was
-      // needed, the table set the pace (3 chunks of 512 tokens over long caches
-      // 228 -> 217 us, a mixed batch with pages of 16 68 -> 63 us).
+      // Where this lane's box of tile t is. The table is read one tile ahead:
+      // read as it was needed, it set the pace (3 chunks of 512 tokens over long
+      // caches 228 -> 217 us, a mixed batch with pages of 16 68 -> 63 us).
       auto place = [&](int t) {
         Place at{0, 0, 0};
         if constexpr (PAGED) {
@@ -611,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return at;
       };
-      Place k_at = place(0);
+      Place next = place(0);
       // Q: key mode takes the two buffers in turn, else stage s takes buffer s
-      for (int s = 0; s < 2 && ok; ++s) {
+      for (int s = 0; s < 2 && ok && !is_v; ++s) {
         if (w->n[s] == 0 || (key && s == 1)) continue;
         const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
         ok = warp_wait(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1, abort_flag, LIM);
@@ -631,41 +634,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                              w->q0 + (key ? 0 : s * p.tok), kvh, pol_q);
         }
       }
+      if (!ok) break;
       // K runs d tiles ahead of V: K(0..d-1), then V(t), K(t + d) in turn, then the last V
-      const int d = min(key ? 2 : 1, nt), turns = 2 * (nt - d);
-      Place v_at = k_at, v_next = k_at;  // of the next V tile and the one after: their K tiles' places
+      const int d = min(key ? 2 : 1, nt);
 #pragma unroll 1
-      for (int e = 0; e < 2 * nt; ++e) {
-        const int r = e - d;
-        const bool is_v = r >= 0 && (r >= turns || (r & 1) == 0);
-        const int t = r < 0 ? e : r >= turns ? r - (nt - d) : is_v ? r >> 1 : d + (r >> 1);
-        const CUtensorMap* m = is_v ? &tmV : &tmK;
-        const uint32_t slot = kv_it % C::kSlots;
+      for (int t = 0; t < nt; ++t) {
+        const uint32_t entry = base + uint32_t(is_v ? (t < nt - d ? d + 2 * t : nt + t) : (t < d ? t : 2 * t - d + 1));
+        const uint32_t slot = entry % C::kSlots, use = entry / C::kSlots;
         uint8_t* dst = sKV + slot * C::kTileBytes;
-        ok = warp_wait(&ctl.kv_empty[slot], ((kv_it / C::kSlots) & 1) ^ 1, abort_flag, LIM);
+        // (The warp's entry before this one is at most 3 back: what it waited
+        // for has been taken, and all before it, so that this wait is for the
+        // slot's last use and no earlier one.)
+        ok = warp_wait(&ctl.kv_empty[slot], (use & 1) ^ 1, abort_flag, LIM);
         if (!ok) break;
-        ++kv_it;
-        if (p.inject == 1 && !injected) {  // test hook: never deliver this tile
+        if (p.inject == 1 && !is_v && !injected) {  // test hook: never deliver this tile
           injected = true;
           continue;
         }
         if constexpr (PAGED) {
-          if (!is_v) {
-            if (k_at.page < 0 || k_at.page >= p.num_pages) {  // no such page: its keys read as zeros, and the caller is told
-              atomicOr(p.status, kDevBadArg);
-              k_at.page = p.num_pages;
-            }
-            if (d == 1 || t == 0) {
-              v_at = k_at;
-            } else {
-              v_next = k_at;
-            }
-          }
-          const Place at = is_v ? v_at : k_at;
-          if (is_v) {
-            v_at = v_next;
-          } else {
-            k_at = place(t + 1);
+          Place at = next;
+          next = place(t + 1);
+          if (at.page < 0 || at.page >= p.num_pages) {  // no such page: its keys read as zeros, and the caller is told
+            atomicOr(p.status, kDevBadArg);
+            at.page = p.num_pages;
           }
           // One lane issues the boxes, unrolled: a copy's operands are uniform
           // registers, which lanes that issue a box each take turns to fill
@@ -693,16 +684,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_4d_hint(dst + c * 16384, m, &ctl.kv_full[slot], c * 64, kvh, kbase + (kt + t) * 128, 0, pol_kv);
         }
-        // (the last entry is the last V)
-        if (e == 2 * nt - 1 && w->fill != 0 && lane == 0) mbar_arrive(&ctl.tail_req[slot]);
+        const int fill = w->fill;
+        if (is_v && t == nt - 1 && fill != 0) {
+          // The sequence ends in this tile: once loaded, its rows past the end
+          // are zeroed before the product reads them (a row is 128 bytes of
+          // each chunk; the swizzle stays within it).
+          __syncwarp();
+          ok = warp_wait(&ctl.kv_full[slot], use & 1, abort_flag, LIM);
+          if (!ok) break;
+          for (int k = fill * 8 + lane; k < 128 * 8; k += 32)
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              *reinterpret_cast<uint4*>(dst + c * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.tail_done[slot]);
+        }
       }
+      base += uint32_t(2 * nt);
       __syncwarp();
       if (lane == 0) release(i);
-    }
-    if (*abort_flag) {
-      // let copies already in flight land before shared memory is released
-      const uint64_t t0 = globaltimer_ns();
-      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
     }
   } else if (warp == 13) {
     // ---------------------------------------------------------- MMA issuer
@@ -860,36 +861,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-  } else if (warp == 14) {
-    // ---------------------------------------------------------- V tail rows
-    uint32_t kv_it = 0, req_phases = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const Work* const w = item(i);
-      if (w == nullptr) break;
-      const int fill = w->fill;
-      kv_it += 2 * w->nt;
-      if (fill != 0) {
-        // An item's last ring entry is its last V tile. The slot holds no
-        // other tile from the request until the products have read this one.
-        const uint32_t e = kv_it - 1, slot = e % C::kSlots;
-        ok = warp_wait(&ctl.tail_req[slot], (req_phases >> slot) & 1, abort_flag, LIM) &&
-             warp_wait(&ctl.kv_full[slot], (e / C::kSlots) & 1, abort_flag, LIM);
-        if (!ok) break;
-        req_phases ^= 1u << slot;
-        uint8_t* dst = sKV + slot * C::kTileBytes;
-        // a row is 128 bytes of each chunk (the swizzle stays within it)
-        for (int k = fill * 8 + lane; k < 128 * 8; k += 32)
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            *reinterpret_cast<uint4*>(dst + c * 16384 + k * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.tail_done[slot]);
-      }
-      __syncwarp();
-      if (lane == 0) release(i);
-    }
   } else if (warp == 15) {
     // --------------------------------------------------------- work items
     int n_done = 0;
@@ -1023,6 +994,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------------------- teardown
+  if ((warp == 12 || warp == 14) && *abort_flag) {
+    // let copies already in flight land before shared memory is released
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
