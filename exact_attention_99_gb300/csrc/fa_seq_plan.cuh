@@ -151,7 +151,7 @@ struct FwdSide {
   static constexpr int kSplitGain = 9;
   // Of divided units: the parts' stores and the last kernel, in tile products.
   // (40 tokens of 8 heads, 2 kv heads over 600 keys, 5 products: 20.6 us
-  // divided, 16.6 whole; over 1040, 9 products: 22.5 divided, about 23 whole.)
+  // divided, 16.6 whole; over 800, 7 products: 21.6 divided, 19.8 whole.)
   static constexpr int kPartsCost = 9;
   static constexpr int kRanked = 2;  // many units of few tiles: back and forth is even enough
   int tok, wl, wr, paged;
