@@ -33,9 +33,9 @@
 //     ring (its last reader, dV, runs early in each step), the dS^T tile,
 //     the dQ staging buffer, LSE/D vectors.
 //     warp 12    TMA producer, warp 13 MMA issuer, warps 14-15 idle
-//     TMEM: S^T [0,128) with P^T (bf16) over its first 64 columns;
-//           dP^T [128,256), reused for dQ once read; dV [256,256+d);
-//           dK [256+d, 256+2d).
+//     TMEM: S^T [0,128) with P^T (bf16) over columns [0,32) and [64,96)
+//           (fa_bwd_layout.h); dP^T [128,256), reused for dQ once read;
+//           dV [256,256+d); dK [256+d, 256+2d).
 //     MMA order per query tile i:
 //       dP(i), dV(i) += P^T dO, S(i+1), dK(i) += dS^T Q, dQ(i) = dS K
 //   bwd_post : dQ = bf16(scale * accumulator) in BSHD (a row-by-row pass for
@@ -49,6 +49,7 @@
 #include <mutex>
 
 #include "../../include/fa.h"
+#include "fa_bwd_layout.h"
 #include "fa_internal.h"
 #include "sm103_math.cuh"
 #include "sm103_ptx.cuh"
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            tmem_st16(t_lane + C::kColS + c0 / 2 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[c * 16]));
+            tmem_st16(t_lane + C::kColS + p_store_col(c0) + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[c * 16]));
         }
         tmem_wait_st();
         tc_fence_before();
@@ -845,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)  // dV += P^T dO   (P^T in TMEM, dO MN-major)
-            mma_ts_lo(tmem + C::kColDV, tmem + C::kColS + kk * 8, sdesc_step(mDO, kk * 2048), idAcc,
+            mma_ts_lo(tmem + C::kColDV, tmem + C::kColS + p_operand_col(kk), sdesc_step(mDO, kk * 2048), idAcc,
                    (st > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&ctl.do_empty);
           if (st + 1 < I.steps) {
