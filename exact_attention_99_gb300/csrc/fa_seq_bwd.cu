@@ -38,7 +38,8 @@
 //                and 64 of the tile's 128 query rows
 //     warps 8-11 dQ drain, dK/dV epilogue
 //     warp 12 TMA producer, warp 13 MMA issuer, warp 14 tail rows
-//     TMEM: S^T / P^T [0,128), dP^T / dQ [128,256), dV [256,256+d),
+//     TMEM: S^T [0,128) with P^T over columns [0,32) and [64,96)
+//           (fa_bwd_layout.h), dP^T / dQ [128,256), dV [256,256+d),
 //           dK [256+d, 256+2d)
 #include <cuda_bf16.h>
 
@@ -46,6 +47,7 @@
 #include <cmath>
 
 #include "../../include/fa.h"
+#include "fa_bwd_layout.h"
 #include "fa_internal.h"
 #include "fa_seq_plan.cuh"
 #include "sm103_math.cuh"
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 32; ++c) pk[c] = pack_bf16x2(pv[2 * c], pv[2 * c + 1]);
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            tmem_st16(t_lane + C::kColS + c0 / 2 + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[c * 16]));
+            tmem_st16(t_lane + C::kColS + p_store_col(c0) + c * 16, *reinterpret_cast<uint32_t(*)[16]>(&pk[c * 16]));
         }
         tmem_wait_st();
         tc_fence_before();
@@ -556,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)  // dV += P^T dO   (P^T in TMEM, dO MN-major)
-              mma_ts_lo(tmem + C::kColDV, tmem + C::kColS + kk * 8, sdesc_step(mDO, kk * 2048), idAcc,
-                        (st > 0 || kk > 0) ? 1u : 0u);
+              mma_ts_lo(tmem + C::kColDV, tmem + C::kColS + p_operand_col(kk), sdesc_step(mDO, kk * 2048),
+                        idAcc, (st > 0 || kk > 0) ? 1u : 0u);
             mma_commit(&ctl.do_empty);
           }
         }

@@ -7,7 +7,7 @@ import subprocess
 import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "exact_attention_99_gb300", "csrc")
-KERNELS = ["fa_bwd.cu"]
+KERNELS = ["fa_bwd.cu", "fa_seq_bwd.cu"]
 
 PROGRAM = r"""
 #include "fa_bwd_layout.h"

@@ -32,3 +32,18 @@ def test_dense(fa, B, Hq, Hkv, N, d, causal):
         again = fa.backward(q, k, v, o, lse, do, causal=causal)
         assert torch.equal(again[1], first[1]) and torch.equal(again[2], first[2])
     assert fa.fa_get_status() == 0
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,causal", [([2000, 900, 3000, 40, 1500], 16, 8, 128, True), ([4096], 4, 1, 128, False),
+                                                  ([2000, 900, 3000, 40, 1500], 16, 8, 64, True), ([700, 650], 6, 2, 64, False)])
+def test_packed(fa, lens, Hq, Hkv, d, causal):
+    g = torch.Generator(device="cuda").manual_seed(sum(lens) + d)
+    n = sum(lens)
+    q, do, k, v = normal(g, n, Hq, d), normal(g, n, Hq, d), normal(g, n, Hkv, d), normal(g, n, Hkv, d)
+    cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
+    o, lse = fa.forward_varlen(q, k, v, cu, cu, causal=causal)
+    first = fa.backward_varlen(q, k, v, o, lse, do, cu, cu, causal=causal)
+    for _ in range(30):
+        again = fa.backward_varlen(q, k, v, o, lse, do, cu, cu, causal=causal)
+        assert torch.equal(again[1], first[1]) and torch.equal(again[2], first[2])
+    assert fa.fa_get_status() == 0
