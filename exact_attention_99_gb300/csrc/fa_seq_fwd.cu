@@ -260,7 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Work* x = &ctl.it[i % kItems];
     return x->flags < 0 ? nullptr : x;
   };
-  auto release = [&](int i) { mbar_arrive(&ctl.it_empty[i % kItems]); };  // by one lane of each warp
+  // by each warp once all its lanes have read the item: warp 15 may then write the next one over it
+  auto release = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
+  };
 
   if (wg <= 1) {
     // ------------------------------------------------------------ softmax
@@ -385,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.stats_full[s]);
       }
-      __syncwarp();
-      if (lane == 0) release(i);
+      release(i);
     }
   } else if (wg == 2) {
     // ------------------------------------------------ correction + epilogue
@@ -572,8 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (row == 0) trace_stamp(p.trace, step0 - 1, 12 + s);
       }
-      __syncwarp();
-      if (lane == 0) release(i);
+      release(i);
     }
     if (lane == 0) bulk_wait_all();  // stores complete (and staging reads done) before the CTA exits
   } else {
@@ -702,8 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       base += uint32_t(2 * nt);
-      __syncwarp();
-      if (lane == 0) release(i);
+      release(i);
     }
   } else if (warp == 13) {
     // ---------------------------------------------------------- MMA issuer
@@ -850,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           step0 += nt;
         }
-        if (ok && lane == 0) release(i);
+        if (ok) release(i);
       }
       if (*abort_flag) {
         // drain the tensor pipe before TMEM is released
