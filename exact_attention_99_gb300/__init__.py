@@ -391,7 +391,9 @@ class _on:
             self.guards.append(torch.cuda.device(device))
         if stream is not None:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=torch.device("cuda", device))
+                # (0 is the default stream's handle, and ExternalStream(0) some new stream)
+                stream = (torch.cuda.ExternalStream(stream, device=torch.device("cuda", device)) if stream != 0
+                          else torch.cuda.default_stream(device))
             self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):

@@ -41,3 +41,36 @@ def test_items_without_keys_between_others(fa, hq, hk, d):
         again = fa.forward_varlen(q, k, v, *c, causal=True)
         assert torch.equal(again[0], o) and torch.equal(again[1], lse)
     assert fa.fa_get_status() == 0
+
+
+def test_a_stream_handle_of_zero_is_the_default_stream(fa, monkeypatch):
+    # the default stream's handle is 0: the call has to be made on it, and not on one of the pool's
+    (q, k, v), cu, _, _ = case([70, 9], [70, 9], 4, 2, 64, 41)
+    c = cu.cuda()
+    pages, table, lens = torch.zeros((9, 16, 2, 64), dtype=torch.bfloat16, device="cuda"), i32(0, 1, 2, 3, 4, 5, 6, 7).view(2, 4), i32(64, 9)
+    side = torch.cuda.Stream()
+    real, seen = fa.lib(), []
+
+    class Recorder:  # the library's calls, each with its stream (the last argument) noted; nothing runs
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args[-1] or 0)) or 0
+
+    def calls(stream):
+        o, lse = fa.forward_varlen(q, k, v, c, c, stream=stream)
+        fa.backward_varlen(q, k, v, o, lse, q.contiguous(), c, c, stream=stream)
+        fa.forward_paged(q, pages, pages, c, lens, table, stream=stream)
+        fa.cache_append(k, v, pages, pages, c, lens, table, stream=stream)
+
+    monkeypatch.setattr(fa, "lib", lambda: Recorder())
+    for current in (torch.cuda.default_stream(), side):
+        with torch.cuda.stream(current):
+            for given in (0, torch.cuda.default_stream(), side.cuda_stream, side):
+                seen.clear()
+                calls(given)
+                want = given if isinstance(given, int) else given.cuda_stream
+                assert [h for _, h in seen] == [want] * 4, (current, given, seen)
+                assert torch.cuda.current_stream() == current
+    monkeypatch.setattr(fa, "lib", lambda: real)
+    want = fa.forward_varlen(q, k, v, c, c)
+    got = fa.forward_varlen(q, k, v, c, c, stream=0)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and fa.fa_get_status() == 0
