@@ -60,6 +60,32 @@ int current_device() {
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// a function of the driver's, or null
+template <class Fn>
+Fn driver_function(const char* name, unsigned version) {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion(name, &fn, version, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  return reinterpret_cast<Fn>(fn);
+}
+
+// the calling thread's current context by its id (no two have the same, also
+// after one was destroyed); 0 if it has none
+unsigned long long context_id() {
+  static const auto get = driver_function<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
+  static const auto id_of = driver_function<PFN_cuCtxGetId_v12000>("cuCtxGetId", 12000);
+  CUcontext ctx = nullptr;
+  unsigned long long id = 0;
+  if (get == nullptr || id_of == nullptr || get(&ctx) != CUDA_SUCCESS || ctx == nullptr ||
+      id_of(ctx, &id) != CUDA_SUCCESS)
+    return 0;
+  return id;
+}
+
 // the copy streams of the current device, created on first use
 bool copy_streams(cudaStream_t (&out)[2 * kCopyLanes + 1]) {
   const int dev = current_device();
@@ -96,13 +122,10 @@ int check_sizes(int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int 
 int check_device() {
   const int dev = current_device();
   if (dev < 0) return FA_ERR_NO_DEVICE;
-  // a thread's first call may come before anything made the device's context
-  // current in it, and the tensor maps are encoded by the driver
-  static thread_local int bound = -1;
-  if (bound != dev) {
-    if (cudaSetDevice(dev) != cudaSuccess) return FA_ERR_NO_DEVICE;
-    bound = dev;
-  }
+  // a thread's first call may come before anything made a context current in
+  // it, and the tensor maps are encoded by the driver; a context that the
+  // caller has made current (its own, or a green one) stays
+  if (context_id() == 0 && cudaSetDevice(dev) != cudaSuccess) return FA_ERR_NO_DEVICE;
   // a device found usable stays so: its attributes are asked for once
   static std::atomic<bool> usable[kMaxDevices];
   if (usable[dev].load(std::memory_order_relaxed)) return FA_OK;
@@ -192,16 +215,7 @@ unsigned* status_word() {
 // cuTensorMapEncodeTiled from the driver, looked up once
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
+  if (!g_encode) g_encode = driver_function<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled", 12000);
   return g_encode;
 }
 
