@@ -16,8 +16,8 @@
 
 namespace fa {
 
-// Per-device status word: kernels OR error bits into it; fa_get_status reads
-// and clears it. A file-scope __device__ word (one copy per device).
+// Status word: kernels OR error bits into it; fa_get_status reads and clears
+// it. A file-scope __device__ word (one copy per context).
 __device__ unsigned g_fa_status;
 
 namespace {
@@ -48,7 +48,11 @@ struct StepSlots {
 };
 std::mutex g_step_mu;  // held for a whole fa_step_host enqueue
 StepSlots g_step[kMaxDevices];
-unsigned* g_status_ptr[kMaxDevices];
+struct StatusPtr {  // every context has a status word of its own
+  unsigned long long context;
+  unsigned* word;
+};
+StatusPtr g_status_ptr[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 DebugCfg g_debug = {kDefaultWaitNs, 0, nullptr, nullptr, nullptr, 0, 0, -1};
 
@@ -71,19 +75,6 @@ Fn driver_function(const char* name, unsigned version) {
     return nullptr;
   }
   return reinterpret_cast<Fn>(fn);
-}
-
-// the calling thread's current context by its id (no two have the same, also
-// after one was destroyed); 0 if it has none
-unsigned long long context_id() {
-  static const auto get = driver_function<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
-  static const auto id_of = driver_function<PFN_cuCtxGetId_v12000>("cuCtxGetId", 12000);
-  CUcontext ctx = nullptr;
-  unsigned long long id = 0;
-  if (get == nullptr || id_of == nullptr || get(&ctx) != CUDA_SUCCESS || ctx == nullptr ||
-      id_of(ctx, &id) != CUDA_SUCCESS)
-    return 0;
-  return id;
 }
 
 // the copy streams of the current device, created on first use
@@ -152,6 +143,17 @@ __global__ void debug_exp2_kernel(const float* x, float* y, int n, int mode) {
 
 }  // namespace
 
+unsigned long long context_id() {
+  static const auto get = driver_function<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
+  static const auto id_of = driver_function<PFN_cuCtxGetId_v12000>("cuCtxGetId", 12000);
+  CUcontext ctx = nullptr;
+  unsigned long long id = 0;
+  if (get == nullptr || id_of == nullptr || get(&ctx) != CUDA_SUCCESS || ctx == nullptr ||
+      id_of(ctx, &id) != CUDA_SUCCESS)
+    return 0;
+  return id;
+}
+
 int normalize_window(int w, int Nq, int Nk) {
   if (w < 0) return -1;
   if (1LL * w >= 1LL * Nq + Nk) return -1;
@@ -203,13 +205,15 @@ int num_sms() {
 unsigned* status_word() {
   const int dev = current_device();
   if (dev < 0) return nullptr;
+  const unsigned long long ctx = context_id();
   std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_status_ptr[dev]) {
+  StatusPtr& s = g_status_ptr[dev];
+  if (s.word == nullptr || s.context != ctx || ctx == 0) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_fa_status) != cudaSuccess) return nullptr;
-    g_status_ptr[dev] = static_cast<unsigned*>(p);
+    s = StatusPtr{ctx, static_cast<unsigned*>(p)};
   }
-  return g_status_ptr[dev];
+  return s.word;
 }
 
 // cuTensorMapEncodeTiled from the driver, looked up once

@@ -47,7 +47,11 @@ cudaMemPool_t workspace_pool();
 // Device properties cached per device.
 int num_sms();
 
-// Per-device status word (device pointer), created on first use.
+// The calling thread's current context by its id (no two have the same, also
+// after one was destroyed); 0 if it has none.
+unsigned long long context_id();
+
+// Status word of the current context (device pointer).
 unsigned* status_word();
 
 // 4-D bf16 tensor map over a BSHD tensor [B, N, H, d]: dims {d, H, N, B},

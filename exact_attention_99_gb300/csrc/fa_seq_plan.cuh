@@ -94,19 +94,20 @@ struct Plan {
   int max_units;
 };
 
-// A kernel's dynamic shared memory limit, set on each device's first launch
-// (one object per kernel).
+// A kernel's dynamic shared memory limit, set on each context's first launch
+// (one object per kernel; `done` holds the context of each device's last).
 struct SmemLimit {
-  std::atomic<bool> done[64] = {};
+  std::atomic<unsigned long long> done[64] = {};
   template <class Kernel>
   cudaError_t set(Kernel kernel, int bytes) {
     int dev = -1;
     const cudaError_t g = cudaGetDevice(&dev);
     if (g != cudaSuccess) return g;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const unsigned long long ctx = context_id();
+    if (ctx != 0 && done[dev].load(std::memory_order_relaxed) == ctx) return cudaSuccess;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    if (e == cudaSuccess) done[dev].store(ctx, std::memory_order_relaxed);
     return e;
   }
 };

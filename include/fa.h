@@ -38,8 +38,9 @@
  *              enqueued and return FA_ERR_INVALID_ARG / FA_ERR_UNSUPPORTED.
  *              A failed launch returns FA_ERR_LAUNCH. Every wait inside the
  *              kernels is bounded; a wait that runs out stops the kernel and
- *              records FA_ERR_TIMEOUT in a per-device status word that
- *              fa_get_status() returns.
+ *              records FA_ERR_TIMEOUT in a status word of the device (one per
+ *              context, where a caller uses several) that fa_get_status()
+ *              returns.
  */
 #ifndef FA_H_
 #define FA_H_

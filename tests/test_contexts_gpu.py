@@ -78,3 +78,51 @@ def test_a_thread_without_a_context(fa):
     t.join()
     assert got == [(0, 0)]
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_each_context_has_its_own_status_word(fa):
+    # appending and a small forward in a context of the caller's, with memory of that context;
+    # a wrong length there is reported there
+    torch.manual_seed(1)
+    hk, d, page, n = 2, 64, 16, 5
+    k, v, q = (torch.randn(n, h, d).to(torch.bfloat16) for h in (hk, hk, 4))
+    want = fa.forward_varlen(*(x.cuda() for x in (q, k, v)), *[torch.tensor([0, n], dtype=torch.int32, device="cuda")] * 2)
+    want = [x.cpu() for x in want]
+    assert fa.fa_get_status() == 0
+
+    def body(drv, ctx):
+        drv.cuMemAlloc_v2.argtypes = [ctypes.c_void_p, ctypes.c_size_t]
+        drv.cuMemcpyHtoD_v2.argtypes = [ctypes.c_uint64, ctypes.c_void_p, ctypes.c_size_t]
+        drv.cuMemcpyDtoH_v2.argtypes = [ctypes.c_void_p, ctypes.c_uint64, ctypes.c_size_t]
+
+        def put(t):
+            p = ctypes.c_uint64()
+            assert drv.cuMemAlloc_v2(ctypes.byref(p), t.numel() * t.element_size()) == 0
+            assert drv.cuMemcpyHtoD_v2(p.value, t.data_ptr(), t.numel() * t.element_size()) == 0
+            return p.value
+
+        def get(p, like):
+            t = torch.empty_like(like)
+            assert drv.cuMemcpyDtoH_v2(t.data_ptr(), p, t.numel() * t.element_size()) == 0
+            return t
+
+        pages = torch.full((3, page, hk, d), 7.0, dtype=torch.bfloat16)
+        dq, dk, dv, kp, vp, o = (put(x) for x in (q, k, v, pages, pages, torch.zeros_like(q)))
+        lse, cu = put(torch.zeros(4, n)), put(torch.tensor([0, n], dtype=torch.int32))
+        table, good, bad = (put(torch.tensor(x, dtype=torch.int32)) for x in ([2], [n], [n - 1]))
+
+        def append(lens):
+            return fa.fa_cache_append(dk, dv, kp, vp, cu, lens, table, 1, hk, n, 3, page, 1, d, hk * d, hk * d, stream=0)
+
+        assert append(bad) == 0 and fa.fa_get_status(0) == 1
+        assert torch.equal(get(kp, pages), pages)
+        assert append(good) == 0 and fa.fa_get_status(0) == 0
+        got = get(kp, pages)
+        assert torch.equal(got[2, :n], k) and (got[:2] == 7).all() and (got[2, n:] == 7).all()
+        assert fa.fa_fwd_varlen(dq, dk, dv, o, lse, cu, cu, 1, 4, hk, n, n, d, 4 * d, hk * d, hk * d, d ** -0.5, -1, -1,
+                                stream=0) == 0
+        assert fa.fa_get_status(0) == 0 and current(drv) == ctx
+        assert torch.equal(get(o, want[0]), want[0]) and torch.equal(get(lse, want[1]), want[1])
+
+    in_own_context(body)
+    assert fa.fa_get_status() == 0
