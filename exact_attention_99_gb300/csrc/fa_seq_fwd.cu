@@ -196,7 +196,8 @@ __device__ __forceinline__ Work work_of(const Params& p, const FwdItem* src, int
 // A lane's box of a key tile in a paged cache.
 struct Place {
   int page, in_page;
-  int boxes;  // of the tile
+  int boxes;    // of the tile
+  bool hidden;  // the box ends before the item's first visible key: its page is not looked up
 };
 
 template <int D, bool PAGED>
@@ -599,18 +600,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w == nullptr) break;
       const int nt = w->nt, kvh = w->kvh, kt = w->kt, kbase = w->kbase, klen = w->klen;
       const bool key = (w->flags & kKeyMode) != 0;
+      // The first key that a row of the item sees. The first tile begins at a
+      // multiple of 128 before it, maybe in pages that the window hides whole:
+      // a server may have given those to other sequences.
+      const int seen = PAGED && p.wl >= 0 ? w->pos - p.wl : 0;
       // Where this lane's box of tile t is. The table is read one tile ahead:
       // read as it was needed, it set the pace (3 chunks of 512 tokens over long
       // caches 228 -> 217 us, a mixed batch with pages of 16 68 -> 63 us).
       auto place = [&](int t) {
-        Place at{0, 0, 0};
+        Place at{0, 0, 0, false};
         if constexpr (PAGED) {
           // boxes that begin before the sequence's end
           const int key0 = (kt + t) * 128;
           at.boxes = min(n_box, (klen - key0 + p.box_rows - 1) / p.box_rows);
           if (t < nt && lane < at.boxes) {
             const int k = key0 + lane * p.box_rows, pg = k / p.page_size;
-            at.page = p.table[size_t(kbase) * p.max_pages + pg];
+            at.hidden = k + p.box_rows <= seen;
+            if (!at.hidden) at.page = p.table[size_t(kbase) * p.max_pages + pg];
             at.in_page = k - pg * p.page_size;
           }
         }
@@ -656,7 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (PAGED) {
           Place at = next;
           next = place(t + 1);
-          if (at.page < 0 || at.page >= p.num_pages) {  // no such page: its keys read as zeros, and the caller is told
+          if (at.hidden) {
+            at.page = p.num_pages;  // reads as zeros
+          } else if (at.page < 0 || at.page >= p.num_pages) {  // no such page: so too, and the caller is told
             atomicOr(p.status, kDevBadArg);
             at.page = p.num_pages;
           }

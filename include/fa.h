@@ -292,8 +292,10 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
  *        lens_k [B]: keys of each sequence (with its new tokens, if those are
  *        in the cache), at most max_pages * page_size
  *        page_table [B, max_pages]: key j of sequence b is row j % page_size of
- *        page page_table[b][j / page_size]; entries past its last page are
- *        not read
+ *        page page_table[b][j / page_size]. Entries past its last page are
+ *        not read, nor are those of pages that a window hides whole from all
+ *        of its new tokens (they may hold anything; v rows that the window
+ *        hides in the other pages must be finite)
  *   out: o, lse
  */
 int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse, const int* cu_q,

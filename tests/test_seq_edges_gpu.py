@@ -74,3 +74,28 @@ def test_a_stream_handle_of_zero_is_the_default_stream(fa, monkeypatch):
     want = fa.forward_varlen(q, k, v, c, c)
     got = fa.forward_varlen(q, k, v, c, c, stream=0)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and fa.fa_get_status() == 0
+
+
+@pytest.mark.parametrize("page", [16, 48, 64, 256])
+@pytest.mark.parametrize("new,keys,left", [([1] * 5, [900, 300, 131, 40, 1], 100), ([1, 200, 33], [3000, 1500, 640], 257),
+                                           ([1], [20011], 1000), ([5, 0, 300], [4, 700, 301], 0)])
+@pytest.mark.parametrize("freed", [-1, "nan"])
+def test_pages_behind_the_window_may_be_gone(fa, page, new, keys, left, freed):
+    # pages that the window hides whole from all new tokens: their entries name no page, or one of NaN
+    hq, hk, d = 8, 2, 64
+    g = su.gen(42)
+    ks, vs = ([su.normal((n, hk, d), g) for n in keys] for _ in range(2))
+    c = su.Cache(ks, vs, page, 43)
+    spare = c.ids[-1]
+    assert torch.isnan(c.k[spare].float()).all()
+    for b, (n, m) in enumerate(zip(new, keys)):
+        first = m - n - left if n else m
+        for p in range(max(0, first) // page):
+            c.k[c.table[b, p]] = c.v[c.table[b, p]] = math.nan
+            c.table[b, p] = -1 if freed == -1 else spare
+    c.cuda()
+    q, cu = su.normal((sum(new), hq, d), g), su.starts(new)
+    o, lse = fa.forward_paged(q.cuda(), c.k, c.v, cu.cuda(), c.lens, c.table, window=(left, 0))
+    assert fa.fa_get_status() == 0
+    seqs = [(q[cu[b]:cu[b + 1]], ks[b], vs[b]) for b in range(len(new))]
+    su.check_forward(o, lse, su.reference(seqs, d ** -0.5, True, (left, 0)), cu)
