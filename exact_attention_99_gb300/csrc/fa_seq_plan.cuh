@@ -28,7 +28,7 @@ namespace fa {
 namespace seq {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 1024;    // of the sort by n; units of more tiles sort as equal
+constexpr int kBuckets = 1024;    // of the sort by n: a length to each, or more where the longest passes them
 constexpr int kMaxWorkers = 256;  // CTAs of a main kernel
 constexpr int kItemCost = 2;
 
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   __shared__ __align__(16) unsigned load[kMaxWorkers];
   __shared__ int rank[kMaxWorkers], taken[Side::kRanked * kMaxWorkers];
   __shared__ unsigned long long worst;
-  __shared__ int bad;
+  __shared__ int bad, longest;
   // (no loop is unrolled: the kernel runs once per call, and fetching its code
   // takes longer than most of what it does)
   const int tid = threadIdx.x;
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   };
   if (tid == 0) {
     bad = 0;
+    longest = 0;
     worst = 0;
   }
 #pragma unroll 1
@@ -360,8 +361,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
   long long* const cost = U <= kNearUnits ? near_cost : P.cost;
   int* const order = U <= kNearUnits ? near_order : P.order;
   __syncthreads();
-  // n of each unit: running sum and histogram
+  // n of each unit: running sum, histogram and largest
   long long T = 0;
+  int most = 0;
 #pragma unroll 1
   for (int u0 = 0; u0 < U; u0 += kPlanThreads) {
     const int u = u0 + tid;
@@ -369,6 +371,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     if (u < U) {
       const int b = find_seq(ustart, B, 1, u);
       n = a.side.range(seq_of(b), u - ustart[b]).n;
+      most = max(most, n);
       atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1);
     }
     n = u < U ? n + kItemCost : 0;
@@ -377,11 +380,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     T += sum;
   }
   if (tid == 0) cost[U] = T;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) atomicMax(&longest, most);
   const long long Ttot = T * Hkv;
 #pragma unroll 1
   for (int c = tid; c <= G; c += kPlanThreads) share[c] = Ttot * c / G;
   __syncthreads();
-  // sorted order (arbitrary within a bucket, which changes no result)
+  const int width = longest / kBuckets + 1;  // lengths to a bucket
+  auto bucket = [&](int u) { return kBuckets - 1 - (int(cost[u + 1] - cost[u]) - kItemCost) / width; };
+  if (width > 1) {
+#pragma unroll 1
+    for (int i = tid; i < kBuckets; i += kPlanThreads) hist[i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int u = tid; u < U; u += kPlanThreads) atomicAdd(&hist[bucket(u)], 1);
+    __syncthreads();
+  }
   long long base = 0;
 #pragma unroll 1
   for (int i0 = 0; i0 < kBuckets; i0 += kPlanThreads) {
@@ -391,10 +405,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Side>
     base += sum;
   }
   __syncthreads();
+  // Sorted order. Units of one length may stand in any order: the workers'
+  // loads are the same. Where a bucket holds several lengths they would not be,
+  // and neither the choice between the divisions that they lead to (which round
+  // differently), so that units then stand in their own order, a warp of them
+  // after the other (some 2 us for a thousand).
+  if (width == 1) {
 #pragma unroll 1
-  for (int u = tid; u < U; u += kPlanThreads) {
-    const int n = int(cost[u + 1] - cost[u]) - kItemCost;
-    order[atomicAdd(&hist[kBuckets - 1 - min(n, kBuckets - 1)], 1)] = u;
+    for (int u = tid; u < U; u += kPlanThreads) order[atomicAdd(&hist[bucket(u)], 1)] = u;
+  } else {
+    const int lane = tid & 31;
+#pragma unroll 1
+    for (int u0 = 0; u0 < U; u0 += kPlanThreads) {
+      const int u = u0 + tid, key = u < U ? bucket(u) : -1;
+#pragma unroll 1
+      for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (tid >> 5 == w) {
+          const unsigned same = __match_any_sync(0xffffffffu, key);
+          const int first = __ffs(same) - 1;
+          int at = lane == first && key >= 0 ? atomicAdd(&hist[key], __popc(same)) : 0;
+          at = __shfl_sync(0xffffffffu, at, first);
+          if (key >= 0) order[at + __popc(same & ((1u << lane) - 1))] = u;
+        }
+        __syncthreads();
+      }
+    }
   }
   __syncthreads();
   const int n_items = U * Hkv;

@@ -1,10 +1,12 @@
 """Calls on sequences of different lengths at the edges of what fa.h allows."""
 import math
+import random
 
 import pytest
 import torch
 
 from tests import seq_util as su
+from tests import test_varlen_bwd_gpu as backward
 from tests.test_varlen_gpu import case
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +101,43 @@ def test_pages_behind_the_window_may_be_gone(fa, page, new, keys, left, freed):
     assert fa.fa_get_status() == 0
     seqs = [(q[cu[b]:cu[b + 1]], ks[b], vs[b]) for b in range(len(new))]
     su.check_forward(o, lse, su.reference(seqs, d ** -0.5, True, (left, 0)), cu)
+
+
+def long_units(B, top, seed):
+    """B sequences of one token over 1030 to `top` key tiles each, their pages taken from one small pool."""
+    rng = random.Random(seed)
+    tiles = [rng.randint(1030, top) for _ in range(B)]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    kp, vp = (torch.randn(64, 256, 1, 64, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(B, 4, 64, device="cuda", generator=g).to(torch.bfloat16)
+    table = torch.randint(0, 64, (B, top // 2 + 1), device="cuda", generator=g).to(torch.int32)
+    return q, kp, vp, su.starts([1] * B).cuda(), i32(*(128 * n - 5 for n in tiles)), table
+
+
+@pytest.mark.parametrize("B,top", [(456, 1400), (700, 1400), (1300, 1200)])
+def test_same_bits_where_units_are_longer_than_the_sort_tells_apart(fa, B, top):
+    # The plan sorts its units by their tiles, in a table of 1024 lengths. Whole or divided is decided by the
+    # sorted order's busiest worker, and here that lies at the border: any change of order among
+    # the longest would decide otherwise now and then, and divided units round otherwise.
+    # (1300 units are more than the plan keeps in shared memory.)
+    a = long_units(B, top, B * 7 + top)
+    o, lse = fa.forward_paged(*a)
+    q, kp, vp, cu, lens, table = a
+    for b in (0, B // 2, B - 1):
+        keys = table[b].long()
+        seq = [q[b:b + 1].cpu()] + [x[keys].reshape(-1, 1, 64)[:int(lens[b])].cpu() for x in (kp, vp)]
+        # (a stage's row sum takes an add to each of its 700 tiles and some 32 within one: below 2^-14)
+        su.check_forward(o[b:b + 1], lse[:, b:b + 1], su.reference([seq], 64 ** -0.5, True), [0, 1])
+    junk = torch.empty(1 << 26, device="cuda")
+    for i in range(60):
+        if i % 3 == 0:
+            junk.zero_()  # other lines in the caches, other times of arrival
+        again = fa.forward_paged(*a)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse), i
+    assert fa.fa_get_status() == 0
+
+
+def test_gradients_of_more_row_tiles_than_the_sort_tells_apart(fa):
+    # 128 query heads to a kv head: a token is a row tile
+    a, b = (backward.run(fa, [1100], [300], 128, 1, 64, seed=44, causal=False) for _ in range(2))
+    assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
