@@ -253,7 +253,9 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *   Errors   : as above for what the host can see. Lengths or pages on the
  *              device that the tensors cannot hold set FA_ERR_INVALID_ARG in the
  *              status word (fa_get_status); bad lengths: the outputs stay as
- *              they are; a bad page: it reads as zeros, or is not written.
+ *              they are (fa_cache_append: see there); a bad page: it reads as
+ *              zeros, or is not written. Without rows (total_q = 0; the
+ *              backward: nor keys) nothing is launched and no length read.
  */
 
 /*
@@ -308,7 +310,12 @@ int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* 
  *   b goes to place lens_k[b] - n_b + i of the sequence (lens_k: the lengths
  *   with the new tokens, as fa_fwd_paged takes them next; n_b <= lens_k[b]).
  *   Every other row of the pages stays as it is. Two rows that the table
- *   sends to one place leave either's values. Needs no workspace.
+ *   sends to one place leave a mixture (every 16 bytes are one's or the
+ *   other's). Needs no workspace.
+ *   Wrong lengths, also those of a sequence without new tokens, set
+ *   FA_ERR_INVALID_ARG in the status word. Unlike the other calls this one then
+ *   still writes the sequences whose own lengths are right; where offsets are
+ *   not in order and two such sequences claim a row, it goes to one of them.
  */
 int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, const int* cu_q, const int* lens_k,
                     const int* page_table, int B, int Hkv, int total_q, int num_pages, int page_size, int max_pages,

@@ -141,3 +141,38 @@ def test_gradients_of_more_row_tiles_than_the_sort_tells_apart(fa):
     # 128 query heads to a kv head: a token is a row tile
     a, b = (backward.run(fa, [1100], [300], 128, 1, 64, seed=44, causal=False) for _ in range(2))
     assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+
+
+def test_append_reports_every_wrong_length(fa):
+    # also those that no token's own sequence shows: offsets out of order, a sequence without new tokens
+    hk, d, page, total, B = 2, 64, 16, 8, 600
+    g = su.gen(45)
+    k, v = (su.normal((total, hk, d), g).cuda() for _ in range(2))
+    start = su.normal((3, page, hk, d), g).cuda()
+    table = i32(0, 1, 2).view(3, 1)
+
+    def run(cu, lens, table):
+        kp, vp = start.clone(), start.clone()
+        fa.cache_append(k, v, kp, vp, cu, lens, table)
+        return fa.fa_get_status(), kp, vp
+
+    for cu, lens in ((i32(0, 5, 3, 8), i32(5, 5, 5)), (i32(0, 0, 8, 8), i32(-1, 8, 3)), (i32(0, 8, 8, 8), i32(8, 4, 17)),
+                     (i32(0, 8, 8, 9), i32(8, 4, 4)), (i32(-2, 0, 8, 8), i32(2, 8, 4))):
+        st, kp, vp = run(cu, lens, table)
+        assert st == FA_ERR_INVALID_ARG, (cu, lens)
+    # the right sequence among them is written, and nothing else
+    st, kp, vp = run(i32(0, 0, 8, 8), i32(-1, 8, 3), table)
+    for got, x in ((kp, k), (vp, v)):
+        want = start.clone()
+        want[1, :8] = x
+        assert torch.equal(got, want)
+    # more sequences than a block looks over
+    many = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    cu, lens = torch.zeros(B + 1, dtype=torch.int32, device="cuda"), torch.full((B,), 3, dtype=torch.int32, device="cuda")
+    cu[1:], lens[0] = total, total
+    assert run(cu, lens, many)[0] == 0
+    for at in (1, 223, 224, 255, 256, 448, B - 1):
+        bad = lens.clone()
+        bad[at] = page + 1
+        assert run(cu, bad, many)[0] == FA_ERR_INVALID_ARG, at
+    assert run(cu, lens, many)[0] == 0
