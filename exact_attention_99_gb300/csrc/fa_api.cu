@@ -509,7 +509,7 @@ extern "C" int fa_cache_append(const void* k, const void* v, void* k_pages, void
   int st = check_seq_sizes(B, Hkv, Hkv, total_q, d);
   if (st == FA_OK) st = check_pages(num_pages, page_size, max_pages, Hkv, d);
   // the values of a block's tokens are counted in 32 bits (8 rows in pieces of 8 values)
-  if (st == FA_OK && 1LL * Hkv * d >= (1LL << 31)) st = FA_ERR_UNSUPPORTED;
+  if (st == FA_OK && 1LL * Hkv * d >= (1LL << 30)) st = FA_ERR_UNSUPPORTED;
   if (st != FA_OK) return st;
   if (!aligned4(cu_q) || !aligned4(lens_k) || !aligned4(page_table)) return FA_ERR_INVALID_ARG;
   if (total_q > 0 && (!aligned16(k) || !aligned16(v))) return FA_ERR_INVALID_ARG;
