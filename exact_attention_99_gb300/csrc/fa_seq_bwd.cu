@@ -107,6 +107,7 @@ struct Params {
   int wl, wr;
   float scale, scale_log2;
   unsigned long long wait_limit_ns;
+  int inject;
   unsigned* status;
 };
 
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 12) {
     // ------------------------------------------------------- TMA producer
-    bool ok = true;
+    bool ok = true, inject = p.inject == 1;  // test hook: the first Q tile is never delivered
     int g = 0, nkv = 0;
     const uint32_t row_bytes = uint32_t(p.tok * p.group * D * 2);
     while (ok && next_item(p, wk, &ctl.cur[warp], lane)) {
@@ -471,7 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qs = g & 1, token = token0 + st * p.tok;
         ok = seq::warp_wait(&ctl.q_empty[qs], ((g >> 1) & 1) ^ 1, abort_flag, LIM);
         if (!ok) break;
-        if (elect_one()) {
+        if (inject) {
+          inject = false;
+        } else if (elect_one()) {
           mbar_arrive_expect_tx(&ctl.q_full[qs], row_bytes);
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
@@ -947,6 +950,7 @@ cudaError_t launch_t(const SeqProblem& pb, const void* o, const float* lse, cons
   p.scale_log2 = pb.scale * 1.4426950408889634f;
   const DebugCfg dc = debug_cfg();
   p.wait_limit_ns = dc.wait_limit_ns;
+  p.inject = dc.inject;
   p.status = status;
   if (e == cudaSuccess) {
     seq::plan_kernel<seq::BwdSide><<<1, seq::kPlanThreads, 0, stream>>>(a);

@@ -337,10 +337,10 @@ const char* fa_status_string(int status);
 /*
  * Test hooks (not for production use).
  * fa_debug_set — wait_limit_ns: per-wait time limit of every kernel (0
- *   restores the default of 2 s). inject: 0 = off; 1 = the forward producer
- *   never issues its first K-tile load, so the consumer's bounded wait must
- *   run out and the kernel must report FA_ERR_TIMEOUT and exit cleanly.
- *   Process-wide; not thread-safe.
+ *   restores the default of 2 s). inject: 0 = off; 1 = the forward's producer
+ *   never issues its first K-tile load (that of fa_bwd_varlen its first Q
+ *   tile), so the consumer's bounded wait must run out and the kernel must
+ *   report FA_ERR_TIMEOUT and exit cleanly. Process-wide; not thread-safe.
  * fa_debug_exp2 — y[i] = 2^x[i] for n device floats, evaluated by the
  *   kernels' own device routine: mode 0 = ex2.approx on the special-function
  *   unit, mode 1 = the fitted polynomial on the FMA pipes.

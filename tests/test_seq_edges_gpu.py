@@ -176,3 +176,23 @@ def test_append_reports_every_wrong_length(fa):
         bad[at] = page + 1
         assert run(cu, bad, many)[0] == FA_ERR_INVALID_ARG, at
     assert run(cu, lens, many)[0] == 0
+
+
+@pytest.mark.parametrize("lens,hq,hk,d", [([300], 2, 1, 128), ([40, 700, 0, 129], 16, 8, 64)])
+def test_a_wait_of_the_backward_that_runs_out_is_reported(fa, lens, hq, hk, d):
+    # the producer never delivers a tile of Q: every wait is bounded, the call ends with a status,
+    # and the next one is as ever
+    run = lambda: backward.run(fa, lens, lens, hq, hk, d, seed=46)  # noqa: E731
+    a = run()
+    (q, k, v), cu, _, _ = case(lens, lens, hq, hk, d, 46)
+    c = cu.cuda()
+    o, lse = fa.forward_varlen(q, k, v, c, c, causal=True)
+    assert fa.fa_get_status() == 0
+    assert fa.fa_debug_set(20_000_000, 1) == 0
+    try:
+        fa.backward_varlen(q, k, v, o, lse, o, c, c, causal=True)
+        assert fa.fa_get_status() == FA_ERR_TIMEOUT
+    finally:
+        fa.fa_debug_set(0, 0)
+    b = run()
+    assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
