@@ -108,6 +108,12 @@ struct SeqProblem {
   float scale;
   int window_left, window_right;  // -1: no limit
 };
+// Tiles of 128 / group tokens that B sequences of total_q tokens fill at most,
+// each its last one in part.
+inline long long seq_row_tiles(const SeqProblem& p) {
+  const long long tiles = p.total_q / (128 / (p.Hq / p.Hkv)) + 1LL * p.B;
+  return tiles < p.total_q ? tiles : p.total_q;
+}
 // cudaErrorMemoryAllocation: the workspace could not be allocated
 cudaError_t launch_seq_fwd(const SeqProblem& p, void* o, float* lse, cudaStream_t stream);
 cudaError_t launch_seq_bwd(const SeqProblem& p, const void* o, const float* lse, const void* dout, void* dq, void* dk,

@@ -845,12 +845,11 @@ struct Space {
   int tile_cap;
   size_t bytes;
 };
-Space carve(uint8_t* base, const SeqProblem& pb, int G, int tok) {
+Space carve(uint8_t* base, const SeqProblem& pb, int G) {
   Space s{};
   seq::Carver c{base, 0};
-  long long units = pb.total_k / 128 + pb.B, tiles = pb.total_q / tok + pb.B;
+  long long units = pb.total_k / 128 + pb.B, tiles = seq_row_tiles(pb);
   if (units > pb.total_k) units = pb.total_k;
-  if (tiles > pb.total_q) tiles = pb.total_q;
   if (tiles < 1) tiles = 1;  // (tensor maps need a row)
   s.tile_cap = int(tiles);
   s.plan = seq::carve_plan<BwdItem>(c, pb.B, units, pb.Hkv, G);
@@ -879,9 +878,9 @@ cudaError_t launch_t(const SeqProblem& pb, const void* o, const float* lse, cons
   if (e != cudaSuccess) return e;
   void* ws = nullptr;
   cudaMemPool_t pool = workspace_pool();
-  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr, pb, G, tok).bytes, pool, stream) != cudaSuccess)
+  if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr, pb, G).bytes, pool, stream) != cudaSuccess)
     return cudaErrorMemoryAllocation;
-  const Space sp = carve(static_cast<uint8_t*>(ws), pb, G, tok);
+  const Space sp = carve(static_cast<uint8_t*>(ws), pb, G);
   CUtensorMap mq, mk, mv, mdo;
   OutMaps out;
   bool ok = true;

@@ -245,7 +245,10 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *              sequences, unused rows of a page) is never used, whatever its
  *              bits; v rows that only the window hides must be finite.
  *   Sizes    : B >= 1, total_q, total_k >= 0 (0: nothing, or no keys at all),
- *              Hq % Hkv == 0, Hq / Hkv <= 128, d in {64, 128}, any finite scale.
+ *              Hq % Hkv == 0, Hq / Hkv <= 128, d in {64, 128}, any finite scale;
+ *              counts are held in 32 bits (total * Hq below 2^31, (total + B) *
+ *              Hkv below 2^30), tensors below 2^40 bytes, else
+ *              FA_ERR_UNSUPPORTED.
  *   Workspace: from the per-device pool that fa_bwd uses, on `stream`: 40 MB
  *              at d = 128 and 20 MB at d = 64 for the parts of divided work, and
  *              about 40 bytes per block of 128 rows and kv head for the plan.
@@ -277,8 +280,15 @@ int fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, float* l
  * dk and dv are sums over the query heads of a group, taken in a fixed order;
  * the additions into dq are not ordered (as in fa_bwd). q, k, v and dout of a
  * sequence's rows must be finite, also where only the window hides them
- * (a hidden probability is 0, and 0 times them is added). Workspace: fp32 dQ
- * (about 4 * total_q * Hq * d bytes) and 40 MB at d = 128 for parts.
+ * (a hidden probability is 0, and 0 times them is added). Workspace: the parts
+ * and the plan (of key tiles here) as above, and an fp32 dQ that is padded to
+ * whole tiles of 128 rows for every sequence and kv head, with T = 128 / (Hq /
+ * Hkv) tokens to a tile:
+ *   512 * (d + 2) * Hkv * min(total_q / T + B, total_q) bytes.
+ * That is about 4 * total_q * Hq * d where sequences are long beside T, and up
+ * to T times as much where they are a token each (4000 of them, 32 query and 8
+ * kv heads, d = 128: 2.1 GB); the time of the passes that clear and read it
+ * grows alike. 128 * Hkv * min(...) below 2^31, else FA_ERR_UNSUPPORTED.
  */
 int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
                   void* dq, void* dk, void* dv, const int* cu_q, const int* cu_k, int B, int Hq, int Hkv, int total_q,
