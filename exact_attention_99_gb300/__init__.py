@@ -168,7 +168,8 @@ def forward_fp8(q, k, v, causal: bool = False, scale: float | None = None, incoh
 
 def _window_args(causal, window):
     """(left, right) bounds for the *_window calls; causal caps right at 0."""
-    wl, wr = (-1, -1) if window is None else (int(window[0]), int(window[1]))
+    # (C ints: a bound past 31 bits is past every length, any negative one is no limit)
+    wl, wr = (-1, -1) if window is None else (max(-1, min(int(w), 2 ** 31 - 1)) for w in window)
     if causal:
         wr = 0 if wr < 0 else min(wr, 0)
     return wl, wr

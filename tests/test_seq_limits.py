@@ -24,3 +24,13 @@ def test_backward_refuses_more_padded_rows_than_its_counts_hold(fa):
 def test_backward_takes_many_empty_sequences(fa):
     # no more tiles than tokens, however many sequences there are
     assert call(fa, "fa_bwd_varlen", B=1 << 25, Hq=2, Hkv=1, total_q=10, total_k=10) == FA_ERR_NO_DEVICE
+
+
+@pytest.mark.parametrize("window,causal,want", [((5, 7), False, (5, 7)), ((-1, -9), False, (-1, -1)), (None, True, (-1, 0)),
+                                                ((4, 7), True, (4, 0)), ((4, -1), True, (4, 0)),
+                                                ((2 ** 31, 2 ** 31 - 1), False, (2 ** 31 - 1, 2 ** 31 - 1)),
+                                                ((2 ** 32 + 5, 2 ** 63 - 1), False, (2 ** 31 - 1, 2 ** 31 - 1)),
+                                                ((-2 ** 32 + 5, -2 ** 63), False, (-1, -1))])
+def test_window_bounds_past_32_bits(fa, window, causal, want):
+    # (ctypes would take their low 32 bits)
+    assert fa._window_args(causal, window) == want
