@@ -43,9 +43,16 @@ import workloads  # noqa: E402
 MAIN = workloads.BY_NAME["fwd_causal_gqa_b1_hq32_hkv8_n16384_d128"]
 METRIC = "attention fwd/bwd TFLOP/s at 1 GB300 and fraction of dense BF16 tensor peak"
 FLUSH_BYTES = 256 << 20
-KERNEL_SOURCES = {"fa_fwd_kernel": ("fa_fwd.cu", "fa_fwd_pipeline.cuh"), "bwd_main_kernel": ("fa_bwd.cu",),
+KERNEL_SOURCES = {"fa_fwd_kernel": ("fa_fwd.cu", "fa_fwd_pipeline.cuh"),
+                  "bwd_main_kernel": ("fa_bwd.cu", "fa_bwd_layout.h"),
                   "fa_fwd8_kernel": ("fa_fwd8.cu", "fa_fwd_pipeline.cuh"),
-                  "fa_fwd_pair_kernel": ("fa_fwd.cu", "fa_fwd_pipeline.cuh")}
+                  "fa_fwd_pair_kernel": ("fa_fwd.cu", "fa_fwd_pipeline.cuh"),
+                  "seq_fwd_kernel": ("fa_seq_fwd.cu", "fa_seq_plan.cuh", "fa_seq.cuh"),
+                  "seq_bwd_kernel": ("fa_seq_bwd.cu", "fa_seq_plan.cuh", "fa_seq.cuh", "fa_bwd_layout.h")}
+# profiling targets of the packed calls: causal sequences one behind the other
+PACKED_CASES = {"packed_causal_b1_hq32_hkv8_n16384_d128": dict(lens=[16384], Hq=32, Hkv=8, d=128, seed=1050),
+                "packed_causal_b1_hq32_hkv8_n16384_d64": dict(lens=[16384], Hq=32, Hkv=8, d=64, seed=1051),
+                "packed_causal_b2_hq32_hkv8_n4096_d128": dict(lens=[4096, 4096], Hq=32, Hkv=8, d=128, seed=1052)}
 PANEL = 1024  # query rows of one oracle sample
 
 
@@ -752,6 +759,8 @@ def run_profile_target(args):
     fa.fa_debug_set(0, 0)
     if fa.fa_tune(fa.TUNE_EXP2_SPLIT, args.exp2_split) or fa.fa_tune(fa.TUNE_CTA_PAIRS, int(args.cta_pairs)):
         raise ValueError("bad --exp2-split")
+    if args.profile_workload in PACKED_CASES:
+        return run_packed_profile_target(fa, args, PACKED_CASES[args.profile_workload])
     if args.profile_workload == WINDOW_CASE["name"]:
         c = WINDOW_CASE
         x = workloads.make_inputs(c["B"], c["H"], c["H"], c["N"], c["N"], c["d"], c["seed"], with_dout=True)
@@ -778,6 +787,25 @@ def run_profile_target(args):
             bwd_call(q, k, v, o, lse, do, dq, dk, dv, *a)
         if st:
             raise RuntimeError(f"launch failed: {st}")
+    torch.cuda.synchronize()
+    if fa.fa_get_status() != 0:
+        raise RuntimeError("device status not OK")
+
+
+def run_packed_profile_target(fa, args, c):
+    """run_profile_target for a case of the packed calls (fwd or bwd)."""
+    import torch
+    if args.profile_pass == "fwd8":
+        raise ValueError("fwd8 profiles the dense calls only")
+    x = workloads.make_inputs(1, c["Hq"], c["Hkv"], sum(c["lens"]), sum(c["lens"]), c["d"], c["seed"], with_dout=True)
+    q, k, v, do = (x[n][0].cuda() for n in ("q", "k", "v", "do"))
+    cu = torch.tensor([0] + c["lens"], device="cuda").cumsum(0).to(torch.int32)
+    o, lse = fa.forward_varlen(q, k, v, cu, cu, causal=True)
+    for _ in range(args.warmup + args.steps):
+        if args.profile_pass == "fwd":
+            fa.forward_varlen(q, k, v, cu, cu, causal=True, out=(o, lse))
+        else:
+            fa.backward_varlen(q, k, v, o, lse, do, cu, cu, causal=True)
     torch.cuda.synchronize()
     if fa.fa_get_status() != 0:
         raise RuntimeError("device status not OK")

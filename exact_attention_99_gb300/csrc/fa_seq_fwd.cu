@@ -40,12 +40,15 @@
 //     tokens, 32 query and 8 kv heads: 1.29 ms, 1710 TFLOP/s, 0.89 of the
 //     measured bf16 matrix product rate (the dense forward: 1.64 ms).
 //   d = 64: the softmax's latency. The same sequence takes 1.15 ms (dense 1.42);
-//     the schedulers issue in 42 % of the cycles, tensor pipe 35 %.
+//     the schedulers issue in 47 % of the cycles, tensor pipe 40 %, exponentials
+//     41 %. (A thread spills 12 bytes; at d = 128 none.)
 //   single tokens: the cache's bytes. 64 sequences of 300 to 32000 keys, 8 kv
 //     heads of 128: 1.70 GB in 258 us, 6.6 TB/s, 0.97 of the measured copy.
 //   items of few tiles: 1.3 to 2.3 us between two items, most of it instruction
 //     fetch (code that runs once per item is not in the cache) and the first
-//     S; small calls: the launches (77 tokens: 8 us).
+//     S; with a window and one query head per kv head the first and the last
+//     of an item's key tiles, which one stage alone sees; the plan before the
+//     first item (11 to 15 us); small calls: the launches (77 tokens: 8 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>
