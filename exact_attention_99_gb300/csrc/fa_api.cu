@@ -469,7 +469,7 @@ extern "C" int fa_bwd_varlen(const void* q, const void* k, const void* v, const 
     st = FA_ERR_INVALID_ARG;
   if (st == FA_OK && total_k > 0 && (!aligned16(dk) || !aligned16(dv))) st = FA_ERR_INVALID_ARG;
   // rows of the padded accumulator are counted in 32 bits
-  if (st == FA_OK && 128 * Hkv * seq_row_tiles(p) >= (1LL << 31)) st = FA_ERR_UNSUPPORTED;
+  if (st == FA_OK && 128LL * Hkv * seq_row_tiles(p) >= (1LL << 31)) st = FA_ERR_UNSUPPORTED;
   if (st == FA_OK) st = check_device();
   if (st != FA_OK || (total_q == 0 && total_k == 0)) return st;
   return seq_result(launch_seq_bwd(p, o, lse, dout, dq, dk, dv, static_cast<cudaStream_t>(stream)));

@@ -34,3 +34,10 @@ def test_backward_takes_many_empty_sequences(fa):
 def test_window_bounds_past_32_bits(fa, window, causal, want):
     # (ctypes would take their low 32 bits)
     assert fa._window_args(causal, window) == want
+
+
+@pytest.mark.parametrize("heads", [1 << 24, 1 << 25, 1 << 28])
+def test_backward_refuses_rows_of_many_heads(fa, heads):
+    # one token: a tile of 128 rows to each kv head
+    assert call(fa, "fa_bwd_varlen", B=1, Hq=heads, Hkv=heads, total_q=1, total_k=1, d=64, q_stride=64 * heads,
+                k_stride=64 * heads, v_stride=64 * heads) == FA_ERR_UNSUPPORTED
