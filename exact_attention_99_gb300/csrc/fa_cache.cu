@@ -11,6 +11,8 @@
 // single tokens: 4 us, a launch.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "fa_internal.h"
 #include "fa_seq.cuh"
 #include "sm103_ptx.cuh"
@@ -19,6 +21,7 @@ namespace fa {
 namespace {
 
 constexpr int kRows = 8, kThreads = 256;
+constexpr int kOthers = kThreads - 32;  // the threads that look over the sequences
 
 struct AppendArgs {
   const uint4* k;
@@ -66,7 +69,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     }
     to[tid] = at;
   } else if (tid >= 32) {
-    constexpr int kOthers = kThreads - 32;
     bool ok = true;
 #pragma unroll 1
     for (long long b = 1LL * blockIdx.x * kOthers + tid - 32; b < a.L.B; b += 1LL * gridDim.x * kOthers) {
@@ -105,7 +107,9 @@ cudaError_t launch_cache_append(const AppendProblem& pb, cudaStream_t stream) {
   a.v_stride16 = pb.v_stride / 8;
   a.status = status_word();
   if (a.status == nullptr) return cudaErrorLaunchFailure;
-  append_kernel<<<unsigned((1LL * pb.total_q + kRows - 1) / kRows), kThreads, 0, stream>>>(a);
+  // a block to 8 tokens; where few tokens go into many sequences, as many as look over those at once
+  const int look = std::min((pb.B + kOthers - 1) / kOthers, 2 * num_sms());
+  append_kernel<<<unsigned(std::max((pb.total_q + kRows - 1) / kRows, look)), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
