@@ -247,7 +247,8 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  *   Sizes    : B >= 1, total_q, total_k >= 0 (0: nothing, or no keys at all),
  *              Hq % Hkv == 0, Hq / Hkv <= 128, d in {64, 128}, any finite scale;
  *              counts are held in 32 bits (total * Hq below 2^31, (total + B) *
- *              Hkv below 2^30), tensors below 2^40 bytes, else
+ *              Hkv below 2^30; fa_cache_append: Hkv * d below 2^30), tensors
+ *              below 2^40 bytes, max_pages * page_size at most 2^28, else
  *              FA_ERR_UNSUPPORTED.
  *   Workspace: from the per-device pool that fa_bwd uses, on `stream`: 40 MB
  *              at d = 128 and 20 MB at d = 64 for the parts of divided work, and
