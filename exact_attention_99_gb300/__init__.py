@@ -20,7 +20,8 @@ import os
 __all__ = ["FAError", "lib", "fa_fwd", "fa_bwd", "fa_bwd_noalloc", "fa_bwd_launches", "fa_get_status", "fa_status_string", "fa_debug_set",
            "fa_debug_exp2", "fa_tune", "TUNE_EXP2_SPLIT", "TUNE_CTA_PAIRS", "TUNE_BWD_SPLIT", "fa_profile_events", "fa_trace", "forward", "backward", "STATUS",
            "fa_fwd_varlen", "fa_bwd_varlen", "fa_fwd_paged", "fa_cache_append", "forward_varlen", "backward_varlen",
-           "forward_paged", "cache_append"]
+           "forward_paged", "cache_append", "fa_fwd_paged_fp8", "fa_cache_append_fp8", "fa_rotary", "forward_paged_fp8",
+           "cache_append_fp8", "rotary", "rotary_backward", "rotary_frequencies"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfa.so")
@@ -78,6 +79,12 @@ def lib() -> ctypes.CDLL:
         L.fa_fwd_paged.restype = i
         L.fa_cache_append.argtypes = [vp] * 7 + [i] * 7 + [ll, ll, vp]
         L.fa_cache_append.restype = i
+        L.fa_fwd_paged_fp8.argtypes = [vp] * 10 + [i] * 8 + [ll, f, i, i, vp]
+        L.fa_fwd_paged_fp8.restype = i
+        L.fa_cache_append_fp8.argtypes = [vp] * 9 + [i] * 7 + [ll, ll, vp]
+        L.fa_cache_append_fp8.restype = i
+        L.fa_rotary.argtypes = [vp] * 7 + [i] * 6 + [ll] * 4 + [f, i, i, vp]
+        L.fa_rotary.restype = i
         L.fa_get_status.argtypes = [vp]
         L.fa_get_status.restype = i
         L.fa_status_string.argtypes = [i]
@@ -330,13 +337,35 @@ def fa_cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, B, Hkv, to
                                  v_stride, _stream(stream))
 
 
-_bf16 = _i32 = _f32 = _empty = None
+def fa_fwd_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, o, lse, cu_q, lens_k, page_table, B, Hq, Hkv, total_q,
+                     num_pages, page_size, max_pages, d, q_stride, scale, window_left, window_right, stream=None) -> int:
+    return lib().fa_fwd_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(o),
+                                  _ptr(lse), _ptr(cu_q), _ptr(lens_k), _ptr(page_table), B, Hq, Hkv, total_q, num_pages,
+                                  page_size, max_pages, d, q_stride, float(scale), int(window_left), int(window_right),
+                                  _stream(stream))
+
+
+def fa_cache_append_fp8(k, v, k_pages, v_pages, k_scales, v_scales, cu_q, lens_k, page_table, B, Hkv, total_q, num_pages,
+                        page_size, max_pages, d, k_stride, v_stride, stream=None) -> int:
+    return lib().fa_cache_append_fp8(_ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales),
+                                     _ptr(cu_q), _ptr(lens_k), _ptr(page_table), B, Hkv, total_q, num_pages, page_size,
+                                     max_pages, d, k_stride, v_stride, _stream(stream))
+
+
+def fa_rotary(q, k, q_out, k_out, inv_freq, cu_q, lens, B, Hq, Hk, total, d, rot, q_stride, k_stride, q_out_stride,
+              k_out_stride, mscale, interleaved, transposed, stream=None) -> int:
+    return lib().fa_rotary(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(inv_freq), _ptr(cu_q), _ptr(lens), B, Hq, Hk,
+                           total, d, rot, q_stride, k_stride, q_out_stride, k_out_stride, float(mscale), int(interleaved),
+                           int(transposed), _stream(stream))
+
+
+_bf16 = _i32 = _f32 = _e4m3 = _empty = None
 
 
 def _types():
-    global _bf16, _i32, _f32, _empty
+    global _bf16, _i32, _f32, _e4m3, _empty
     import torch
-    _bf16, _i32, _f32, _empty = torch.bfloat16, torch.int32, torch.float32, torch.empty
+    _bf16, _i32, _f32, _e4m3, _empty = torch.bfloat16, torch.int32, torch.float32, torch.float8_e4m3fn, torch.empty
 
 
 def _tokens(name, t, device, shape):
@@ -371,12 +400,12 @@ def _packed(name, t, shape, device, dtype=None):
         raise ValueError(f"{name} must be a contiguous {dtype or _bf16} tensor of shape {tuple(shape)} on cuda:{device}")
 
 
-def _pages(k_pages, v_pages, hkv, d, device):
+def _pages(k_pages, v_pages, hkv, d, device, dtype=None):
     shape = k_pages.shape
     if len(shape) != 4 or shape[2] != hkv or shape[3] != d:
         raise ValueError(f"k_pages must have the shape [pages, page_size, {hkv}, {d}]")
-    _packed("k_pages", k_pages, shape, device)
-    _packed("v_pages", v_pages, shape, device)
+    _packed("k_pages", k_pages, shape, device, dtype)
+    _packed("v_pages", v_pages, shape, device, dtype)
     return shape[0], shape[1]
 
 
@@ -505,9 +534,9 @@ def backward_varlen(q, k, v, o, lse, dout, cu_q, cu_k, causal: bool = False, sca
         return _bwd_varlen(_current_stream(), q, k, v, o, lse, dout, cu_q, cu_k, out, shape, kshape, strides, scale, wl, wr)
 
 
-def _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, d, device):
-    """Checks shared by forward_paged and cache_append: B, pages, page size, pages of a sequence."""
-    num_pages, page_size = _pages(k_pages, v_pages, hkv, d, device)
+def _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, d, device, dtype=None):
+    """Checks shared by the calls over a paged cache: B, pages, page size, pages of a sequence."""
+    num_pages, page_size = _pages(k_pages, v_pages, hkv, d, device, dtype)
     shape = page_table.shape
     if len(shape) != 2:
         raise ValueError("page_table must have the shape [sequences, pages]")
@@ -574,3 +603,187 @@ def cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, stream=None) 
         return _append(s, k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)
     with _on(device, stream):
         _append(_current_stream(), k, v, k_pages, v_pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)
+
+
+# --- a cache in 8 bits (see fa.h) -----------------------------------------------
+
+def _cache8_args(k_pages, v_pages, k_scales, v_scales, cu_q, lens_k, page_table, hkv, d, device):
+    """_cache_args of an e4m3 cache, with its scales."""
+    sizes = _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, d, device, _e4m3)
+    shape = (sizes[1], sizes[2] // 16, hkv)
+    _packed("k_scales", k_scales, shape, device, _f32)
+    _packed("v_scales", v_scales, shape, device, _f32)
+    return sizes
+
+
+def _fwd_paged8(stream, q, pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes, scale, wl, wr):
+    o, lse = _seq_out(q, shape, out)
+    total_q, hq, d = shape
+    B, num_pages, page_size, max_pages = sizes
+    st = lib().fa_fwd_paged_fp8(q.data_ptr(), *(x.data_ptr() for x in pages), o.data_ptr(), lse.data_ptr(),
+                                cu_q.data_ptr(), lens_k.data_ptr(), page_table.data_ptr(), B, hq, hkv, total_q,
+                                num_pages, page_size, max_pages, d, qs, scale, wl, wr, stream)
+    if st != 0:
+        raise FAError(st, "fa_fwd_paged_fp8")
+    return o, lse
+
+
+def forward_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, cu_q, lens_k, page_table, causal: bool = True,
+                      scale: float | None = None, out=None, stream=None, window=None):
+    """forward_paged over a cache in 8 bits: pages [num_pages, page_size, Hkv, d]
+    of torch.float8_e4m3fn, scales [num_pages, page_size / 16, Hkv] fp32 (see fa.h
+    fa_fwd_paged_fp8)."""
+    device = _first("q", q)
+    shape = q.shape
+    qs = _tokens("q", q, device, shape)
+    hkv = k_pages.shape[2] if k_pages.dim() == 4 else 0
+    sizes = _cache8_args(k_pages, v_pages, k_scales, v_scales, cu_q, lens_k, page_table, hkv, shape[2], device)
+    scale = 1.0 / math.sqrt(shape[2]) if scale is None else scale
+    wl, wr = (-1, 0 if causal else -1) if window is None else _window_args(causal, window)
+    pages = (k_pages, v_pages, k_scales, v_scales)
+    s = _here(device, stream)
+    if s is not None:
+        return _fwd_paged8(s, q, pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes, scale, wl, wr)
+    with _on(device, stream):
+        return _fwd_paged8(_current_stream(), q, pages, cu_q, lens_k, page_table, out, shape, qs, hkv, sizes, scale, wl, wr)
+
+
+def _append8(stream, k, v, pages, cu_q, lens_k, page_table, shape, ks, vs, sizes):
+    total, hkv, d = shape
+    B, num_pages, page_size, max_pages = sizes
+    st = lib().fa_cache_append_fp8(k.data_ptr(), v.data_ptr(), *(x.data_ptr() for x in pages), cu_q.data_ptr(),
+                                   lens_k.data_ptr(), page_table.data_ptr(), B, hkv, total, num_pages, page_size,
+                                   max_pages, d, ks, vs, stream)
+    if st != 0:
+        raise FAError(st, "fa_cache_append_fp8")
+
+
+def cache_append_fp8(k, v, k_pages, v_pages, k_scales, v_scales, cu_q, lens_k, page_table, stream=None) -> None:
+    """k, v [total_q, Hkv, d] of new tokens (bf16, CUDA; tokens may be strided)
+    into the pages of a cache in 8 bits, in place, with a scale for each block
+    of 16 tokens and head (see fa.h fa_cache_append_fp8)."""
+    device = _first("k", k)
+    shape = k.shape
+    ks, vs = _tokens("k", k, device, shape), _tokens("v", v, device, shape)
+    sizes = _cache8_args(k_pages, v_pages, k_scales, v_scales, cu_q, lens_k, page_table, shape[1], shape[2], device)
+    pages = (k_pages, v_pages, k_scales, v_scales)
+    s = _here(device, stream)
+    if s is not None:
+        return _append8(s, k, v, pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)
+    with _on(device, stream):
+        _append8(_current_stream(), k, v, pages, cu_q, lens_k, page_table, shape, ks, vs, sizes)
+
+
+# --- rotary positions (see fa.h) --------------------------------------------------
+
+def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                       original_length: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq, mscale) for `rotary`: dim / 2 inverse frequencies (fp32, on
+    the CPU) and the factor of the turned values, computed in 64 bits.
+
+    f_j = base^(-2 j / dim). `scaling`, for contexts `factor` times as long as
+    those that a model was made for:
+      None       f_j;
+      "linear"   f_j / factor: all places are drawn together;
+      "ntk"      the base times factor^(dim / (dim - 2)): the slowest pair turns
+                 by 1 / factor, the fastest as before;
+      "yarn"     between f_j and f_j / factor by how often the pair turns within
+                 original_length places: f_j from beta_fast turns on, f_j /
+                 factor up to beta_slow, a line over j between; mscale is
+                 0.1 ln(factor) + 1.
+    """
+    import torch
+    if dim < 2 or dim % 2 or not base > 1.0 or not math.isfinite(base):
+        raise ValueError("rotary_frequencies: dim must be even and base finite and above 1")
+    if not (math.isfinite(factor) and factor >= 1.0):
+        raise ValueError("rotary_frequencies: factor must be finite and 1 at least")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"rotary_frequencies: no scaling {scaling!r}")
+    mscale = 1.0
+    if scaling == "ntk" and dim > 2:
+        base = base * factor ** (dim / (dim - 2))
+    f = [base ** (-2.0 * j / dim) for j in range(dim // 2)]
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling == "yarn":
+        if original_length is None or original_length < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("rotary_frequencies: yarn needs original_length and beta_fast > beta_slow > 0")
+
+        def pair_of(turns):  # the (fractional) pair that turns so often within original_length
+            return dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo = max(math.floor(pair_of(beta_fast)), 0)
+        hi = min(math.ceil(pair_of(beta_slow)), dim - 1)
+        span = max(hi - lo, 0.001)
+        f = [x / factor * r + x * (1.0 - r) for j, x in enumerate(f) for r in (min(max((j - lo) / span, 0.0), 1.0),)]
+        mscale = 0.1 * math.log(factor) + 1.0
+    return torch.tensor(f, dtype=torch.float64).to(torch.float32), mscale
+
+
+def _rotary(stream, q, k, inv_freq, cu, lens, out, sizes, strides, mscale, interleaved, transposed):
+    hq, hk, total, d = sizes
+    if out is None:
+        qo, ko = (None if x is None else _empty(x.shape, dtype=_bf16, device=x.device) for x in (q, k))
+    else:
+        qo, ko = out
+    so = [0, 0]
+    for i, (name, x, y) in enumerate((("q", q, qo), ("k", k, ko))):
+        if (x is None) != (y is None):
+            raise ValueError(f"the outputs must hold {name} if and only if it is given")
+        if y is not None:
+            so[i] = _tokens(f"the output of {name}", y, x.get_device(), x.shape)
+    st = lib().fa_rotary(_ptr(q), _ptr(k), _ptr(qo), _ptr(ko), inv_freq.data_ptr(), cu.data_ptr(), _ptr(lens),
+                         cu.shape[0] - 1, hq, hk, total, d, 2 * inv_freq.shape[0], *strides, *so, mscale, interleaved,
+                         transposed, stream)
+    if st != 0:
+        raise FAError(st, "fa_rotary")
+    return qo, ko
+
+
+def _turn(q, k, inv_freq, cu, lens, interleaved, mscale, out, stream, transposed):
+    if q is None and k is None:
+        raise ValueError("q or k must be given")
+    some = q if q is not None else k
+    device = _first("q" if q is not None else "k", some)
+    total, _, d = some.shape
+    strides = [0, 0]
+    if q is not None:
+        strides[0] = _tokens("q", q, device, q.shape)
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != total or k.shape[1] < 1 or k.shape[2] != d:
+            raise ValueError(f"k must have the shape [{total}, kv heads, {d}]")
+        strides[1] = _tokens("k", k, device, k.shape)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must hold a frequency for each pair")
+    _packed("inv_freq", inv_freq, inv_freq.shape, device, _f32)
+    n = cu.shape
+    _ints("cu", cu, n, device)
+    if len(n) != 1 or n[0] < 2:
+        raise ValueError("cu must hold the row offsets of one sequence at least")
+    if lens is not None:
+        _ints("lens", lens, (n[0] - 1,), device)
+    sizes = (0 if q is None else q.shape[1], 0 if k is None else k.shape[1], total, d)
+    s = _here(device, stream)
+    a = (q, k, inv_freq, cu, lens, out, sizes, strides, float(mscale), int(bool(interleaved)), transposed)
+    if s is not None:
+        return _rotary(s, *a)
+    with _on(device, stream):
+        return _rotary(_current_stream(), *a)
+
+
+def rotary(q, k, inv_freq, cu, lens=None, interleaved: bool = False, mscale: float = 1.0, out=None, stream=None):
+    """q [total, Hq, d] and k [total, Hkv, d] (bf16, CUDA; tokens may be
+    strided; either may be None) turned by their places: row i of sequence b is
+    at lens[b] - n_b + i (lens int32 [B], the lengths with the new tokens, as
+    cache_append takes them), or at i without lens; cu int32 [B + 1] row offsets;
+    inv_freq fp32 [rot / 2] on the device, for the first rot values of a head
+    (see fa.h fa_rotary and rotary_frequencies). out: a pair of tensors, (q, k)
+    themselves for in place; new ones otherwise. Returns the outputs."""
+    return _turn(q, k, inv_freq, cu, lens, interleaved, mscale, out, stream, 0)
+
+
+def rotary_backward(dq, dk, inv_freq, cu, lens=None, interleaved: bool = False, mscale: float = 1.0, out=None,
+                    stream=None):
+    """The gradients of rotary's inputs from those of its outputs (bf16): the
+    transposed turn, with the arguments that rotary had."""
+    return _turn(dq, dk, inv_freq, cu, lens, interleaved, mscale, out, stream, 1)

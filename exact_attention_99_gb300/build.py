@@ -16,8 +16,10 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libfa.so")
 BUILD_DIR = os.path.join(PKG, "_build")
-SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd8.cu", "fa_bwd.cu", "fa_seq_fwd.cu", "fa_seq_bwd.cu", "fa_cache.cu"]
-HEADERS = ["fa_internal.h", "fa_bwd_layout.h", "fa_fwd_pipeline.cuh", "fa_seq.cuh", "fa_seq_plan.cuh", "sm103_ptx.cuh", "sm103_math.cuh", "exp2_poly.h"]
+SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd8.cu", "fa_bwd.cu", "fa_seq_fwd.cu", "fa_seq_bwd.cu", "fa_cache.cu",
+           "fa_rotary.cu", "fa_cache8.cu", "fa_seq_fwd8.cu"]
+HEADERS = ["fa_internal.h", "fa_bwd_layout.h", "fa_fwd_pipeline.cuh", "fa_seq.cuh", "fa_seq_plan.cuh", "sm103_ptx.cuh", "sm103_math.cuh",
+           "sm103_fp8.cuh", "exp2_poly.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -475,10 +475,12 @@ extern "C" int fa_bwd_varlen(const void* q, const void* k, const void* v, const 
   return seq_result(launch_seq_bwd(p, o, lse, dout, dq, dk, dv, static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
-                            const int* cu_q, const int* lens_k, const int* page_table, int B, int Hq, int Hkv,
-                            int total_q, int num_pages, int page_size, int max_pages, int d, long long q_stride,
-                            float scale, int window_left, int window_right, void* stream) {
+namespace {
+// the checks of the calls over a paged cache, and their problem
+int paged_problem(SeqProblem& p, const void* q, const void* k_pages, const void* v_pages, const void* o,
+                  const float* lse, const int* cu_q, const int* lens_k, const int* page_table, int B, int Hq, int Hkv,
+                  int total_q, int num_pages, int page_size, int max_pages, int d, long long q_stride, float scale,
+                  int window_left, int window_right) {
   int st = check_seq_sizes(B, Hq, Hkv, total_q, d);
   if (st == FA_OK) st = check_pages(num_pages, page_size, max_pages, Hkv, d);
   if (st != FA_OK) return st;
@@ -486,9 +488,7 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   if (total_q > 0 && (!aligned16(q) || !aligned16(o) || !aligned16(lse))) return FA_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
   st = check_stride(q_stride, Hq, d, total_q);
-  if (st == FA_OK) st = check_device();
-  if (st != FA_OK || total_q == 0) return st;
-  SeqProblem p{};
+  if (st != FA_OK) return st;
   p.q = q;
   p.k = k_pages;
   p.v = v_pages;
@@ -507,13 +507,12 @@ extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pa
   p.scale = scale;
   p.window_left = clip_window(window_left, total_q + 1LL * max_pages * page_size);
   p.window_right = clip_window(window_right, total_q + 1LL * max_pages * page_size);
-  return seq_result(launch_seq_fwd(p, o, lse, static_cast<cudaStream_t>(stream)));
+  return FA_OK;
 }
-
-extern "C" int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, const int* cu_q,
-                               const int* lens_k, const int* page_table, int B, int Hkv, int total_q, int num_pages,
-                               int page_size, int max_pages, int d, long long k_stride, long long v_stride,
-                               void* stream) {
+// the checks of the calls that fill one, and their problem
+int append_problem(AppendProblem& p, const void* k, const void* v, void* k_pages, void* v_pages, const int* cu_q,
+                   const int* lens_k, const int* page_table, int B, int Hkv, int total_q, int num_pages, int page_size,
+                   int max_pages, int d, long long k_stride, long long v_stride) {
   int st = check_seq_sizes(B, Hkv, Hkv, total_q, d);
   if (st == FA_OK) st = check_pages(num_pages, page_size, max_pages, Hkv, d);
   // the values of a block's tokens are counted in 32 bits (8 rows in pieces of 8 values)
@@ -524,11 +523,91 @@ extern "C" int fa_cache_append(const void* k, const void* v, void* k_pages, void
   if (!aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
   st = check_stride(k_stride, Hkv, d, total_q);
   if (st == FA_OK) st = check_stride(v_stride, Hkv, d, total_q);
+  if (st != FA_OK) return st;
+  p = AppendProblem{k,       v,         k_pages,   v_pages,   cu_q, lens_k,   page_table, B, Hkv,
+                    total_q, d,         num_pages, page_size, max_pages, k_stride, v_stride};
+  return FA_OK;
+}
+}  // namespace
+
+extern "C" int fa_fwd_paged(const void* q, const void* k_pages, const void* v_pages, void* o, float* lse,
+                            const int* cu_q, const int* lens_k, const int* page_table, int B, int Hq, int Hkv,
+                            int total_q, int num_pages, int page_size, int max_pages, int d, long long q_stride,
+                            float scale, int window_left, int window_right, void* stream) {
+  SeqProblem p{};
+  int st = paged_problem(p, q, k_pages, v_pages, o, lse, cu_q, lens_k, page_table, B, Hq, Hkv, total_q, num_pages,
+                         page_size, max_pages, d, q_stride, scale, window_left, window_right);
   if (st == FA_OK) st = check_device();
   if (st != FA_OK || total_q == 0) return st;
-  const AppendProblem p{k,       v,         k_pages,   v_pages,   cu_q, lens_k,   page_table, B, Hkv,
-                        total_q, d,         num_pages, page_size, max_pages, k_stride, v_stride};
+  return seq_result(launch_seq_fwd(p, o, lse, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                const float* v_scales, void* o, float* lse, const int* cu_q, const int* lens_k,
+                                const int* page_table, int B, int Hq, int Hkv, int total_q, int num_pages,
+                                int page_size, int max_pages, int d, long long q_stride, float scale, int window_left,
+                                int window_right, void* stream) {
+  SeqProblem p{};
+  int st = paged_problem(p, q, k_pages, v_pages, o, lse, cu_q, lens_k, page_table, B, Hq, Hkv, total_q, num_pages,
+                         page_size, max_pages, d, q_stride, scale, window_left, window_right);
+  if (st == FA_OK && (!aligned4(k_scales) || !aligned4(v_scales))) st = FA_ERR_INVALID_ARG;
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total_q == 0) return st;
+  return seq_result(launch_seq_fwd8(p, Fp8Scales{k_scales, v_scales}, o, lse, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, const int* cu_q,
+                               const int* lens_k, const int* page_table, int B, int Hkv, int total_q, int num_pages,
+                               int page_size, int max_pages, int d, long long k_stride, long long v_stride,
+                               void* stream) {
+  AppendProblem p{};
+  int st = append_problem(p, k, v, k_pages, v_pages, cu_q, lens_k, page_table, B, Hkv, total_q, num_pages, page_size,
+                          max_pages, d, k_stride, v_stride);
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total_q == 0) return st;
   return seq_result(launch_cache_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scales,
+                                   float* v_scales, const int* cu_q, const int* lens_k, const int* page_table, int B,
+                                   int Hkv, int total_q, int num_pages, int page_size, int max_pages, int d,
+                                   long long k_stride, long long v_stride, void* stream) {
+  AppendProblem p{};
+  int st = append_problem(p, k, v, k_pages, v_pages, cu_q, lens_k, page_table, B, Hkv, total_q, num_pages, page_size,
+                          max_pages, d, k_stride, v_stride);
+  if (st == FA_OK && (!aligned4(k_scales) || !aligned4(v_scales))) st = FA_ERR_INVALID_ARG;
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total_q == 0) return st;
+  return seq_result(launch_cache_append8(p, k_scales, v_scales, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const float* inv_freq,
+                         const int* cu_q, const int* lens, int B, int Hq, int Hk, int total, int d, int rot,
+                         long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                         float mscale, int interleaved, int transposed, void* stream) {
+  if (B < 1 || Hq < 0 || Hk < 0 || (Hq == 0 && Hk == 0) || total < 0 || d < 1 || rot < 0) return FA_ERR_INVALID_ARG;
+  if (interleaved < 0 || interleaved > 1 || transposed < 0 || transposed > 1 || !std::isfinite(mscale) || rot > d)
+    return FA_ERR_INVALID_ARG;
+  if (rot < 16 || rot % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if ((d != 64 && d != 128) || total > (1 << 28) || B > (1 << 28)) return FA_ERR_UNSUPPORTED;
+  int st = FA_OK;
+  // a token's pieces are counted in 32 bits
+  if ((1LL * Hq + Hk) * d >= (1LL << 30) || 1LL * total * (1LL * Hq + Hk) >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+  if (!aligned4(inv_freq) || !aligned4(cu_q) || (lens != nullptr && !aligned4(lens))) return FA_ERR_INVALID_ARG;
+  if (Hq > 0 && total > 0 && (!aligned16(q) || !aligned16(q_out))) return FA_ERR_INVALID_ARG;
+  if (Hk > 0 && total > 0 && (!aligned16(k) || !aligned16(k_out))) return FA_ERR_INVALID_ARG;
+  if (Hq > 0) st = check_stride(q_stride, Hq, d, total);
+  if (st == FA_OK && Hq > 0) st = check_stride(q_out_stride, Hq, d, total);
+  if (st == FA_OK && Hk > 0) st = check_stride(k_stride, Hk, d, total);
+  if (st == FA_OK && Hk > 0) st = check_stride(k_out_stride, Hk, d, total);
+  // in place: the same rows
+  if (st == FA_OK && ((Hq > 0 && q == q_out && q_stride != q_out_stride) || (Hk > 0 && k == k_out && k_stride != k_out_stride)))
+    st = FA_ERR_INVALID_ARG;
+  if (st == FA_OK) st = check_device();
+  if (st != FA_OK || total == 0) return st;
+  const RotaryProblem p{q,     k, q_out, k_out, inv_freq, cu_q,     lens,         B,            Hq,     Hk,
+                        total, d, rot,   q_stride, k_stride, q_out_stride, k_out_stride, mscale, interleaved, transposed};
+  return seq_result(launch_rotary(p, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int fa_get_status(void* stream) {

@@ -134,6 +134,31 @@ struct AppendProblem {
 };
 cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t stream);
 
+// A cache in e4m3: the pages of SeqProblem and AppendProblem hold codes, and
+// these their scales, [num_pages, page_size / 16, Hkv].
+struct Fp8Scales {
+  const float* k;
+  const float* v;
+};
+cudaError_t launch_cache_append8(const AppendProblem& p, float* k_scales, float* v_scales, cudaStream_t stream);
+cudaError_t launch_seq_fwd8(const SeqProblem& p, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream);
+
+// q and k turned by their places (strides in elements; Hq or Hk 0: none).
+struct RotaryProblem {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const float* inv_freq;  // [rot / 2]
+  const int* cu_q;
+  const int* lens;        // [B], or null: sequences begin at place 0
+  int B, Hq, Hk, total, d, rot;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;
+  float mscale;
+  int interleaved, transposed;
+};
+cudaError_t launch_rotary(const RotaryProblem& p, cudaStream_t stream);
+
 cudaError_t launch_debug_exp2(const float* x, float* y, int n, int mode, cudaStream_t stream);
 
 }  // namespace fa

@@ -1,0 +1,55 @@
+// e4m3 values of a cache and their scales, for sm_103a.
+#pragma once
+#include <cstdint>
+
+#include "sm103_math.cuh"
+
+namespace fa {
+
+constexpr int kFp8Block = 16;  // tokens of a block that has a scale (for each head)
+
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// two e4m3 codes to f16 (which holds every e4m3 value)
+__device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return r;
+}
+// two values to e4m3, nearest even, past the largest the largest, NaN to NaN
+__device__ __forceinline__ uint16_t e4m3x2_of(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// two values to f16, nearest even
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float f16_lo(uint32_t x) {
+  float r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ float f16_hi(uint32_t x) {
+  float r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(r) : "r"(x));
+  return r;
+}
+
+// four bf16 values (two words) times f, to four codes
+__device__ __forceinline__ uint32_t e4m3x4_of_bf16(uint32_t x, uint32_t y, float f) {
+  const uint32_t a = e4m3x2_of(u2f(x << 16) * f, u2f(x & 0xffff0000u) * f);
+  const uint32_t b = e4m3x2_of(u2f(y << 16) * f, u2f(y & 0xffff0000u) * f);
+  return a | (b << 16);
+}
+// four codes times f, rounded to codes again
+__device__ __forceinline__ uint32_t e4m3x4_times(uint32_t x, float f) {
+  const uint32_t a = f16x2_of_e4m3x2(uint16_t(x)), b = f16x2_of_e4m3x2(uint16_t(x >> 16));
+  return uint32_t(e4m3x2_of(f16_lo(a) * f, f16_hi(a) * f)) | (uint32_t(e4m3x2_of(f16_lo(b) * f, f16_hi(b) * f)) << 16);
+}
+
+}  // namespace fa

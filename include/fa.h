@@ -333,6 +333,74 @@ int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, 
                     int d, long long k_stride, long long v_stride, void* stream);
 
 /*
+ * A cache in 8 bits.
+ *
+ * k_pages and v_pages hold e4m3 codes (a byte each) in the layout of
+ * fa_fwd_paged's, and k_scales and v_scales [num_pages, page_size / 16, Hkv]
+ * (fp32) a scale for each block of 16 tokens and head: row r of a page stands
+ * for scale[page][r / 16][head] * code[page][r][head][...]. A scale that is used
+ * must be positive and finite. Conventions, limits and errors are those of the
+ * bf16 calls; scales are aligned to 4 bytes.
+ */
+
+/*
+ * fa_cache_append_fp8 — the new tokens' k and v (bf16) into the pages of such a
+ *   cache, at the places that fa_cache_append gives them. The scale of a block
+ *   is 2^e with the smallest whole e, -64 at least, for which every finite value
+ *   of its rows is at most 448 * 2^e. New rows of a block that holds rows of the
+ *   sequence before them leave its scale or raise it; raised, the rows held are
+ *   rounded again in the new scale (exactly, but where a code becomes subnormal).
+ *   Rows behind the new ones keep their codes, whose meaning goes with the
+ *   block's scale. Codes are the nearest, ties to even; infinities and NaN are
+ *   held as NaN, and a block of nothing else has the smallest scale. Two
+ *   sequences whose new rows the table sends to one block leave it undefined.
+ *   Lengths and errors as fa_cache_append. Needs no workspace.
+ */
+int fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pages, float* k_scales, float* v_scales,
+                        const int* cu_q, const int* lens_k, const int* page_table, int B, int Hkv, int total_q,
+                        int num_pages, int page_size, int max_pages, int d, long long k_stride, long long v_stride,
+                        void* stream);
+
+/*
+ * fa_fwd_paged_fp8 — fa_fwd_paged over such a cache: the attention of the
+ *   values that it stands for (nothing of them is rounded; P is rounded to 11
+ *   bits). Rows past a sequence's end are not used, whatever their codes; their
+ *   block's scale is that of the rows before them. Workspace: from the pool, 20
+ *   MB at most.
+ */
+int fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                     const float* v_scales, void* o, float* lse, const int* cu_q, const int* lens_k,
+                     const int* page_table, int B, int Hq, int Hkv, int total_q, int num_pages, int page_size,
+                     int max_pages, int d, long long q_stride, float scale, int window_left, int window_right,
+                     void* stream);
+
+/*
+ * fa_rotary — q and k of packed tokens turned by their places.
+ *   in : q [total, Hq, d], k [total, Hk, d] (bf16, strided as above; Hq or Hk
+ *        may be 0, their pointers then are not used), inv_freq [rot / 2] (fp32,
+ *        device, finite), cu_q [B + 1], lens [B] or null
+ *   out: q_out, k_out (same shapes, strides of their own), or q and k
+ *        themselves, in place
+ *   Row i of sequence b is at place p = lens[b] - n_b + i, the place that
+ *   fa_cache_append gives it, or i where lens is null. The first rot values of
+ *   each head are pairs, (x[j], x[j + rot / 2]), or with interleaved = 1
+ *   (x[2 j], x[2 j + 1]), j < rot / 2; pair (a, b) becomes
+ *     mscale * (a cos t - b sin t), mscale * (b cos t + a sin t), t = p * inv_freq[j],
+ *   with transposed = 1 the same with -t: the gradient of the call's inputs
+ *   from that of its outputs. The other values of a head are copied. Angles
+ *   are exact to 2^-31 of a half turn at every place; cos and sin are rounded to
+ *   fp32 and the results to bf16.
+ *   rot is a multiple of 16, 16 <= rot <= d, d in {64, 128}; (Hq + Hk) * d below
+ *   2^30, total * (Hq + Hk) below 2^31. Outputs may not overlap other rows of
+ *   the inputs. Rows outside every sequence are left as they are. Needs no
+ *   workspace. Wrong lengths as in fa_cache_append (n_b <= lens[b]).
+ */
+int fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const float* inv_freq, const int* cu_q,
+              const int* lens, int B, int Hq, int Hk, int total, int d, int rot, long long q_stride,
+              long long k_stride, long long q_out_stride, long long k_out_stride, float mscale, int interleaved,
+              int transposed, void* stream);
+
+/*
  * fa_get_status — synchronises `stream`, then returns and clears the
  * current device's status word: FA_OK, or FA_ERR_TIMEOUT if any kernel of
  * this library gave up on a bounded wait since the last call, or else
