@@ -141,6 +141,8 @@ struct Fp8Scales {
   const float* v;
 };
 cudaError_t launch_cache_append8(const AppendProblem& p, float* k_scales, float* v_scales, cudaStream_t stream);
+// as the packed and paged forward (any rows), and for few rows to a kv head
+cudaError_t launch_seq_fwd_codes(const SeqProblem& p, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream);
 cudaError_t launch_seq_fwd8(const SeqProblem& p, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream);
 
 // q and k turned by their places (strides in elements; Hq or Hk 0: none).

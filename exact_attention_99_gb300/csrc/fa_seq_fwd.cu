@@ -53,17 +53,21 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
 #include "fa_seq_plan.cuh"
+#include "sm103_fp8.cuh"
 #include "sm103_math.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
 namespace seq {
 
-constexpr int kThreads = 512;
+// what the keys are: packed sequences, a paged cache, a paged cache of codes
+enum Kind { kPacked, kPaged, kCodes };
+__host__ __device__ constexpr int threads_of(Kind kind) { return kind == kCodes ? 640 : 512; }
 constexpr uint32_t kOCol0 = 256;
 constexpr float kTau = 8.0f;  // rescale threshold (log2 units), as in the dense forward
 
@@ -72,6 +76,8 @@ constexpr float kTau = 8.0f;  // rescale threshold (log2 units), as in the dense
 // --------------------------------------------------------------------------
 struct Params {
   __nv_bfloat16* o;
+  const __nv_bfloat16* q;  // codes: read by plain loads
+  long long q_stride;
   float* lse;          // [Hq, total_q]
   const PlanHead* head;
   const int* first;
@@ -87,6 +93,7 @@ struct Params {
   int Hq, group, tok, total_q;
   int o_box;           // tokens of a warp's 32 rows, if they are whole tokens (tmO's boxes), else 0
   int num_pages, page_size, box_rows, max_pages;
+  const float* scales[2];  // codes: of K, V, [num_pages, page_size / 16, Hkv]
   float scale_log2;    // |scale| * log2(e)
   uint32_t neg_s;      // 1 for a negative scale
   int wl, wr;
@@ -113,6 +120,10 @@ struct Tiles {
   static constexpr int kSmemDyn = (2 + kSlots) * kTileBytes + kStgBytes + 1024;
 };
 constexpr int kMaxSlots = 8;
+// registers of a thread over a cache of codes: 640 threads are launched with 96 each,
+// 2 x softmax + the three others = 5 x 96
+constexpr int kRegsSoftmax8 = 128, kRegsCorrection8 = 80, kRegsOther8 = 64, kRegsCodes = 80;
+static_assert(2 * kRegsSoftmax8 + kRegsCorrection8 + kRegsOther8 + kRegsCodes == 5 * 96, "what the block is launched with");
 
 // bits of the MMA issuer's phases: Q loaded, P stored (a pair each)
 constexpr int kPhQ = 0, kPhP = 2;
@@ -140,9 +151,31 @@ struct Work {
 // sequences: 36 us either way, 3000: 81 us here, 39 us planned).
 constexpr int kFewUnits = 304, kFewRounds = 4;
 
+//
+// Over a cache of codes (kCodes) four more warps stand between the producers and
+// the products: a tile's codes land in the lower half of its ring slot, and a
+// warp turns the codes of its 32 rows to f16 in place (every e4m3 value is one),
+// and Q's rows to f16 too, divided by a power of two of the row. The scales of the
+// tile's blocks of 16 keys go to the softmax: with block scales a of K and b of V,
+//   x = scale log2(e) a (q . k^) + log2(b), P' = 2^(x - m + kShift), l = sum P' / b:
+// b in the exponent leaves the P V product without a further factor, and P' largest
+// where it weighs most. P' is at most 2^(kShift + kTau) = 2^15, which f16 holds.
+constexpr float kShift = 7.0f;
+constexpr int kScaleTiles = 8;  // ring of scales (a tile's are used before the tile four on has been taken)
+struct Codes {
+  uint64_t raw_full[kMaxSlots];    // a tile's codes have landed
+  uint64_t sc_full[kScaleTiles];
+  float4 sc[kScaleTiles][8];       // of each block: a scale log2(e), log2(b), 1 / b
+  int8_t q_exp[kItems][2][128];    // a row's power of two
+};
+struct NoCodes {};
+
+template <Kind KIND>
 struct __align__(16) Ctl {
-  FwdItem unit[kFewUnits];
-  int cost[kFewUnits + 1];  // cost of the units before
+  static constexpr int kUnits = KIND == kCodes ? 240 : kFewUnits;  // (the codes' share of shared memory)
+  FwdItem unit[kUnits];
+  int cost[kUnits + 1];  // cost of the units before
+  std::conditional_t<KIND == kCodes, Codes, NoCodes> codes;
   Work it[kItems];
   uint64_t it_full[kItems], it_empty[kItems];
   uint64_t q_full[2], q_empty[2];
@@ -203,13 +236,14 @@ struct Place {
   bool hidden;  // the box ends before the item's first visible key: its page is not looked up
 };
 
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, Kind KIND>
+__global__ void __launch_bounds__(threads_of(KIND), 1)
     seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const Params p) {
   using C = Tiles<D>;
+  constexpr bool PAGED = KIND != kPacked, CODES = KIND == kCodes;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Ctl ctl;
+  __shared__ Ctl<KIND> ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * C::kTileBytes;
@@ -223,10 +257,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.abort = 0;
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ctl.it_full[i], 1);
-      mbar_init(&ctl.it_empty[i], 15);  // every warp but this one's
+      mbar_init(&ctl.it_empty[i], threads_of(KIND) / 32 - 1);  // every warp but this one's
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl.q_full[s], 1);
+      mbar_init(&ctl.q_full[s], CODES ? 4 : 1);
       mbar_init(&ctl.q_empty[s], 1);
       mbar_init(&ctl.s_full[s], 1);
       mbar_init(&ctl.p_full[s], 8);
@@ -237,9 +271,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ctl.drain, 1);
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&ctl.kv_full[i], 1);
+      mbar_init(&ctl.kv_full[i], CODES ? 4 : 1);
       mbar_init(&ctl.kv_empty[i], 1);
       mbar_init(&ctl.tail_done[i], 1);
+    }
+    if constexpr (CODES) {
+      for (int i = 0; i < C::kSlots; ++i) mbar_init(&ctl.codes.raw_full[i], 1);
+      for (int i = 0; i < kScaleTiles; ++i) mbar_init(&ctl.codes.sc_full[i], 4);
     }
     fence_mbar_init();
   }
@@ -272,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (wg <= 1) {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<168>();
+    setmaxnreg_inc<CODES ? kRegsSoftmax8 : 168>();
     const int s = wg, wq = warp & 3;
     const int row = (wq << 5) + lane;
     const uint32_t t_s = tmem + (uint32_t(wq) << 21) + uint32_t(s * 128);  // lane quarter + S columns
@@ -280,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_tok = row / p.group;
     uint32_t ph_s = 0, ph_st = 0;
     int step0 = 0;  // running key-tile counter (trace only)
+    [[maybe_unused]] uint32_t tiles0 = 0;  // key tiles of the items before
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const Work* const w = item(i);
@@ -287,6 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool key = (w->flags & kKeyMode) != 0;
       const int step = step0 + w->a[s];
       step0 += key ? w->n[0] : w->nt;
+      [[maybe_unused]] uint32_t tile = tiles0 + uint32_t(key ? s : w->a[s]);
+      tiles0 += uint32_t(w->nt);
+      [[maybe_unused]] float rf = 0.0f;
       const int n = w->n[s];
       const bool mine = (wq << 5) < w->rows[s];  // the warp has rows
       float m_run = -INFINITY, l_run = 0.0f;
@@ -302,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph_s ^= 1;
           if (row == 0) trace_stamp(p.trace, step + j, 4 + 3 * s);
           if (!mine) {
+            if constexpr (CODES) tile += key ? 2 : 1;
             if (lane == 0) {
               if (j > 0) mbar_arrive(&ctl.alpha_full[s]);
               mbar_arrive(&ctl.p_full[s]);
@@ -309,79 +352,188 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
           tc_fence_after();
-          uint32_t v[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
-          tmem_wait_ld();
-          // masked where the tile reaches past the keys or crosses a bound of some row
-          if (kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl)) {
-            int hi = klen - kb;  // columns [lo, hi) are visible
-            int lo = 0;
+          if constexpr (CODES) {
+            // The scales of the tile's blocks (and, before them, the rows' powers of two).
+            const uint32_t ring = tile % kScaleTiles, use = tile / kScaleTiles;
+            tile += key ? 2 : 1;
+            if (!warp_wait(&ctl.codes.sc_full[ring], use & 1, abort_flag, LIM)) { ok = false; break; }
+            if (j == 0) rf = exp2i(ctl.codes.q_exp[i % kItems][key ? 0 : s][row]);
+            const float4* const sc = ctl.codes.sc[ring];
+            int hi = klen - kb, lo = 0;  // columns [lo, hi) are visible
+            const bool edge = kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl);
             if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
             if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
             const uint32_t span = uint32_t(max(hi - lo, 0));
-            // only the blocks of 32 columns that some row of the warp does not
-            // see whole: code that runs once per item is slow to fetch
+            // The lower half of S is read twice, for its maximum and for its exponentials:
+            // its 64 registers are what 640 threads have less than 512.
+            uint32_t v[64], x[32];
+            auto masked = [&](uint32_t* y, int c0) {
 #pragma unroll
-            for (int b = 0; b < 128; b += 32) {
-              if (lo <= b && hi >= b + 32) continue;
+              for (int c = 0; c < 32; ++c)
+                if (uint32_t(c0 + c - lo) >= span) y[c] = f2u(-INFINITY);
+            };
+            // (a product of scales that underflows would make -inf * 0 of a masked score)
+            auto factor = [&](float a) { return fmaxf(a * rf, 1.1754944e-38f); };
+            float mx = -INFINITY;
+            auto maximum = [&](const uint32_t* y, int b) {  // of blocks b, b + 1
 #pragma unroll
-              for (int c = b; c < b + 32; ++c)
-                if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t* z = y + 16 * h;
+                float a = fmax3(u2f(z[0]), u2f(z[1]), u2f(z[2])), c = fmax3(u2f(z[3]), u2f(z[4]), u2f(z[5]));
+                a = fmax3(a, u2f(z[6]), u2f(z[7]));
+                c = fmax3(c, u2f(z[8]), u2f(z[9]));
+                a = fmax3(a, u2f(z[10]), u2f(z[11]));
+                c = fmax3(c, u2f(z[12]), u2f(z[13]));
+                a = fmax3(a, u2f(z[14]), u2f(z[15]));
+                const float4 t = sc[b + h];
+                mx = fmaxf(mx, fmaf(fmaxf(a, c), factor(t.x), t.y));
+              }
+            };
+            tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+            tmem_wait_ld();
+            if (edge) masked(v, 0), masked(v + 32, 32);
+            maximum(v, 0);
+            maximum(v + 32, 2);
+            tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+            tmem_wait_ld();
+            if (edge) masked(v, 64), masked(v + 32, 96);
+            maximum(v, 4);
+            maximum(v + 32, 6);
+            const float m_new = (mx > m_run + kTau) ? mx : m_run;
+            const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
+            const float alpha = ex2_mufu(m_run - m_use);
+            if (j > 0) {
+              ctl.alpha[s][row] = alpha;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
             }
-          }
-          float mA = -INFINITY, mB = -INFINITY, mC = -INFINITY, mD = -INFINITY;
+            const float base = kShift - m_use;
+            l_run *= alpha;
+            m_run = m_new;
+            uint32_t pk[16];
+            auto exponentials = [&](const uint32_t* y, int b) {  // of blocks b, b + 1
 #pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            mA = fmax3(mA, u2f(v[c]), u2f(v[c + 1]));
-            mB = fmax3(mB, u2f(v[c + 2]), u2f(v[c + 3]));
-            mC = fmax3(mC, u2f(v[c + 4]), u2f(v[c + 5]));
-            mD = fmax3(mD, u2f(v[c + 6]), u2f(v[c + 7]));
-          }
-          const float mx = fmaxf(fmaxf(mA, mB), fmaxf(mC, mD));
-          const float m_cand = fmaxf(m_run, mx * sl);
-          const float m_new = (m_cand > m_run + kTau) ? m_cand : m_run;
-          const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
-          const float alpha = ex2_mufu(m_run - m_use);
-          if (j > 0) {  // (there is no O to correct before the first)
-            ctl.alpha[s][row] = alpha;
+              for (int h = 0; h < 2; ++h) {
+                const float4 t = sc[b + h];
+                const float f = factor(t.x), n = t.y + base;
+                const uint64_t f2 = pack2(f, f), n2 = pack2(n, n);
+                uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                  const uint64_t z = ffma2(pack2(u2f(y[16 * h + 2 * c]), u2f(y[16 * h + 2 * c + 1])), f2, n2);
+                  float a, e;
+                  unpack2(z, a, e);
+                  a = ex2_mufu(a);
+                  e = ex2_mufu(e);
+                  const uint64_t pr = pack2(a, e);
+                  if ((c & 1) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
+                  if ((c & 1) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
+                  // P' to f16 (nearest even), the type of the products: off by at most
+                  // 2^-12 of each that is 2^-21 of the largest; the row sum keeps 32 bits
+                  pk[8 * h + c] = f16x2_of(a, e);
+                }
+                float la, lb;
+                unpack2(fadd2(acc0, acc1), la, lb);
+                l_run = fmaf(la + lb, t.z, l_run);
+              }
+            };
+            // P' of the upper half over the first columns of S's upper half, that of
+            // the lower half over those of the lower
+            tmem_ld32(t_s, x);
+            exponentials(v, 4);
+            tmem_st16(t_s + 64, pk);
+            exponentials(v + 32, 6);
+            tmem_st16(t_s + 80, pk);
+            tmem_wait_ld();
+            tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            if (edge) masked(x, 0);
+            exponentials(x, 0);
+            tmem_wait_ld();
+            tmem_st16(t_s, pk);
+            if (edge) masked(v, 32);
+            exponentials(v, 2);
+            tmem_st16(t_s + 16, pk);
+            tmem_wait_st();
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
-          }
-          if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
-          const uint64_t sl2 = pack2(sl, sl);
-          const uint64_t nm2 = pack2(-m_use, -m_use);
-          uint64_t acc0 = 0, acc1 = 0, acc2 = 0, acc3 = 0;
-          uint32_t pk[64];
+            if (lane == 0) mbar_arrive(&ctl.p_full[s]);
+          } else {
+            uint32_t v[128];
 #pragma unroll
-          for (int c = 0; c < 64; ++c) {
-            const uint64_t y = ffma2(pack2(u2f(v[2 * c]), u2f(v[2 * c + 1])), sl2, nm2);
-            float a, b;
-            unpack2(y, a, b);
-            a = ex2_mufu(a);
-            b = ex2_mufu(b);
-            const uint64_t pr = pack2(a, b);
-            if ((c & 3) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
-            if ((c & 3) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
-            if ((c & 3) == 2) acc2 = c == 2 ? pr : fadd2(acc2, pr);
-            if ((c & 3) == 3) acc3 = c == 3 ? pr : fadd2(acc3, pr);
-            // P to bf16 (nearest even), the type that the P V product takes
-            // beside a bf16 V: off by at most 2^-8 of each probability; the row
-            // sum keeps the 32-bit values
-            pk[c] = pack_bf16x2(a, b);
-          }
+            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+            tmem_wait_ld();
+            // masked where the tile reaches past the keys or crosses a bound of some row
+            if (kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl)) {
+              int hi = klen - kb;  // columns [lo, hi) are visible
+              int lo = 0;
+              if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
+              if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
+              const uint32_t span = uint32_t(max(hi - lo, 0));
+              // only the blocks of 32 columns that some row of the warp does not
+              // see whole: code that runs once per item is slow to fetch
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[c * 16]));
-          const uint64_t acc = fadd2(fadd2(acc0, acc1), fadd2(acc2, acc3));
-          float la, lb;
-          unpack2(acc, la, lb);
-          l_run = fmaf(l_run, alpha, la + lb);
-          m_run = m_new;
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
-          if (lane == 0) mbar_arrive(&ctl.p_full[s]);
+              for (int b = 0; b < 128; b += 32) {
+                if (lo <= b && hi >= b + 32) continue;
+#pragma unroll
+                for (int c = b; c < b + 32; ++c)
+                  if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+              }
+            }
+            float mA = -INFINITY, mB = -INFINITY, mC = -INFINITY, mD = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+              mA = fmax3(mA, u2f(v[c]), u2f(v[c + 1]));
+              mB = fmax3(mB, u2f(v[c + 2]), u2f(v[c + 3]));
+              mC = fmax3(mC, u2f(v[c + 4]), u2f(v[c + 5]));
+              mD = fmax3(mD, u2f(v[c + 6]), u2f(v[c + 7]));
+            }
+            const float mx = fmaxf(fmaxf(mA, mB), fmaxf(mC, mD));
+            const float m_cand = fmaxf(m_run, mx * sl);
+            const float m_new = (m_cand > m_run + kTau) ? m_cand : m_run;
+            const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
+            const float alpha = ex2_mufu(m_run - m_use);
+            if (j > 0) {  // (there is no O to correct before the first)
+              ctl.alpha[s][row] = alpha;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
+            }
+            if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
+            const uint64_t sl2 = pack2(sl, sl);
+            const uint64_t nm2 = pack2(-m_use, -m_use);
+            uint64_t acc0 = 0, acc1 = 0, acc2 = 0, acc3 = 0;
+            uint32_t pk[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              const uint64_t y = ffma2(pack2(u2f(v[2 * c]), u2f(v[2 * c + 1])), sl2, nm2);
+              float a, b;
+              unpack2(y, a, b);
+              a = ex2_mufu(a);
+              b = ex2_mufu(b);
+              const uint64_t pr = pack2(a, b);
+              if ((c & 3) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
+              if ((c & 3) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
+              if ((c & 3) == 2) acc2 = c == 2 ? pr : fadd2(acc2, pr);
+              if ((c & 3) == 3) acc3 = c == 3 ? pr : fadd2(acc3, pr);
+              // P to bf16 (nearest even), the type that the P V product takes
+              // beside a bf16 V: off by at most 2^-8 of each probability; the row
+              // sum keeps the 32-bit values
+              pk[c] = pack_bf16x2(a, b);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[c * 16]));
+            const uint64_t acc = fadd2(fadd2(acc0, acc1), fadd2(acc2, acc3));
+            float la, lb;
+            unpack2(acc, la, lb);
+            l_run = fmaf(l_run, alpha, la + lb);
+            m_run = m_new;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
+            if (lane == 0) mbar_arrive(&ctl.p_full[s]);
+          }
         }
         if (!ok) break;
       }
@@ -389,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(&ctl.stats_empty[s], ph_st ^ 1, abort_flag, LIM)) { ok = false; break; }
         ph_st ^= 1;
         ctl.stat_l[s][row] = l_run;
-        ctl.stat_m[s][row] = m_run;
+        ctl.stat_m[s][row] = CODES ? m_run - kShift : m_run;  // (of codes O and l are 2^kShift of what belongs to m)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.stats_full[s]);
       }
@@ -397,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (wg == 2) {
     // ------------------------------------------------ correction + epilogue
-    setmaxnreg_dec<104>();
+    setmaxnreg_dec<CODES ? kRegsCorrection8 : 104>();
     const int wq = warp & 3;
     const int row = (wq << 5) + lane;
     const uint32_t t_lane = tmem + (uint32_t(wq) << 21) + kOCol0;
@@ -582,8 +734,158 @@ __global__ void __launch_bounds__(kThreads, 1)
       release(i);
     }
     if (lane == 0) bulk_wait_all();  // stores complete (and staging reads done) before the CTA exits
-  } else {
-    setmaxnreg_dec<72>();
+  } else if (wg == 3) {
+    setmaxnreg_dec<CODES ? kRegsOther8 : 72>();
+  }
+  if constexpr (CODES) {
+    if (wg == 4) {
+      // ------------------------------------------------ codes to f16
+      setmaxnreg_dec<kRegsCodes>();
+      const int cw = warp & 3;  // rows [32 cw, 32 cw + 32) of a tile
+      uint32_t base = 0, q_uses[2] = {0, 0}, key_items = 0, tiles0 = 0;
+      bool ok = true;
+      // A lane reads 16 codes of a row and writes them as two pieces of 8 values.
+      // Four lanes have half a row (d = 128); the rows of neighbouring fours differ in
+      // bits 0 and 2, so that neither the reads of codes (128-byte swizzle, or rows of 64
+      // bytes) nor the writes meet in a bank.
+      const int in8 = (0x63724150u >> (4 * (lane >> 2))) & 7, quarter = lane & 3;
+      // this lane's block of a tile (lanes 0, 1) and its scales, looked up two tiles ahead, read one ahead
+      for (int i = 0; ok; ++i) {
+        const Work* const w = item(i);
+        if (w == nullptr) break;
+        const int nt = w->nt, kvh = w->kvh, kt = w->kt, klen = w->klen, fill = w->fill;
+        const bool key = (w->flags & kKeyMode) != 0;
+        const int seen = p.wl >= 0 ? w->pos - p.wl : 0;  // the first key that a row of the item sees
+        const int* const row_of_table = p.table + size_t(w->kbase) * p.max_pages;
+        // row of the scales of block 2 cw + lane of tile t, or -1: not used
+        auto block_key = [&](int t) { return ((kt + t) * 8 + 2 * cw + lane) * kFp8Block; };
+        auto look_up = [&](int t) {
+          const int k = block_key(t);
+          return t < nt && lane < 2 && k < klen && k + kFp8Block > seen ? row_of_table[k / p.page_size] : -1;
+        };
+        auto read = [&](int t, int page) {
+          float2 r = make_float2(1.0f, 1.0f);
+          if (page >= 0 && page < p.num_pages) {
+            const int k = block_key(t);
+            const size_t at = (size_t(page) * (p.page_size / kFp8Block) + k % p.page_size / kFp8Block) * p.Hkv + kvh;
+            r.x = p.scales[0][at];
+            r.y = p.scales[1][at];
+          }
+          return r;
+        };
+        int page0 = look_up(0);
+        int page1 = look_up(1);
+        float2 next = read(0, page0);
+        // Q's rows, as the producer of bf16 tiles loads them: 16 bytes a lane
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (w->n[s] == 0 || (key && s == 1)) continue;
+          const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
+          ok = warp_wait(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1, abort_flag, LIM);
+          if (!ok) break;
+          if (b == 0) {
+            ++q_uses[0];
+          } else {
+            ++q_uses[1];
+          }
+          constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
+          const int rows = w->rows[s], col = lane % kLanes;
+          const int q0 = w->q0 + (key ? 0 : s * p.tok);
+#pragma unroll 1
+          for (int r0 = cw * 32; r0 < min(rows, cw * 32 + 32); r0 += kBatch * kAtOnce) {
+            uint4 x[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+              const int r = r0 + e * kAtOnce + lane / kLanes, tok = r / p.group;
+              x[e] = make_uint4(0, 0, 0, 0);
+              if (r < rows)
+                x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + (q0 + tok) * p.q_stride +
+                                                            (1LL * kvh * p.group + (r - tok * p.group)) * D + col * 8));
+            }
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+              const int r = r0 + e * kAtOnce + lane / kLanes;
+              uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu), __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
+              m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+              for (int d = 1; d < kLanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+              // the row's largest value into [2^14, 2^15)
+              const int ex = max(int(m >> 7) - 127, -100) - 14;
+              const float f = exp2i(-ex);
+              const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+              uint32_t z[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) z[k] = f16x2_of(u2f(y[k] << 16) * f, u2f(y[k] & 0xffff0000u) * f);
+              *reinterpret_cast<uint4*>(sQ + b * C::kTileBytes + (col >> 3) * 16384 + r * 128 + (((col & 7) ^ (r & 7)) << 4)) =
+                  make_uint4(z[0], z[1], z[2], z[3]);
+              if (col == 0) ctl.codes.q_exp[i % kItems][s][r] = int8_t(ex);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.q_full[b]);
+        }
+        if (!ok) break;
+        const int d = min(key ? 2 : 1, nt);
+#pragma unroll 1
+        for (int x = 0; x < 2 * nt; ++x) {
+          // the ring's entries: K(0..d-1), then V(t), K(t + d) in turn, then the last V
+          const int y = x - d;
+          const bool is_v = y >= 0 && (y >= 2 * (nt - d) || (y & 1) == 0);
+          const int t = y < 0 ? x : y >= 2 * (nt - d) ? y - (nt - d) : (y >> 1) + ((y & 1) ? d : 0);
+          const uint32_t entry = base + uint32_t(x), slot = entry % C::kSlots;
+          if (!is_v) {
+            if (lane < 2)
+              ctl.codes.sc[(tiles0 + t) % kScaleTiles][2 * cw + lane] =
+                  make_float4(next.x * p.scale_log2, __log2f(next.y), __fdividef(1.0f, next.y), 0.0f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.codes.sc_full[(tiles0 + t) % kScaleTiles]);
+            next = read(t + 1, page1);
+            page1 = look_up(t + 2);
+          }
+          ok = warp_wait(&ctl.codes.raw_full[slot], (entry / C::kSlots) & 1, abort_flag, LIM);
+          if (!ok) break;
+          uint8_t* const tile = sKV + slot * C::kTileBytes;
+          uint8_t* const mine = tile + cw * 4096;
+          constexpr int kHalves = D / 64;
+          uint4 c[4][kHalves];
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+              c[g][h] = *reinterpret_cast<const uint4*>(
+                  mine + (g * 8 + in8) * D + (D == 128 ? ((h * 4 + quarter) ^ in8) << 4 : quarter << 4));
+          if (is_v && t == nt - 1 && fill != 0) {  // rows past the sequence's end: 0 * NaN would stay NaN
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (cw * 32 + g * 8 + in8 >= fill)
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) c[g][h] = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();  // the warp's codes have been read: its rows may be written over them
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              const uint32_t z[4] = {c[g][h].x, c[g][h].y, c[g][h].z, c[g][h].w};
+              uint32_t f[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                f[2 * k] = f16x2_of_e4m3x2(uint16_t(z[k]));
+                f[2 * k + 1] = f16x2_of_e4m3x2(uint16_t(z[k] >> 16));
+              }
+              uint8_t* const to = tile + h * 16384 + (cw * 32 + g * 8 + in8) * 128;
+              *reinterpret_cast<uint4*>(to + (((2 * quarter) ^ in8) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+              *reinterpret_cast<uint4*>(to + (((2 * quarter + 1) ^ in8) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.kv_full[slot]);
+        }
+        base += uint32_t(2 * nt);
+        tiles0 += uint32_t(nt);
+        if (ok) release(i);
+      }
+    }
   }
   if (warp == 12 || warp == 14) {
     // ------------------------------------------------------ TMA producers
@@ -627,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Place next = place(0);
       // Q: key mode takes the two buffers in turn, else stage s takes buffer s
-      for (int s = 0; s < 2 && ok && !is_v; ++s) {
+      for (int s = 0; s < 2 && ok && !is_v && !CODES; ++s) {
         if (w->n[s] == 0 || (key && s == 1)) continue;
         const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
         ok = warp_wait(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1, abort_flag, LIM);
@@ -680,7 +982,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             page[x] = __shfl_sync(0xffffffffu, at.page, x);
             in_page[x] = __shfl_sync(0xffffffffu, at.in_page, x);
           }
-          if (elect_one()) {
+          if (CODES) {
+            if constexpr (CODES)
+              if (elect_one()) {
+                mbar_arrive_expect_tx(&ctl.codes.raw_full[slot], uint32_t(at.boxes * p.box_rows * D));
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  if (x >= at.boxes) break;
+                  const int r = x * p.box_rows;  // 32 rows of codes stand where 32 rows of 64 values will
+                  tma_load_4d_hint(dst + (r >> 5) * 4096 + (r & 31) * D, m, &ctl.codes.raw_full[slot], 0, kvh, in_page[x],
+                                   page[x], pol_kv);
+                }
+              }
+          } else if (elect_one()) {
             mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(at.boxes * p.box_rows * D * 2));
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
@@ -698,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d_hint(dst + c * 16384, m, &ctl.kv_full[slot], c * 64, kvh, kbase + (kt + t) * 128, 0, pol_kv);
         }
         const int fill = w->fill;
-        if (is_v && t == nt - 1 && fill != 0) {
+        if (!CODES && is_v && t == nt - 1 && fill != 0) {
           // The sequence ends in this tile: once loaded, its rows past the end
           // are zeroed before the product reads them (a row is 128 bytes of
           // each chunk; the swizzle stays within it).
@@ -723,8 +1037,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // producer's and all waits, 1.78 -> 1.29 ms on one causal sequence of 16384
     // tokens, against one lane walking: MMA operands are uniform registers).
     {
-      const uint32_t idS = idesc_bf16_f32(128, 128, 0, 0) | (p.neg_s << 13);
-      constexpr uint32_t idPV = idesc_bf16_f32(128, D, 0, 1);
+      const uint32_t idS = (CODES ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0)) | (p.neg_s << 13);
+      constexpr uint32_t idPV = CODES ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
       const uint32_t dq = sdesc_lo(smem_u32(sQ), 16), dk = sdesc_lo(smem_u32(sKV), 16),
                      dv = sdesc_lo(smem_u32(sKV), 16384);
       // Phases of the barriers of each stage (or slot), a bit each: arrays
@@ -763,7 +1077,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b0 = sdesc_step(dv, slot * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts_lo(tmem + kOCol0 + uint32_t(s * D), tmem + uint32_t(s * 128) + kk * 8, sdesc_step(b0, kk * 2048), idPV,
+          mma_ts_lo(tmem + kOCol0 + uint32_t(s * D), tmem + uint32_t(s * 128) + (CODES && kk >= 4 ? 64 + (kk - 4) * 8 : kk * 8),
+                    sdesc_step(b0, kk * 2048), idPV,
                     (acc || kk > 0) ? 1u : 0u);
       };
       auto issue_s = [&](int s, uint32_t b, uint32_t slot) {
@@ -789,7 +1104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Work* const w = item(i);
         if (w == nullptr) break;
         const int nt = w->nt;
-        const bool fill = w->fill != 0;
+        const bool fill = !CODES && w->fill != 0;
         if (nt > 0 && (w->flags & kKeyMode)) {
           const uint32_t b = key_items++ & 1;
           ok = wait_phase(&ctl.q_full[b], kPhQ + int(b));
@@ -1141,9 +1456,11 @@ Space carve(uint8_t* base, const SeqProblem& pb, int G, long long units) {
   return s;
 }
 
-template <int D, bool PAGED>
-cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t stream) {
+template <int D, Kind KIND>
+cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* lse, cudaStream_t stream) {
   using C = Tiles<D>;
+  constexpr bool PAGED = KIND != kPacked;
+  constexpr int few_units = Ctl<KIND>::kUnits;
   const int G = std::min(num_sms(), seq::kMaxWorkers);
   const int group = pb.Hq / pb.Hkv, tok = 128 / group;
   Params p{};
@@ -1166,7 +1483,26 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
     if (!encode_tiled(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, o, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  if constexpr (PAGED) {
+  if constexpr (KIND == kCodes) {
+    // rows of D bytes; 32 of 64 bytes go together (see the producers)
+    p.box_rows = D == 128 ? 128 : 32;
+    while (pb.page_size % p.box_rows != 0) p.box_rows /= 2;  // 16 at least
+    const void* kp[2] = {pb.k, pb.v};
+    CUtensorMap* maps[2] = {&mk, &mv};
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t row = uint64_t(pb.Hkv) * D;
+      const uint64_t dims[4] = {uint64_t(D), uint64_t(pb.Hkv), uint64_t(pb.page_size), uint64_t(pb.num_pages)};
+      const uint64_t strides[3] = {uint64_t(D), row, row * pb.page_size};
+      const uint32_t box[4] = {uint32_t(D), 1, uint32_t(p.box_rows), 1};
+      if (!encode_tiled(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, kp[i], dims, strides, box,
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    }
+    p.q = static_cast<const __nv_bfloat16*>(pb.q);
+    p.q_stride = pb.q_stride;
+    p.scales[0] = sc->k;
+    p.scales[1] = sc->v;
+  } else if constexpr (PAGED) {
     p.box_rows = 128;
     while (pb.page_size % p.box_rows != 0) p.box_rows /= 2;  // 16 at least
     if (!make_bshd_map(&mk, pb.k, pb.num_pages, pb.page_size, pb.Hkv, D, p.box_rows) ||
@@ -1189,14 +1525,14 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   }
   p.status = status_word();
   if (p.status == nullptr) return cudaErrorLaunchFailure;
-  auto kern = seq_fwd_kernel<D, PAGED>;
+  auto kern = seq_fwd_kernel<D, KIND>;
   static SmemLimit limit;
   cudaError_t e = limit.set(kern, C::kSmemDyn);
   if (e != cudaSuccess) return e;
   // a sequence of n tokens has ceil(n / (2 tok)) units
   long long units = pb.total_q / (2 * tok) + pb.B;
   if (units > pb.total_q) units = pb.total_q;
-  const bool few = pb.B <= kFewUnits && units <= kFewUnits && units * pb.Hkv <= (PAGED ? kFewRounds : 1) * G;
+  const bool few = pb.B <= few_units && units <= few_units && units * pb.Hkv <= (PAGED ? kFewRounds : 1) * G;
   // Few items of few key tiles are never divided: no workspace, no last kernel.
   long long keys = pb.page_table != nullptr ? 1LL * pb.max_pages * pb.page_size : pb.total_k;
   if (pb.window_left >= 0 && pb.window_right >= 0)  // and whole tiles around those that a unit sees
@@ -1256,7 +1592,7 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(G);
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(threads_of(KIND));
   lc.dynamicSmemBytes = C::kSmemDyn;
   lc.stream = stream;
   lc.attrs = pdl;
@@ -1284,8 +1620,15 @@ cudaError_t launch_t(const SeqProblem& pb, void* o, float* lse, cudaStream_t str
 cudaError_t launch_seq_fwd(const SeqProblem& pb, void* o, float* lse, cudaStream_t stream) {
   const bool paged = pb.page_table != nullptr;
   if (pb.d == 128)
-    return paged ? seq::launch_t<128, true>(pb, o, lse, stream) : seq::launch_t<128, false>(pb, o, lse, stream);
-  return paged ? seq::launch_t<64, true>(pb, o, lse, stream) : seq::launch_t<64, false>(pb, o, lse, stream);
+    return paged ? seq::launch_t<128, seq::kPaged>(pb, nullptr, o, lse, stream)
+                 : seq::launch_t<128, seq::kPacked>(pb, nullptr, o, lse, stream);
+  return paged ? seq::launch_t<64, seq::kPaged>(pb, nullptr, o, lse, stream)
+               : seq::launch_t<64, seq::kPacked>(pb, nullptr, o, lse, stream);
+}
+
+cudaError_t launch_seq_fwd_codes(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream) {
+  return pb.d == 128 ? seq::launch_t<128, seq::kCodes>(pb, &sc, o, lse, stream)
+                     : seq::launch_t<64, seq::kCodes>(pb, &sc, o, lse, stream);
 }
 
 }  // namespace fa

@@ -738,6 +738,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
 cudaError_t launch_seq_fwd8(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream) {
   // rows of a unit: as many as the mean sequence has
   const long long rows = (1LL * pb.total_q + pb.B - 1) / pb.B * (pb.Hq / pb.Hkv);
+  if (rows > 32) return launch_seq_fwd_codes(pb, sc, o, lse, stream);
   const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   if (pb.d == 128)
     return nt == 1   ? seq8::launch_t<128, 1>(pb, sc, o, lse, stream)
