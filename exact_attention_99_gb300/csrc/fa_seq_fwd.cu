@@ -67,7 +67,7 @@ namespace seq {
 
 // what the keys are: packed sequences, a paged cache, a paged cache of codes
 enum Kind { kPacked, kPaged, kCodes };
-__host__ __device__ constexpr int threads_of(Kind kind) { return kind == kCodes ? 640 : 512; }
+constexpr int kThreads = 512;
 constexpr uint32_t kOCol0 = 256;
 constexpr float kTau = 8.0f;  // rescale threshold (log2 units), as in the dense forward
 
@@ -109,6 +109,7 @@ struct Params {
 //   softmax s   4+3s S ready, 5+3s alpha published, 6+3s P stored
 //   correction  10+s O released for PV
 //   epilogue s  12+s O written (step of the item's last tile)
+//   codes       14 a K tile's codes landed, 15 turned to f16
 constexpr int kItems = 4;  // ring of work items
 
 template <int D>
@@ -120,10 +121,6 @@ struct Tiles {
   static constexpr int kSmemDyn = (2 + kSlots) * kTileBytes + kStgBytes + 1024;
 };
 constexpr int kMaxSlots = 8;
-// registers of a thread over a cache of codes: 640 threads are launched with 96 each,
-// 2 x softmax + the three others = 5 x 96
-constexpr int kRegsSoftmax8 = 128, kRegsCorrection8 = 80, kRegsOther8 = 64, kRegsCodes = 80;
-static_assert(2 * kRegsSoftmax8 + kRegsCorrection8 + kRegsOther8 + kRegsCodes == 5 * 96, "what the block is launched with");
 
 // bits of the MMA issuer's phases: Q loaded, P stored (a pair each)
 constexpr int kPhQ = 0, kPhP = 2;
@@ -152,16 +149,18 @@ struct Work {
 constexpr int kFewUnits = 304, kFewRounds = 4;
 
 //
-// Over a cache of codes (kCodes) four more warps stand between the producers and
-// the products: a tile's codes land in the lower half of its ring slot, and a
-// warp turns the codes of its 32 rows to f16 in place (every e4m3 value is one),
-// and Q's rows to f16 too, divided by a power of two of the row. The scales of the
-// tile's blocks of 16 keys go to the softmax: with block scales a of K and b of V,
+// Over a cache of codes (kCodes) the warps that correct O and write it elsewhere
+// stand between the producers and the products: a tile's codes land in the lower
+// half of its ring slot, a warp turns those of its 32 rows to f16 in place (every
+// e4m3 value is one), and Q's rows to f16 too, divided by a power of two of the
+// row. The scales of the tile's blocks of 16 keys go to the softmax: with a of K
+// and b of V,
 //   x = scale log2(e) a (q . k^) + log2(b), P' = 2^(x - m + kShift), l = sum P' / b:
 // b in the exponent leaves the P V product without a further factor, and P' largest
 // where it weighs most. P' is at most 2^(kShift + kTau) = 2^15, which f16 holds.
 constexpr float kShift = 7.0f;
-constexpr int kScaleTiles = 8;  // ring of scales (a tile's are used before the tile four on has been taken)
+constexpr float kLow = -3.4028235e38f;  // the running maximum before any key
+constexpr int kScaleTiles = 8;  // ring of scales (a tile's are used before the tile seven on is converted)
 struct Codes {
   uint64_t raw_full[kMaxSlots];    // a tile's codes have landed
   uint64_t sc_full[kScaleTiles];
@@ -182,7 +181,8 @@ struct __align__(16) Ctl {
   uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
   uint64_t tail_done[kMaxSlots];  // a V tile that the sequence ends in: loaded, its rows past the end zeroed
   // p_full: P stored (4 softmax warps) and O corrected, or read by the epilogue
-  // of the stage's item before (4 correction warps)
+  // of the stage's item before (4 correction warps; over codes the 4 softmax warps
+  // again, those of stage 0 for both where they join them)
   uint64_t s_full[2], p_full[2], alpha_full[2], o_full[2];
   uint64_t stats_full[2], stats_empty[2];
   uint64_t drain;
@@ -236,8 +236,428 @@ struct Place {
   bool hidden;  // the box ends before the item's first visible key: its page is not looked up
 };
 
+// item i of this CTA, or null when there is none (or a wait ran out)
+template <Kind KIND>
+__device__ __forceinline__ const Work* next_item(Ctl<KIND>& ctl, int i, uint64_t LIM) {
+  if (!warp_wait(&ctl.it_full[i % kItems], (i / kItems) & 1, &ctl.abort, LIM)) return nullptr;
+  const Work* x = &ctl.it[i % kItems];
+  return x->flags < 0 ? nullptr : x;
+}
+// by each warp once all its lanes have read the item: warp 15 may then write the next one over it
+template <Kind KIND>
+__device__ __forceinline__ void release_item(Ctl<KIND>& ctl, int i) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
+}
+
+// Codes: rows [32 cw, 32 cw + 32) of Q's and of every key tile turned to f16.
+template <int D>
+__device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl, uint8_t* sQ, uint8_t* sKV, int cw,
+                                              int lane, uint64_t LIM) {
+  using C = Tiles<D>;
+  uint32_t base = 0, q_uses[2] = {0, 0}, key_items = 0, tiles0 = 0;
+  bool ok = true;
+  // A lane reads 16 codes of a row and writes them as two pieces of 8 values.
+  // Four lanes have half a row (d = 128); the rows of neighbouring fours differ in
+  // bits 0 and 2, so that neither the reads of codes (128-byte swizzle, or rows of 64
+  // bytes) nor the writes meet in a bank.
+  const int in8 = (0x63724150u >> (4 * (lane >> 2))) & 7, quarter = lane & 3;
+  // this lane's block of a tile (lanes 0, 1) and its scales, looked up two tiles ahead, read one ahead
+  for (int i = 0; ok; ++i) {
+    const Work* const w = next_item(ctl, i, LIM);
+    if (w == nullptr) break;
+    const int nt = w->nt, kvh = w->kvh, kt = w->kt, klen = w->klen, fill = w->fill;
+    const bool key = (w->flags & kKeyMode) != 0;
+    const int seen = p.wl >= 0 ? w->pos - p.wl : 0;  // the first key that a row of the item sees
+    const int* const row_of_table = p.table + size_t(w->kbase) * p.max_pages;
+    // row of the scales of block 2 cw + lane of tile t, or -1: not used
+    auto block_key = [&](int t) { return ((kt + t) * 8 + 2 * cw + lane) * kFp8Block; };
+    auto look_up = [&](int t) {
+      const int k = block_key(t);
+      return t < nt && lane < 2 && k < klen && k + kFp8Block > seen ? row_of_table[k / p.page_size] : -1;
+    };
+    auto read = [&](int t, int page) {
+      float2 r = make_float2(1.0f, 1.0f);
+      if (page >= 0 && page < p.num_pages) {
+        const int k = block_key(t);
+        const size_t at = (size_t(page) * (p.page_size / kFp8Block) + k % p.page_size / kFp8Block) * p.Hkv + kvh;
+        r.x = p.scales[0][at];
+        r.y = p.scales[1][at];
+      }
+      return r;
+    };
+    int page0 = look_up(0);
+    int page1 = look_up(1);
+    float2 next = read(0, page0);
+    // Q's rows, as the producer of bf16 tiles loads them: 16 bytes a lane
+    for (int s = 0; s < 2 && ok; ++s) {
+      if (w->n[s] == 0 || (key && s == 1)) continue;
+      const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
+      ok = warp_wait(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1, &ctl.abort, LIM);
+      if (!ok) break;
+      if (b == 0) {
+        ++q_uses[0];
+      } else {
+        ++q_uses[1];
+      }
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
+      const int rows = w->rows[s], col = lane % kLanes;
+      const int q0 = w->q0 + (key ? 0 : s * p.tok);
+#pragma unroll 1
+      for (int r0 = cw * 32; r0 < cw * 32 + 32 && cw * 32 < rows; r0 += kBatch * kAtOnce) {  // (rows past the last: zeros)
+        uint4 x[kBatch];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int r = r0 + e * kAtOnce + lane / kLanes, tok = r / p.group;
+          x[e] = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + (q0 + tok) * p.q_stride +
+                                                        (1LL * kvh * p.group + (r - tok * p.group)) * D + col * 8));
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          const int r = r0 + e * kAtOnce + lane / kLanes;
+          uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu), __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
+          m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+          for (int d = 1; d < kLanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+          // the row's largest value into [2^14, 2^15)
+          const int ex = max(int(m >> 7) - 127, -100) - 14;
+          const float f = exp2i(-ex);
+          const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+          uint32_t z[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) z[k] = f16x2_of(u2f(y[k] << 16) * f, u2f(y[k] & 0xffff0000u) * f);
+          *reinterpret_cast<uint4*>(sQ + b * C::kTileBytes + (col >> 3) * 16384 + r * 128 + (((col & 7) ^ (r & 7)) << 4)) =
+              make_uint4(z[0], z[1], z[2], z[3]);
+          if (col == 0) ctl.codes.q_exp[i % kItems][s][r] = int8_t(ex);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.q_full[b]);
+    }
+    if (!ok) break;
+    const int d = min(key ? 2 : 1, nt);
+#pragma unroll 1
+    for (int x = 0; x < 2 * nt; ++x) {
+      // the ring's entries: K(0..d-1), then V(t), K(t + d) in turn, then the last V
+      const int y = x - d;
+      const bool is_v = y >= 0 && (y >= 2 * (nt - d) || (y & 1) == 0);
+      const int t = y < 0 ? x : y >= 2 * (nt - d) ? y - (nt - d) : (y >> 1) + ((y & 1) ? d : 0);
+      const uint32_t entry = base + uint32_t(x), slot = entry % C::kSlots;
+      if (!is_v) {
+        if (lane < 2)
+          ctl.codes.sc[(tiles0 + t) % kScaleTiles][2 * cw + lane] =
+              make_float4(next.x * p.scale_log2, __log2f(next.y), __fdividef(1.0f, next.y), 0.0f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.codes.sc_full[(tiles0 + t) % kScaleTiles]);
+        next = read(t + 1, page1);
+        page1 = look_up(t + 2);
+      }
+      ok = warp_wait(&ctl.codes.raw_full[slot], (entry / C::kSlots) & 1, &ctl.abort, LIM);
+      if (!ok) break;
+      if (!is_v && threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 14);
+      uint8_t* const tile = sKV + slot * C::kTileBytes;
+      uint8_t* const mine = tile + cw * 4096;
+      constexpr int kHalves = D / 64;
+      uint4 c[4][kHalves];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          c[g][h] = *reinterpret_cast<const uint4*>(
+              mine + (g * 8 + in8) * D + (D == 128 ? ((h * 4 + quarter) ^ in8) << 4 : quarter << 4));
+      if (is_v && t == nt - 1 && fill != 0) {  // rows past the sequence's end: 0 * NaN would stay NaN
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (cw * 32 + g * 8 + in8 >= fill)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) c[g][h] = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();  // the warp's codes have been read: its rows may be written over them
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          const uint32_t z[4] = {c[g][h].x, c[g][h].y, c[g][h].z, c[g][h].w};
+          uint32_t f[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            f[2 * k] = f16x2_of_e4m3x2(uint16_t(z[k]));
+            f[2 * k + 1] = f16x2_of_e4m3x2(uint16_t(z[k] >> 16));
+          }
+          uint8_t* const to = tile + h * 16384 + (cw * 32 + g * 8 + in8) * 128;
+          *reinterpret_cast<uint4*>(to + (((2 * quarter) ^ in8) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+          *reinterpret_cast<uint4*>(to + (((2 * quarter + 1) ^ in8) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+        }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (!is_v && threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 15);
+      if (lane == 0) mbar_arrive(&ctl.kv_full[slot]);
+    }
+    base += uint32_t(2 * nt);
+    tiles0 += uint32_t(nt);
+    if (ok) release_item(ctl, i);
+  }
+}
+
+// O's columns of a warp's rows times alpha
+template <int D>
+__device__ __forceinline__ void codes_rescale(uint32_t t_o, float alpha) {
+  const uint64_t a2 = pack2(alpha, alpha);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t x[16];
+    tmem_ld16(t_o + c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float a, b;
+      unpack2(fmul2(pack2(u2f(x[e]), u2f(x[e + 1])), a2), a, b);
+      x[e] = f2u(a);
+      x[e + 1] = f2u(b);
+    }
+    tmem_st16(t_o + c, x);
+  }
+}
+
+// Codes: softmax of stage s, rows [32 wq, 32 wq + 32), with O's corrections and the epilogue.
+template <int D>
+__device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl, uint32_t tmem, int s, int wq, int lane,
+                                              uint64_t LIM) {
+  const int row = (wq << 5) + lane;
+  const uint32_t t_lane = tmem + (uint32_t(wq) << 21), t_s = t_lane + uint32_t(s * 128), t_o = t_lane + kOCol0 + uint32_t(s * D);
+  const int row_tok = row / p.group, row_head = row - row_tok * p.group;
+  // ph_of: phases of o_full, bit 0 of this stage's, bit 1 of stage 1's for stage 0. A
+  // stage's phase ends with each item that it has tiles of, also where the other's
+  // warps wait for it: the bit then turns without a wait (the next wait for it comes
+  // after an S that was issued behind those products).
+  uint32_t ph_s = 0, ph_st = 0, ph_of = 0;
+  int step0 = 0;        // running key-tile counter (trace only)
+  uint32_t tiles0 = 0;  // key tiles of the items before
+  bool ok = true;
+  if (lane == 0) mbar_arrive(&ctl.p_full[s]);  // O may be written
+  for (int i = 0; ok; ++i) {
+    const Work* const w = next_item(ctl, i, LIM);
+    if (w == nullptr) break;
+    const bool key = (w->flags & kKeyMode) != 0;
+    const int step = step0 + w->a[s];
+    step0 += key ? w->n[0] : w->nt;
+    const int n = w->n[s];
+    const bool mine = (wq << 5) < w->rows[s];  // the warp has rows
+    uint32_t tile = tiles0 + uint32_t(key ? s : w->a[s]);
+    tiles0 += uint32_t(w->nt);
+    float m_run = kLow, l_run = 0.0f, rf = 0.0f;
+    if (n > 0) {
+      const int stage_pos = w->pos + (key ? 0 : s * p.tok);
+      const int pos = stage_pos + row_tok;  // this row's place among the keys
+      const int pos_l = stage_pos + (key ? w->ntok : s == 0 ? p.tok : w->ntok - p.tok) - 1;  // the last row's
+      const int klen = w->klen;
+      int kb = (w->kt + (key ? s : w->a[s])) * 128;  // the tile's first key
+      for (int j = 0; j < n; ++j, kb += key ? 256 : 128, tile += key ? 2 : 1) {
+        if (!warp_wait(&ctl.s_full[s], ph_s, &ctl.abort, LIM)) { ok = false; break; }
+        ph_s ^= 1;
+        if (row == 0) trace_stamp(p.trace, step + j, 4 + 3 * s);
+        if (mine) {
+          tc_fence_after();
+          // the scales of the tile's blocks (and, before them, the rows' powers of two)
+          const uint32_t ring = tile % kScaleTiles, use = tile / kScaleTiles;
+          if (!warp_wait(&ctl.codes.sc_full[ring], use & 1, &ctl.abort, LIM)) { ok = false; break; }
+          if (j == 0) rf = exp2i(ctl.codes.q_exp[i % kItems][key ? 0 : s][row]);
+          const float4* const sc = ctl.codes.sc[ring];
+          const bool edge = kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl);
+          int hi = klen - kb, lo = 0;  // columns [lo, hi) are visible
+          if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
+          if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
+          const uint32_t span = uint32_t(max(hi - lo, 0));
+          // The exponents are made with the maximum as it stands, and their own
+          // maximum with them: one that passes it by more than kTau is rare after an
+          // item's first tile. Then S is read again, and O and the row sum are
+          // multiplied by what the new maximum makes of them. (Maximum first and then
+          // exponents, with a warp of its own for O's factors: 2.45 us a tile.)
+          uint32_t v[128];
+          auto load = [&] {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+            tmem_wait_ld();
+            if (edge) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+            }
+          };
+          // v times its scales, plus `base`, in place; returns the largest
+          auto exponents = [&](float base) -> float {
+            float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+              const float4 t = sc[b];
+              // (a product of scales that underflows would make -inf * 0 of a masked score)
+              const float f = fmaxf(t.x * rf, 1.1754944e-38f), x = t.y + base;
+              const uint64_t f2 = pack2(f, f), x2 = pack2(x, x);
+#pragma unroll
+              for (int c = 16 * b; c < 16 * b + 16; c += 4) {
+                float y0, y1, y2, y3;
+                unpack2(ffma2(pack2(u2f(v[c]), u2f(v[c + 1])), f2, x2), y0, y1);
+                unpack2(ffma2(pack2(u2f(v[c + 2]), u2f(v[c + 3])), f2, x2), y2, y3);
+                ma = fmax3(ma, y0, y1);
+                mb = fmax3(mb, y2, y3);
+                v[c] = f2u(y0);
+                v[c + 1] = f2u(y1);
+                v[c + 2] = f2u(y2);
+                v[c + 3] = f2u(y3);
+              }
+            }
+            return fmaxf(ma, mb);
+          };
+          load();
+          // (each row for itself, so that no row's roundings depend on its neighbours)
+          const bool over = exponents(kShift - m_run) > kShift + kTau;
+          if (__any_sync(0xffffffffu, over)) {
+            load();
+            const float mx = exponents(0.0f), m_new = over ? fmaxf(m_run, mx) : m_run;
+            const float alpha = ex2_mufu(m_run - m_new);  // (0 for the first)
+            m_run = m_new;
+            l_run *= alpha;
+            load();
+            exponents(kShift - m_run);
+            if (j > 0) codes_rescale<D>(t_o, alpha);  // S is there, so the product before it is done
+          }
+          if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
+          uint32_t pk[16];
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float a = ex2_mufu(u2f(v[16 * b + 2 * c])), e = ex2_mufu(u2f(v[16 * b + 2 * c + 1]));
+              const uint64_t pr = pack2(a, e);
+              if ((c & 1) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
+              if ((c & 1) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
+              // P' to f16 (nearest even), the type of the products: off by at most
+              // 2^-12 of each that is 2^-21 of the largest; the row sum keeps 32 bits
+              pk[8 * (b & 1) + c] = f16x2_of(a, e);
+            }
+            float la, lb;
+            unpack2(fadd2(acc0, acc1), la, lb);
+            l_run = fmaf(la + lb, sc[b].z, l_run);
+            if (b & 1) tmem_st16(t_s + (b >> 1) * 16, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
+        }
+        if (lane == 0) {
+          mbar_arrive(&ctl.p_full[s]);
+          if (j > 0) mbar_arrive(&ctl.p_full[s]);  // for O
+        }
+      }
+      if (!ok) break;
+    }
+    // ---- epilogue: O and l are 2^kShift of what belongs to m
+    float m = m_run == kLow ? -INFINITY : m_run - kShift, l = l_run;
+    if (key && s == 1) {  // joined by stage 0's warps
+      if (n > 0) {
+        if (!warp_wait(&ctl.stats_empty[1], ph_st ^ 1, &ctl.abort, LIM)) break;
+        ph_st ^= 1;
+        ctl.stat_l[1][row] = l;
+        ctl.stat_m[1][row] = m;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.stats_full[1]);
+        ph_of ^= 1;
+      }
+      release_item(ctl, i);
+      continue;
+    }
+    const int nj = key ? w->n[1] : 0;  // > 0: stage 1 is joined
+    if (s == 0 && !key && w->n[1] > 0) ph_of ^= 2;
+    float f0 = 1.0f, f1 = 0.0f;
+    if (nj > 0) {
+      if (!warp_wait(&ctl.stats_full[1], ph_st, &ctl.abort, LIM)) break;
+      ph_st ^= 1;
+      const float l1 = ctl.stat_l[1][row], m1 = ctl.stat_m[1][row];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.stats_empty[1]);
+      const float mj = fmaxf(m, m1), mu = mj == -INFINITY ? 0.0f : mj;
+      f0 = ex2_mufu(m - mu);  // (0 for a stage that saw no key)
+      f1 = ex2_mufu(m1 - mu);
+      l = l * f0 + l1 * f1;
+      m = mj;
+    }
+    const bool part = (w->flags & kPart) != 0;
+    const float inv = part ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+    f0 *= inv;
+    f1 *= inv;
+    if (n > 0) {
+      if (!warp_wait(&ctl.o_full[s], ph_of & 1, &ctl.abort, LIM)) break;
+      ph_of ^= 1;
+      if (nj > 0) {
+        if (!warp_wait(&ctl.o_full[1], (ph_of >> 1) & 1, &ctl.abort, LIM)) break;
+        ph_of ^= 2;
+      }
+      tc_fence_after();
+    }
+    if (mine) {
+      const bool valid = row < w->rows[s];
+      const int token = w->q0 + s * p.tok + row_tok, head = w->kvh * p.group + row_head;
+      const size_t at = size_t(2 * int(blockIdx.x) + ((w->flags & kCont) ? 0 : 1)) * 256 + s * 128 + row;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t x[32];
+        tmem_ld32(t_o + c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = n > 0 ? f2u(u2f(x[e]) * f0) : 0u;
+        if (nj > 0) {
+#pragma unroll
+          for (int h = 0; h < 32; h += 16) {
+            uint32_t y[16];
+            tmem_ld16(t_o + D + c + h, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[h + e] = f2u(fmaf(u2f(y[e]), f1, u2f(x[h + e])));
+          }
+        }
+        if (!valid) continue;
+        if (part) {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.o + (size_t(token) * p.Hq + head) * D + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t* z = &x[8 * e];
+            dst[e] = make_uint4(pack_bf16x2(u2f(z[0]), u2f(z[1])), pack_bf16x2(u2f(z[2]), u2f(z[3])),
+                                pack_bf16x2(u2f(z[4]), u2f(z[5])), pack_bf16x2(u2f(z[6]), u2f(z[7])));
+          }
+        }
+      }
+      if (valid) {
+        if (part) {
+          p.part_ml[at] = make_float2(m, l);
+        } else {
+          p.lse[size_t(head) * p.total_q + token] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+        }
+      }
+    }
+    if (n > 0) {  // the next item's products may overwrite O
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.p_full[s]);
+        if (nj > 0) mbar_arrive(&ctl.p_full[1]);
+      }
+    }
+    if (row == 0) trace_stamp(p.trace, step0 - 1, 12 + s);
+    release_item(ctl, i);
+  }
+}
+
 template <int D, Kind KIND>
-__global__ void __launch_bounds__(threads_of(KIND), 1)
+__global__ void __launch_bounds__(kThreads, 1)
     seq_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const Params p) {
   using C = Tiles<D>;
@@ -257,7 +677,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     ctl.abort = 0;
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ctl.it_full[i], 1);
-      mbar_init(&ctl.it_empty[i], threads_of(KIND) / 32 - 1);  // every warp but this one's
+      mbar_init(&ctl.it_empty[i], 15);  // every warp but this one's
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.q_full[s], CODES ? 4 : 1);
@@ -296,21 +716,22 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
   grid_dep_wait();    // the plan
   grid_dep_launch();  // the joining kernel may start (and wait) meanwhile
   const uint32_t tmem = ctl.tmem_base;
-  // item i of this CTA, or null when there is none (or a wait ran out)
-  auto item = [&](int i) -> const Work* {
-    if (!warp_wait(&ctl.it_full[i % kItems], (i / kItems) & 1, abort_flag, LIM)) return nullptr;
-    const Work* x = &ctl.it[i % kItems];
-    return x->flags < 0 ? nullptr : x;
-  };
-  // by each warp once all its lanes have read the item: warp 15 may then write the next one over it
-  auto release = [&](int i) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
-  };
+  auto item = [&](int i) { return next_item(ctl, i, LIM); };
+  auto release = [&](int i) { release_item(ctl, i); };
 
-  if (wg <= 1) {
+  if (CODES && wg <= 2) {
+    if constexpr (CODES) {
+      if (wg <= 1) {
+        setmaxnreg_inc<168>();
+        codes_softmax<D>(p, ctl, tmem, wg, warp & 3, lane, LIM);
+      } else {
+        setmaxnreg_dec<104>();
+        codes_convert<D>(p, ctl, sQ, sKV, warp & 3, lane, LIM);
+      }
+    }
+  } else if (wg <= 1) {
     // ------------------------------------------------------------ softmax
-    setmaxnreg_inc<CODES ? kRegsSoftmax8 : 168>();
+    setmaxnreg_inc<168>();
     const int s = wg, wq = warp & 3;
     const int row = (wq << 5) + lane;
     const uint32_t t_s = tmem + (uint32_t(wq) << 21) + uint32_t(s * 128);  // lane quarter + S columns
@@ -318,7 +739,6 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     const int row_tok = row / p.group;
     uint32_t ph_s = 0, ph_st = 0;
     int step0 = 0;  // running key-tile counter (trace only)
-    [[maybe_unused]] uint32_t tiles0 = 0;  // key tiles of the items before
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const Work* const w = item(i);
@@ -326,9 +746,6 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       const bool key = (w->flags & kKeyMode) != 0;
       const int step = step0 + w->a[s];
       step0 += key ? w->n[0] : w->nt;
-      [[maybe_unused]] uint32_t tile = tiles0 + uint32_t(key ? s : w->a[s]);
-      tiles0 += uint32_t(w->nt);
-      [[maybe_unused]] float rf = 0.0f;
       const int n = w->n[s];
       const bool mine = (wq << 5) < w->rows[s];  // the warp has rows
       float m_run = -INFINITY, l_run = 0.0f;
@@ -344,7 +761,6 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
           ph_s ^= 1;
           if (row == 0) trace_stamp(p.trace, step + j, 4 + 3 * s);
           if (!mine) {
-            if constexpr (CODES) tile += key ? 2 : 1;
             if (lane == 0) {
               if (j > 0) mbar_arrive(&ctl.alpha_full[s]);
               mbar_arrive(&ctl.p_full[s]);
@@ -352,188 +768,79 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
             continue;
           }
           tc_fence_after();
-          if constexpr (CODES) {
-            // The scales of the tile's blocks (and, before them, the rows' powers of two).
-            const uint32_t ring = tile % kScaleTiles, use = tile / kScaleTiles;
-            tile += key ? 2 : 1;
-            if (!warp_wait(&ctl.codes.sc_full[ring], use & 1, abort_flag, LIM)) { ok = false; break; }
-            if (j == 0) rf = exp2i(ctl.codes.q_exp[i % kItems][key ? 0 : s][row]);
-            const float4* const sc = ctl.codes.sc[ring];
-            int hi = klen - kb, lo = 0;  // columns [lo, hi) are visible
-            const bool edge = kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl);
+          uint32_t v[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+          tmem_wait_ld();
+          // masked where the tile reaches past the keys or crosses a bound of some row
+          if (kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl)) {
+            int hi = klen - kb;  // columns [lo, hi) are visible
+            int lo = 0;
             if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
             if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
             const uint32_t span = uint32_t(max(hi - lo, 0));
-            // The lower half of S is read twice, for its maximum and for its exponentials:
-            // its 64 registers are what 640 threads have less than 512.
-            uint32_t v[64], x[32];
-            auto masked = [&](uint32_t* y, int c0) {
+            // only the blocks of 32 columns that some row of the warp does not
+            // see whole: code that runs once per item is slow to fetch
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (uint32_t(c0 + c - lo) >= span) y[c] = f2u(-INFINITY);
-            };
-            // (a product of scales that underflows would make -inf * 0 of a masked score)
-            auto factor = [&](float a) { return fmaxf(a * rf, 1.1754944e-38f); };
-            float mx = -INFINITY;
-            auto maximum = [&](const uint32_t* y, int b) {  // of blocks b, b + 1
+            for (int b = 0; b < 128; b += 32) {
+              if (lo <= b && hi >= b + 32) continue;
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t* z = y + 16 * h;
-                float a = fmax3(u2f(z[0]), u2f(z[1]), u2f(z[2])), c = fmax3(u2f(z[3]), u2f(z[4]), u2f(z[5]));
-                a = fmax3(a, u2f(z[6]), u2f(z[7]));
-                c = fmax3(c, u2f(z[8]), u2f(z[9]));
-                a = fmax3(a, u2f(z[10]), u2f(z[11]));
-                c = fmax3(c, u2f(z[12]), u2f(z[13]));
-                a = fmax3(a, u2f(z[14]), u2f(z[15]));
-                const float4 t = sc[b + h];
-                mx = fmaxf(mx, fmaf(fmaxf(a, c), factor(t.x), t.y));
-              }
-            };
-            tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-            tmem_wait_ld();
-            if (edge) masked(v, 0), masked(v + 32, 32);
-            maximum(v, 0);
-            maximum(v + 32, 2);
-            tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-            tmem_wait_ld();
-            if (edge) masked(v, 64), masked(v + 32, 96);
-            maximum(v, 4);
-            maximum(v + 32, 6);
-            const float m_new = (mx > m_run + kTau) ? mx : m_run;
-            const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
-            const float alpha = ex2_mufu(m_run - m_use);
-            if (j > 0) {
-              ctl.alpha[s][row] = alpha;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
+              for (int c = b; c < b + 32; ++c)
+                if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
             }
-            const float base = kShift - m_use;
-            l_run *= alpha;
-            m_run = m_new;
-            uint32_t pk[16];
-            auto exponentials = [&](const uint32_t* y, int b) {  // of blocks b, b + 1
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float4 t = sc[b + h];
-                const float f = factor(t.x), n = t.y + base;
-                const uint64_t f2 = pack2(f, f), n2 = pack2(n, n);
-                uint64_t acc0 = 0, acc1 = 0;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                  const uint64_t z = ffma2(pack2(u2f(y[16 * h + 2 * c]), u2f(y[16 * h + 2 * c + 1])), f2, n2);
-                  float a, e;
-                  unpack2(z, a, e);
-                  a = ex2_mufu(a);
-                  e = ex2_mufu(e);
-                  const uint64_t pr = pack2(a, e);
-                  if ((c & 1) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
-                  if ((c & 1) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
-                  // P' to f16 (nearest even), the type of the products: off by at most
-                  // 2^-12 of each that is 2^-21 of the largest; the row sum keeps 32 bits
-                  pk[8 * h + c] = f16x2_of(a, e);
-                }
-                float la, lb;
-                unpack2(fadd2(acc0, acc1), la, lb);
-                l_run = fmaf(la + lb, t.z, l_run);
-              }
-            };
-            // P' of the upper half over the first columns of S's upper half, that of
-            // the lower half over those of the lower
-            tmem_ld32(t_s, x);
-            exponentials(v, 4);
-            tmem_st16(t_s + 64, pk);
-            exponentials(v + 32, 6);
-            tmem_st16(t_s + 80, pk);
-            tmem_wait_ld();
-            tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            if (edge) masked(x, 0);
-            exponentials(x, 0);
-            tmem_wait_ld();
-            tmem_st16(t_s, pk);
-            if (edge) masked(v, 32);
-            exponentials(v, 2);
-            tmem_st16(t_s + 16, pk);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.p_full[s]);
-          } else {
-            uint32_t v[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
-            tmem_wait_ld();
-            // masked where the tile reaches past the keys or crosses a bound of some row
-            if (kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl)) {
-              int hi = klen - kb;  // columns [lo, hi) are visible
-              int lo = 0;
-              if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
-              if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
-              const uint32_t span = uint32_t(max(hi - lo, 0));
-              // only the blocks of 32 columns that some row of the warp does not
-              // see whole: code that runs once per item is slow to fetch
-#pragma unroll
-              for (int b = 0; b < 128; b += 32) {
-                if (lo <= b && hi >= b + 32) continue;
-#pragma unroll
-                for (int c = b; c < b + 32; ++c)
-                  if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
-              }
-            }
-            float mA = -INFINITY, mB = -INFINITY, mC = -INFINITY, mD = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 128; c += 8) {
-              mA = fmax3(mA, u2f(v[c]), u2f(v[c + 1]));
-              mB = fmax3(mB, u2f(v[c + 2]), u2f(v[c + 3]));
-              mC = fmax3(mC, u2f(v[c + 4]), u2f(v[c + 5]));
-              mD = fmax3(mD, u2f(v[c + 6]), u2f(v[c + 7]));
-            }
-            const float mx = fmaxf(fmaxf(mA, mB), fmaxf(mC, mD));
-            const float m_cand = fmaxf(m_run, mx * sl);
-            const float m_new = (m_cand > m_run + kTau) ? m_cand : m_run;
-            const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
-            const float alpha = ex2_mufu(m_run - m_use);
-            if (j > 0) {  // (there is no O to correct before the first)
-              ctl.alpha[s][row] = alpha;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
-            }
-            if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
-            const uint64_t sl2 = pack2(sl, sl);
-            const uint64_t nm2 = pack2(-m_use, -m_use);
-            uint64_t acc0 = 0, acc1 = 0, acc2 = 0, acc3 = 0;
-            uint32_t pk[64];
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const uint64_t y = ffma2(pack2(u2f(v[2 * c]), u2f(v[2 * c + 1])), sl2, nm2);
-              float a, b;
-              unpack2(y, a, b);
-              a = ex2_mufu(a);
-              b = ex2_mufu(b);
-              const uint64_t pr = pack2(a, b);
-              if ((c & 3) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
-              if ((c & 3) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
-              if ((c & 3) == 2) acc2 = c == 2 ? pr : fadd2(acc2, pr);
-              if ((c & 3) == 3) acc3 = c == 3 ? pr : fadd2(acc3, pr);
-              // P to bf16 (nearest even), the type that the P V product takes
-              // beside a bf16 V: off by at most 2^-8 of each probability; the row
-              // sum keeps the 32-bit values
-              pk[c] = pack_bf16x2(a, b);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[c * 16]));
-            const uint64_t acc = fadd2(fadd2(acc0, acc1), fadd2(acc2, acc3));
-            float la, lb;
-            unpack2(acc, la, lb);
-            l_run = fmaf(l_run, alpha, la + lb);
-            m_run = m_new;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
-            if (lane == 0) mbar_arrive(&ctl.p_full[s]);
           }
+          float mA = -INFINITY, mB = -INFINITY, mC = -INFINITY, mD = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 128; c += 8) {
+            mA = fmax3(mA, u2f(v[c]), u2f(v[c + 1]));
+            mB = fmax3(mB, u2f(v[c + 2]), u2f(v[c + 3]));
+            mC = fmax3(mC, u2f(v[c + 4]), u2f(v[c + 5]));
+            mD = fmax3(mD, u2f(v[c + 6]), u2f(v[c + 7]));
+          }
+          const float mx = fmaxf(fmaxf(mA, mB), fmaxf(mC, mD));
+          const float m_cand = fmaxf(m_run, mx * sl);
+          const float m_new = (m_cand > m_run + kTau) ? m_cand : m_run;
+          const float m_use = (m_new == -INFINITY) ? 0.0f : m_new;
+          const float alpha = ex2_mufu(m_run - m_use);
+          if (j > 0) {  // (there is no O to correct before the first)
+            ctl.alpha[s][row] = alpha;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
+          }
+          if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
+          const uint64_t sl2 = pack2(sl, sl);
+          const uint64_t nm2 = pack2(-m_use, -m_use);
+          uint64_t acc0 = 0, acc1 = 0, acc2 = 0, acc3 = 0;
+          uint32_t pk[64];
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const uint64_t y = ffma2(pack2(u2f(v[2 * c]), u2f(v[2 * c + 1])), sl2, nm2);
+            float a, b;
+            unpack2(y, a, b);
+            a = ex2_mufu(a);
+            b = ex2_mufu(b);
+            const uint64_t pr = pack2(a, b);
+            if ((c & 3) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
+            if ((c & 3) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
+            if ((c & 3) == 2) acc2 = c == 2 ? pr : fadd2(acc2, pr);
+            if ((c & 3) == 3) acc3 = c == 3 ? pr : fadd2(acc3, pr);
+            // P to bf16 (nearest even), the type that the P V product takes
+            // beside a bf16 V: off by at most 2^-8 of each probability; the row
+            // sum keeps the 32-bit values
+            pk[c] = pack_bf16x2(a, b);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st16(t_s + c * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[c * 16]));
+          const uint64_t acc = fadd2(fadd2(acc0, acc1), fadd2(acc2, acc3));
+          float la, lb;
+          unpack2(acc, la, lb);
+          l_run = fmaf(l_run, alpha, la + lb);
+          m_run = m_new;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
+          if (lane == 0) mbar_arrive(&ctl.p_full[s]);
         }
         if (!ok) break;
       }
@@ -541,7 +848,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         if (!warp_wait(&ctl.stats_empty[s], ph_st ^ 1, abort_flag, LIM)) { ok = false; break; }
         ph_st ^= 1;
         ctl.stat_l[s][row] = l_run;
-        ctl.stat_m[s][row] = CODES ? m_run - kShift : m_run;  // (of codes O and l are 2^kShift of what belongs to m)
+        ctl.stat_m[s][row] = m_run;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.stats_full[s]);
       }
@@ -549,7 +856,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
     }
   } else if (wg == 2) {
     // ------------------------------------------------ correction + epilogue
-    setmaxnreg_dec<CODES ? kRegsCorrection8 : 104>();
+    setmaxnreg_dec<104>();
     const int wq = warp & 3;
     const int row = (wq << 5) + lane;
     const uint32_t t_lane = tmem + (uint32_t(wq) << 21) + kOCol0;
@@ -734,158 +1041,8 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
       release(i);
     }
     if (lane == 0) bulk_wait_all();  // stores complete (and staging reads done) before the CTA exits
-  } else if (wg == 3) {
-    setmaxnreg_dec<CODES ? kRegsOther8 : 72>();
-  }
-  if constexpr (CODES) {
-    if (wg == 4) {
-      // ------------------------------------------------ codes to f16
-      setmaxnreg_dec<kRegsCodes>();
-      const int cw = warp & 3;  // rows [32 cw, 32 cw + 32) of a tile
-      uint32_t base = 0, q_uses[2] = {0, 0}, key_items = 0, tiles0 = 0;
-      bool ok = true;
-      // A lane reads 16 codes of a row and writes them as two pieces of 8 values.
-      // Four lanes have half a row (d = 128); the rows of neighbouring fours differ in
-      // bits 0 and 2, so that neither the reads of codes (128-byte swizzle, or rows of 64
-      // bytes) nor the writes meet in a bank.
-      const int in8 = (0x63724150u >> (4 * (lane >> 2))) & 7, quarter = lane & 3;
-      // this lane's block of a tile (lanes 0, 1) and its scales, looked up two tiles ahead, read one ahead
-      for (int i = 0; ok; ++i) {
-        const Work* const w = item(i);
-        if (w == nullptr) break;
-        const int nt = w->nt, kvh = w->kvh, kt = w->kt, klen = w->klen, fill = w->fill;
-        const bool key = (w->flags & kKeyMode) != 0;
-        const int seen = p.wl >= 0 ? w->pos - p.wl : 0;  // the first key that a row of the item sees
-        const int* const row_of_table = p.table + size_t(w->kbase) * p.max_pages;
-        // row of the scales of block 2 cw + lane of tile t, or -1: not used
-        auto block_key = [&](int t) { return ((kt + t) * 8 + 2 * cw + lane) * kFp8Block; };
-        auto look_up = [&](int t) {
-          const int k = block_key(t);
-          return t < nt && lane < 2 && k < klen && k + kFp8Block > seen ? row_of_table[k / p.page_size] : -1;
-        };
-        auto read = [&](int t, int page) {
-          float2 r = make_float2(1.0f, 1.0f);
-          if (page >= 0 && page < p.num_pages) {
-            const int k = block_key(t);
-            const size_t at = (size_t(page) * (p.page_size / kFp8Block) + k % p.page_size / kFp8Block) * p.Hkv + kvh;
-            r.x = p.scales[0][at];
-            r.y = p.scales[1][at];
-          }
-          return r;
-        };
-        int page0 = look_up(0);
-        int page1 = look_up(1);
-        float2 next = read(0, page0);
-        // Q's rows, as the producer of bf16 tiles loads them: 16 bytes a lane
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (w->n[s] == 0 || (key && s == 1)) continue;
-          const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
-          ok = warp_wait(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1, abort_flag, LIM);
-          if (!ok) break;
-          if (b == 0) {
-            ++q_uses[0];
-          } else {
-            ++q_uses[1];
-          }
-          constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
-          const int rows = w->rows[s], col = lane % kLanes;
-          const int q0 = w->q0 + (key ? 0 : s * p.tok);
-#pragma unroll 1
-          for (int r0 = cw * 32; r0 < min(rows, cw * 32 + 32); r0 += kBatch * kAtOnce) {
-            uint4 x[kBatch];
-#pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-              const int r = r0 + e * kAtOnce + lane / kLanes, tok = r / p.group;
-              x[e] = make_uint4(0, 0, 0, 0);
-              if (r < rows)
-                x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + (q0 + tok) * p.q_stride +
-                                                            (1LL * kvh * p.group + (r - tok * p.group)) * D + col * 8));
-            }
-#pragma unroll
-            for (int e = 0; e < kBatch; ++e) {
-              const int r = r0 + e * kAtOnce + lane / kLanes;
-              uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu), __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
-              m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-              for (int d = 1; d < kLanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-              // the row's largest value into [2^14, 2^15)
-              const int ex = max(int(m >> 7) - 127, -100) - 14;
-              const float f = exp2i(-ex);
-              const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-              uint32_t z[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) z[k] = f16x2_of(u2f(y[k] << 16) * f, u2f(y[k] & 0xffff0000u) * f);
-              *reinterpret_cast<uint4*>(sQ + b * C::kTileBytes + (col >> 3) * 16384 + r * 128 + (((col & 7) ^ (r & 7)) << 4)) =
-                  make_uint4(z[0], z[1], z[2], z[3]);
-              if (col == 0) ctl.codes.q_exp[i % kItems][s][r] = int8_t(ex);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.q_full[b]);
-        }
-        if (!ok) break;
-        const int d = min(key ? 2 : 1, nt);
-#pragma unroll 1
-        for (int x = 0; x < 2 * nt; ++x) {
-          // the ring's entries: K(0..d-1), then V(t), K(t + d) in turn, then the last V
-          const int y = x - d;
-          const bool is_v = y >= 0 && (y >= 2 * (nt - d) || (y & 1) == 0);
-          const int t = y < 0 ? x : y >= 2 * (nt - d) ? y - (nt - d) : (y >> 1) + ((y & 1) ? d : 0);
-          const uint32_t entry = base + uint32_t(x), slot = entry % C::kSlots;
-          if (!is_v) {
-            if (lane < 2)
-              ctl.codes.sc[(tiles0 + t) % kScaleTiles][2 * cw + lane] =
-                  make_float4(next.x * p.scale_log2, __log2f(next.y), __fdividef(1.0f, next.y), 0.0f);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.codes.sc_full[(tiles0 + t) % kScaleTiles]);
-            next = read(t + 1, page1);
-            page1 = look_up(t + 2);
-          }
-          ok = warp_wait(&ctl.codes.raw_full[slot], (entry / C::kSlots) & 1, abort_flag, LIM);
-          if (!ok) break;
-          uint8_t* const tile = sKV + slot * C::kTileBytes;
-          uint8_t* const mine = tile + cw * 4096;
-          constexpr int kHalves = D / 64;
-          uint4 c[4][kHalves];
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-              c[g][h] = *reinterpret_cast<const uint4*>(
-                  mine + (g * 8 + in8) * D + (D == 128 ? ((h * 4 + quarter) ^ in8) << 4 : quarter << 4));
-          if (is_v && t == nt - 1 && fill != 0) {  // rows past the sequence's end: 0 * NaN would stay NaN
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (cw * 32 + g * 8 + in8 >= fill)
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) c[g][h] = make_uint4(0, 0, 0, 0);
-          }
-          __syncwarp();  // the warp's codes have been read: its rows may be written over them
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
-              const uint32_t z[4] = {c[g][h].x, c[g][h].y, c[g][h].z, c[g][h].w};
-              uint32_t f[8];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                f[2 * k] = f16x2_of_e4m3x2(uint16_t(z[k]));
-                f[2 * k + 1] = f16x2_of_e4m3x2(uint16_t(z[k] >> 16));
-              }
-              uint8_t* const to = tile + h * 16384 + (cw * 32 + g * 8 + in8) * 128;
-              *reinterpret_cast<uint4*>(to + (((2 * quarter) ^ in8) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-              *reinterpret_cast<uint4*>(to + (((2 * quarter + 1) ^ in8) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
-            }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.kv_full[slot]);
-        }
-        base += uint32_t(2 * nt);
-        tiles0 += uint32_t(nt);
-        if (ok) release(i);
-      }
-    }
+  } else {
+    setmaxnreg_dec<72>();
   }
   if (warp == 12 || warp == 14) {
     // ------------------------------------------------------ TMA producers
@@ -1077,8 +1234,7 @@ __global__ void __launch_bounds__(threads_of(KIND), 1)
         const uint32_t b0 = sdesc_step(dv, slot * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts_lo(tmem + kOCol0 + uint32_t(s * D), tmem + uint32_t(s * 128) + (CODES && kk >= 4 ? 64 + (kk - 4) * 8 : kk * 8),
-                    sdesc_step(b0, kk * 2048), idPV,
+          mma_ts_lo(tmem + kOCol0 + uint32_t(s * D), tmem + uint32_t(s * 128) + kk * 8, sdesc_step(b0, kk * 2048), idPV,
                     (acc || kk > 0) ? 1u : 0u);
       };
       auto issue_s = [&](int s, uint32_t b, uint32_t slot) {
@@ -1592,7 +1748,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(G);
-  lc.blockDim = dim3(threads_of(KIND));
+  lc.blockDim = dim3(kThreads);
   lc.dynamicSmemBytes = C::kSmemDyn;
   lc.stream = stream;
   lc.attrs = pdl;
