@@ -122,8 +122,8 @@ struct Tiles {
 };
 constexpr int kMaxSlots = 8;
 
-// bits of the MMA issuer's phases: Q loaded, P stored (a pair each)
-constexpr int kPhQ = 0, kPhP = 2;
+// bits of the MMA issuer's phases: Q loaded, P stored, of codes its second half (a pair each)
+constexpr int kPhQ = 0, kPhP = 2, kPhP2 = 4;
 
 // An item as the roles see it, laid out by warp 15. Its key tile t is taken by
 //   key mode: stage t & 1, as its step t >> 1;
@@ -471,67 +471,57 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
           if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
           if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
           const uint32_t span = uint32_t(max(hi - lo, 0));
-          // The exponents are made with the maximum as it stands, and their own
-          // maximum with them: one that passes it by more than kTau is rare after an
-          // item's first tile. Then S is read again, and O and the row sum are
-          // multiplied by what the new maximum makes of them. (Maximum first and then
-          // exponents, with a warp of its own for O's factors: 2.45 us a tile.)
           uint32_t v[128];
-          auto load = [&] {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
-            tmem_wait_ld();
-            if (edge) {
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+          tmem_wait_ld();
+          if (edge) {
 #pragma unroll
-              for (int c = 0; c < 128; ++c)
-                if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+            for (int c = 0; c < 128; ++c)
+              if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+          }
+          // (a product of scales that underflows would make -inf * 0 of a masked score)
+          auto factor = [&](float a) { return fmaxf(a * rf, 1.1754944e-38f); };
+          float mx = -INFINITY;
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const uint32_t* z = &v[16 * b];
+            float ma = fmax3(u2f(z[0]), u2f(z[1]), u2f(z[2])), mb = fmax3(u2f(z[3]), u2f(z[4]), u2f(z[5]));
+#pragma unroll
+            for (int c = 6; c < 14; c += 4) {
+              ma = fmax3(ma, u2f(z[c]), u2f(z[c + 1]));
+              mb = fmax3(mb, u2f(z[c + 2]), u2f(z[c + 3]));
             }
-          };
-          // v times its scales, plus `base`, in place; returns the largest
-          auto exponents = [&](float base) -> float {
-            float ma = -INFINITY, mb = -INFINITY;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-              const float4 t = sc[b];
-              // (a product of scales that underflows would make -inf * 0 of a masked score)
-              const float f = fmaxf(t.x * rf, 1.1754944e-38f), x = t.y + base;
-              const uint64_t f2 = pack2(f, f), x2 = pack2(x, x);
-#pragma unroll
-              for (int c = 16 * b; c < 16 * b + 16; c += 4) {
-                float y0, y1, y2, y3;
-                unpack2(ffma2(pack2(u2f(v[c]), u2f(v[c + 1])), f2, x2), y0, y1);
-                unpack2(ffma2(pack2(u2f(v[c + 2]), u2f(v[c + 3])), f2, x2), y2, y3);
-                ma = fmax3(ma, y0, y1);
-                mb = fmax3(mb, y2, y3);
-                v[c] = f2u(y0);
-                v[c + 1] = f2u(y1);
-                v[c + 2] = f2u(y2);
-                v[c + 3] = f2u(y3);
-              }
-            }
-            return fmaxf(ma, mb);
-          };
-          load();
-          // (each row for itself, so that no row's roundings depend on its neighbours)
-          const bool over = exponents(kShift - m_run) > kShift + kTau;
+            ma = fmaxf(fmax3(ma, u2f(z[14]), u2f(z[15])), mb);
+            const float4 t = sc[b];
+            mx = fmaxf(mx, fmaf(ma, factor(t.x), t.y));
+          }
+          // A maximum that passes the one held by more than kTau is rare after an item's
+          // first tile. (Each row for itself, so that no row's roundings depend on its
+          // neighbours.)
+          const bool over = mx > m_run + kTau;
           if (__any_sync(0xffffffffu, over)) {
-            load();
-            const float mx = exponents(0.0f), m_new = over ? fmaxf(m_run, mx) : m_run;
+            const float m_new = over ? mx : m_run;
             const float alpha = ex2_mufu(m_run - m_new);  // (0 for the first)
             m_run = m_new;
             l_run *= alpha;
-            load();
-            exponents(kShift - m_run);
             if (j > 0) codes_rescale<D>(t_o, alpha);  // S is there, so the product before it is done
           }
+          const float base = kShift - m_run;
           if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
           uint32_t pk[16];
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
+            const float4 t = sc[b];
+            const float f = factor(t.x), x = t.y + base;
+            const uint64_t f2 = pack2(f, f), x2 = pack2(x, x);
             uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float a = ex2_mufu(u2f(v[16 * b + 2 * c])), e = ex2_mufu(u2f(v[16 * b + 2 * c + 1]));
+              float a, e;
+              unpack2(ffma2(pack2(u2f(v[16 * b + 2 * c]), u2f(v[16 * b + 2 * c + 1])), f2, x2), a, e);
+              a = ex2_mufu(a);
+              e = ex2_mufu(e);
               const uint64_t pr = pack2(a, e);
               if ((c & 1) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
               if ((c & 1) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
@@ -541,17 +531,23 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
             }
             float la, lb;
             unpack2(fadd2(acc0, acc1), la, lb);
-            l_run = fmaf(la + lb, sc[b].z, l_run);
+            l_run = fmaf(la + lb, t.z, l_run);
             if (b & 1) tmem_st16(t_s + (b >> 1) * 16, pk);
+            if ((b & 3) == 3) {  // 64 keys' P' are there: their product may begin
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(b == 3 ? &ctl.p_full[s] : &ctl.alpha_full[s]);
+                if (b == 3 && j > 0) mbar_arrive(&ctl.p_full[s]);  // for O
+              }
+            }
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
           if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
-        }
-        if (lane == 0) {
+        } else if (lane == 0) {
           mbar_arrive(&ctl.p_full[s]);
-          if (j > 0) mbar_arrive(&ctl.p_full[s]);  // for O
+          if (j > 0) mbar_arrive(&ctl.p_full[s]);
+          mbar_arrive(&ctl.alpha_full[s]);
         }
       }
       if (!ok) break;
@@ -1228,12 +1224,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         return wait(&ctl.tail_done[slot], phase);
       };
       // O of stage s (+)= P V; S of stage s = Q (buffer b) K^T
+      // (over codes, where the softmax has more to do for a tile, the product of its
+      // first 64 keys does not wait for the others' P)
       auto issue_pv = [&](int s, uint32_t slot, bool acc) {
+        const uint32_t b0 = sdesc_step(dv, slot * C::kTileBytes);
+        if constexpr (CODES) {
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts_lo(tmem + kOCol0 + uint32_t(s * D), tmem + uint32_t(s * 128) + kk * 8, sdesc_step(b0, kk * 2048), idPV,
+                        (acc || kk > 0) ? 1u : 0u);
+          }
+          __syncwarp();
+          if (!wait_phase(&ctl.alpha_full[s], kPhP2 + s)) {
+            ok = false;
+            return;
+          }
+        }
         tc_fence_after();
         if (!elect_one()) return;
-        const uint32_t b0 = sdesc_step(dv, slot * C::kTileBytes);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
+        for (int kk = CODES ? 4 : 0; kk < 8; ++kk)
           mma_ts_lo(tmem + kOCol0 + uint32_t(s * D), tmem + uint32_t(s * 128) + kk * 8, sdesc_step(b0, kk * 2048), idPV,
                     (acc || kk > 0) ? 1u : 0u);
       };
