@@ -76,8 +76,7 @@ constexpr float kTau = 8.0f;  // rescale threshold (log2 units), as in the dense
 // --------------------------------------------------------------------------
 struct Params {
   __nv_bfloat16* o;
-  const __nv_bfloat16* q;  // codes: read by plain loads
-  long long q_stride;
+  const float* q_factor;   // codes: [total_q, Hq] what a row of Q was divided by
   float* lse;          // [Hq, total_q]
   const PlanHead* head;
   const int* first;
@@ -109,7 +108,7 @@ struct Params {
 //   softmax s   4+3s S ready, 5+3s alpha published, 6+3s P stored
 //   correction  10+s O released for PV
 //   epilogue s  12+s O written (step of the item's last tile)
-//   codes       14 a K tile's codes landed, 15 turned to f16
+//   codes       14 a V tile's codes landed, 15 turned to f16
 constexpr int kItems = 4;  // ring of work items
 
 template <int D>
@@ -149,12 +148,15 @@ struct Work {
 constexpr int kFewUnits = 304, kFewRounds = 4;
 
 //
-// Over a cache of codes (kCodes) the warps that correct O and write it elsewhere
-// stand between the producers and the products: a tile's codes land in the lower
-// half of its ring slot, a warp turns those of its 32 rows to f16 in place (every
-// e4m3 value is one), and Q's rows to f16 too, divided by a power of two of the
-// row. The scales of the tile's blocks of 16 keys go to the softmax: with a of K
-// and b of V,
+// Over a cache of codes (kCodes) the products take K as it is: S = (Q_hi + Q_lo) K^T
+// in e4m3, where a row of Q, divided by a power of two, is the sum of two e4m3
+// values, each off by at most half a step: exact for what is 2^-9 of the row's largest
+// value or more (bf16 has 8 bits, two e4m3 significands 4 each), and off by at most
+// 2^-17 of that largest below. The rate is twice that of 16 bits, so S takes as long.
+// P V wants P's 11 bits: V's codes land in the lower half of their ring slot, and the
+// warps that elsewhere correct O and write it turn those of 32 rows each to f16 in
+// place (every e4m3 value is one). The scales of the tile's blocks of 16 keys go to
+// the softmax: with a of K and b of V,
 //   x = scale log2(e) a (q . k^) + log2(b), P' = 2^(x - m + kShift), l = sum P' / b:
 // b in the exponent leaves the P V product without a further factor, and P' largest
 // where it weighs most. P' is at most 2^(kShift + kTau) = 2^15, which f16 holds.
@@ -162,10 +164,8 @@ constexpr float kShift = 7.0f;
 constexpr float kLow = -3.4028235e38f;  // the running maximum before any key
 constexpr int kScaleTiles = 8;  // ring of scales (a tile's are used before the tile seven on is converted)
 struct Codes {
-  uint64_t raw_full[kMaxSlots];    // a tile's codes have landed
   uint64_t sc_full[kScaleTiles];
   float4 sc[kScaleTiles][8];       // of each block: a scale log2(e), log2(b), 1 / b
-  int8_t q_exp[kItems][2][128];    // a row's power of two
 };
 struct NoCodes {};
 
@@ -179,7 +179,8 @@ struct __align__(16) Ctl {
   uint64_t it_full[kItems], it_empty[kItems];
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
-  uint64_t tail_done[kMaxSlots];  // a V tile that the sequence ends in: loaded, its rows past the end zeroed
+  // a V tile that the sequence ends in: loaded, its rows past the end zeroed; of codes any V tile, turned to f16
+  uint64_t tail_done[kMaxSlots];
   // p_full: P stored (4 softmax warps) and O corrected, or read by the epilogue
   // of the stage's item before (4 correction warps; over codes the 4 softmax warps
   // again, those of stage 0 for both where they join them)
@@ -250,12 +251,12 @@ __device__ __forceinline__ void release_item(Ctl<KIND>& ctl, int i) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
 }
 
-// Codes: rows [32 cw, 32 cw + 32) of Q's and of every key tile turned to f16.
+// Codes: rows [32 cw, 32 cw + 32) of every V tile turned to f16; the tiles' scales.
 template <int D>
-__device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl, uint8_t* sQ, uint8_t* sKV, int cw,
-                                              int lane, uint64_t LIM) {
+__device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl, uint8_t* sKV, int cw, int lane,
+                                              uint64_t LIM) {
   using C = Tiles<D>;
-  uint32_t base = 0, q_uses[2] = {0, 0}, key_items = 0, tiles0 = 0;
+  uint32_t base = 0, tiles0 = 0;
   bool ok = true;
   // A lane reads 16 codes of a row and writes them as two pieces of 8 values.
   // Four lanes have half a row (d = 128); the rows of neighbouring fours differ in
@@ -289,55 +290,6 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
     int page0 = look_up(0);
     int page1 = look_up(1);
     float2 next = read(0, page0);
-    // Q's rows, as the producer of bf16 tiles loads them: 16 bytes a lane
-    for (int s = 0; s < 2 && ok; ++s) {
-      if (w->n[s] == 0 || (key && s == 1)) continue;
-      const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
-      ok = warp_wait(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1, &ctl.abort, LIM);
-      if (!ok) break;
-      if (b == 0) {
-        ++q_uses[0];
-      } else {
-        ++q_uses[1];
-      }
-      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;
-      const int rows = w->rows[s], col = lane % kLanes;
-      const int q0 = w->q0 + (key ? 0 : s * p.tok);
-#pragma unroll 1
-      for (int r0 = cw * 32; r0 < cw * 32 + 32 && cw * 32 < rows; r0 += kBatch * kAtOnce) {  // (rows past the last: zeros)
-        uint4 x[kBatch];
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int r = r0 + e * kAtOnce + lane / kLanes, tok = r / p.group;
-          x[e] = make_uint4(0, 0, 0, 0);
-          if (r < rows)
-            x[e] = __ldg(reinterpret_cast<const uint4*>(p.q + (q0 + tok) * p.q_stride +
-                                                        (1LL * kvh * p.group + (r - tok * p.group)) * D + col * 8));
-        }
-#pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-          const int r = r0 + e * kAtOnce + lane / kLanes;
-          uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu), __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
-          m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-          for (int d = 1; d < kLanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-          // the row's largest value into [2^14, 2^15)
-          const int ex = max(int(m >> 7) - 127, -100) - 14;
-          const float f = exp2i(-ex);
-          const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-          uint32_t z[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) z[k] = f16x2_of(u2f(y[k] << 16) * f, u2f(y[k] & 0xffff0000u) * f);
-          *reinterpret_cast<uint4*>(sQ + b * C::kTileBytes + (col >> 3) * 16384 + r * 128 + (((col & 7) ^ (r & 7)) << 4)) =
-              make_uint4(z[0], z[1], z[2], z[3]);
-          if (col == 0) ctl.codes.q_exp[i % kItems][s][r] = int8_t(ex);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.q_full[b]);
-    }
-    if (!ok) break;
     const int d = min(key ? 2 : 1, nt);
 #pragma unroll 1
     for (int x = 0; x < 2 * nt; ++x) {
@@ -355,9 +307,12 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
         next = read(t + 1, page1);
         page1 = look_up(t + 2);
       }
-      ok = warp_wait(&ctl.codes.raw_full[slot], (entry / C::kSlots) & 1, &ctl.abort, LIM);
+      // (K's tiles too, whose codes stay: a phase that is not waited for might still be
+      // open at the next wait for the slot, which would then return at once)
+      ok = warp_wait(&ctl.kv_full[slot], (entry / C::kSlots) & 1, &ctl.abort, LIM);
       if (!ok) break;
-      if (!is_v && threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 14);
+      if (!is_v) continue;
+      if (threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 14);
       uint8_t* const tile = sKV + slot * C::kTileBytes;
       uint8_t* const mine = tile + cw * 4096;
       constexpr int kHalves = D / 64;
@@ -368,7 +323,7 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
         for (int h = 0; h < kHalves; ++h)
           c[g][h] = *reinterpret_cast<const uint4*>(
               mine + (g * 8 + in8) * D + (D == 128 ? ((h * 4 + quarter) ^ in8) << 4 : quarter << 4));
-      if (is_v && t == nt - 1 && fill != 0) {  // rows past the sequence's end: 0 * NaN would stay NaN
+      if (t == nt - 1 && fill != 0) {  // rows past the sequence's end: 0 * NaN would stay NaN
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           if (cw * 32 + g * 8 + in8 >= fill)
@@ -393,13 +348,27 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
         }
       fence_proxy_async_smem();
       __syncwarp();
-      if (!is_v && threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 15);
-      if (lane == 0) mbar_arrive(&ctl.kv_full[slot]);
+      if (threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 15);
+      if (lane == 0) mbar_arrive(&ctl.tail_done[slot]);
     }
     base += uint32_t(2 * nt);
     tiles0 += uint32_t(nt);
     if (ok) release_item(ctl, i);
   }
+}
+
+// The scales of a tile's block b. Reads that the compiler may move over the stores to
+// tensor memory, though not over the wait before scales_at (as it may with no plain
+// read): every second block waited for its own.
+__device__ __forceinline__ uint32_t scales_at(const float4* sc) {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(smem_u32(sc)) : "memory");
+  return r;
+}
+__device__ __forceinline__ float4 scales_of(uint32_t sc, int b) {
+  float4 r;
+  asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(sc + 16 * b));
+  return r;
 }
 
 // O's columns of a warp's rows times alpha
@@ -424,8 +393,8 @@ __device__ __forceinline__ void codes_rescale(uint32_t t_o, float alpha) {
 
 // Codes: softmax of stage s, rows [32 wq, 32 wq + 32), with O's corrections and the epilogue.
 template <int D>
-__device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl, uint32_t tmem, int s, int wq, int lane,
-                                              uint64_t LIM) {
+__device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl, uint32_t tmem, uint8_t* stg, int s, int wq,
+                                              int lane, uint64_t LIM) {
   const int row = (wq << 5) + lane;
   const uint32_t t_lane = tmem + (uint32_t(wq) << 21), t_s = t_lane + uint32_t(s * 128), t_o = t_lane + kOCol0 + uint32_t(s * D);
   const int row_tok = row / p.group, row_head = row - row_tok * p.group;
@@ -448,7 +417,10 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
     const bool mine = (wq << 5) < w->rows[s];  // the warp has rows
     uint32_t tile = tiles0 + uint32_t(key ? s : w->a[s]);
     tiles0 += uint32_t(w->nt);
-    float m_run = kLow, l_run = 0.0f, rf = 0.0f;
+    float m_run = kLow, l_run = 0.0f;
+    // the row's factor (rows past the last: those of other tokens, as Q's are)
+    const int f_token = min(w->q0 + (key ? 0 : s * p.tok) + row_tok, p.total_q - 1);
+    const float rf = mine ? __ldg(p.q_factor + size_t(f_token) * p.Hq + w->kvh * p.group + row_head) : 0.0f;
     if (n > 0) {
       const int stage_pos = w->pos + (key ? 0 : s * p.tok);
       const int pos = stage_pos + row_tok;  // this row's place among the keys
@@ -461,30 +433,35 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
         if (row == 0) trace_stamp(p.trace, step + j, 4 + 3 * s);
         if (mine) {
           tc_fence_after();
-          // the scales of the tile's blocks (and, before them, the rows' powers of two)
+          // the scales of the tile's blocks
           const uint32_t ring = tile % kScaleTiles, use = tile / kScaleTiles;
           if (!warp_wait(&ctl.codes.sc_full[ring], use & 1, &ctl.abort, LIM)) { ok = false; break; }
-          if (j == 0) rf = exp2i(ctl.codes.q_exp[i % kItems][key ? 0 : s][row]);
-          const float4* const sc = ctl.codes.sc[ring];
+          const uint32_t sc = scales_at(ctl.codes.sc[ring]);
           const bool edge = kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl);
           int hi = klen - kb, lo = 0;  // columns [lo, hi) are visible
           if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
           if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
           const uint32_t span = uint32_t(max(hi - lo, 0));
           uint32_t v[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
-          tmem_wait_ld();
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
-          }
           // (a product of scales that underflows would make -inf * 0 of a masked score)
           auto factor = [&](float a) { return fmaxf(a * rf, 1.1754944e-38f); };
           float mx = -INFINITY;
+          tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
+            if ((b & 3) == 0) {
+              tmem_wait_ld();
+              if (b == 0) {  // the other half on its way
+                tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
+                tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
+              }
+              if (edge) {
+#pragma unroll
+                for (int c = 16 * b; c < 16 * b + 64; ++c)
+                  if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+              }
+            }
             const uint32_t* z = &v[16 * b];
             float ma = fmax3(u2f(z[0]), u2f(z[1]), u2f(z[2])), mb = fmax3(u2f(z[3]), u2f(z[4]), u2f(z[5]));
 #pragma unroll
@@ -493,7 +470,7 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
               mb = fmax3(mb, u2f(z[c + 2]), u2f(z[c + 3]));
             }
             ma = fmaxf(fmax3(ma, u2f(z[14]), u2f(z[15])), mb);
-            const float4 t = sc[b];
+            const float4 t = scales_of(sc, b);
             mx = fmaxf(mx, fmaf(ma, factor(t.x), t.y));
           }
           // A maximum that passes the one held by more than kTau is rare after an item's
@@ -508,11 +485,12 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
             if (j > 0) codes_rescale<D>(t_o, alpha);  // S is there, so the product before it is done
           }
           const float base = kShift - m_run;
+          const uint32_t sc2 = scales_at(ctl.codes.sc[ring]);  // (read again: no registers to keep them in)
           if (row == 0) trace_stamp(p.trace, step + j, 5 + 3 * s);
           uint32_t pk[16];
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
-            const float4 t = sc[b];
+            const float4 t = scales_of(sc2, b);
             const float f = factor(t.x), x = t.y + base;
             const uint64_t f2 = pack2(f, f), x2 = pack2(x, x);
             uint64_t acc0 = 0, acc1 = 0;
@@ -532,17 +510,21 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
             float la, lb;
             unpack2(fadd2(acc0, acc1), la, lb);
             l_run = fmaf(la + lb, t.z, l_run);
-            if (b & 1) tmem_st16(t_s + (b >> 1) * 16, pk);
-            if ((b & 3) == 3) {  // 64 keys' P' are there: their product may begin
+            if (b == 5) {  // the first 64 keys' P' are there: their product may begin
               tmem_wait_st();
               tc_fence_before();
               __syncwarp();
               if (lane == 0) {
-                mbar_arrive(b == 3 ? &ctl.p_full[s] : &ctl.alpha_full[s]);
-                if (b == 3 && j > 0) mbar_arrive(&ctl.p_full[s]);  // for O
+                mbar_arrive(&ctl.p_full[s]);
+                if (j > 0) mbar_arrive(&ctl.p_full[s]);  // for O
               }
             }
+            if (b & 1) tmem_st16(t_s + (b >> 1) * 16, pk);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.alpha_full[s]);
           if (row == 0) trace_stamp(p.trace, step + j, 6 + 3 * s);
         } else if (lane == 0) {
           mbar_arrive(&ctl.p_full[s]);
@@ -596,40 +578,45 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
       tc_fence_after();
     }
     if (mine) {
+      // 16 columns of each row at a time go through a staging buffer, so that a store
+      // writes 8 rows' whole sectors and not 32 rows' halves. Loops that are not
+      // unrolled: code that runs once per item is slow to fetch (32 columns at a time,
+      // unrolled: 4 us an item).
       const bool valid = row < w->rows[s];
       const int token = w->q0 + s * p.tok + row_tok, head = w->kvh * p.group + row_head;
       const size_t at = size_t(2 * int(blockIdx.x) + ((w->flags & kCont) ? 0 : 1)) * 256 + s * 128 + row;
+      const int dst_row = !valid ? -1 : part ? int(at) : token * p.Hq + head;  // (below 2^31 both)
+      const int turn = (lane >> 1) & 3;  // neighbouring rows' pieces in other banks
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t x[32];
-        tmem_ld32(t_o + c, x);
+      for (int c = 0; c < D; c += 16) {
+        uint32_t x[16];
+        tmem_ld16(t_o + c, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = n > 0 ? f2u(u2f(x[e]) * f0) : 0u;
+        for (int e = 0; e < 16; ++e) x[e] = n > 0 ? f2u(u2f(x[e]) * f0) : 0u;
         if (nj > 0) {
+          uint32_t y[16];
+          tmem_ld16(t_o + D + c, y);
+          tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 32; h += 16) {
-            uint32_t y[16];
-            tmem_ld16(t_o + D + c + h, y);
-            tmem_wait_ld();
+          for (int e = 0; e < 16; ++e) x[e] = f2u(fmaf(u2f(y[e]), f1, u2f(x[e])));
+        }
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[h + e] = f2u(fmaf(u2f(y[e]), f1, u2f(x[h + e])));
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(stg + lane * 64 + ((e ^ turn) << 4)) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        __syncwarp();
+#pragma unroll 1
+        for (int rr = lane >> 2; rr < 32; rr += 8) {
+          const int to = __shfl_sync(0xffffffffu, dst_row, rr);
+          const float4 y = *reinterpret_cast<const float4*>(stg + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+          const size_t to_at = size_t(max(to, 0)) * D + c + (lane & 3) * 4;
+          if (to >= 0 && part) {
+            *reinterpret_cast<float4*>(p.part_o + to_at) = y;
+          } else if (to >= 0) {
+            *reinterpret_cast<uint2*>(p.o + to_at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
           }
         }
-        if (!valid) continue;
-        if (part) {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.o + (size_t(token) * p.Hq + head) * D + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t* z = &x[8 * e];
-            dst[e] = make_uint4(pack_bf16x2(u2f(z[0]), u2f(z[1])), pack_bf16x2(u2f(z[2]), u2f(z[3])),
-                                pack_bf16x2(u2f(z[4]), u2f(z[5])), pack_bf16x2(u2f(z[6]), u2f(z[7])));
-          }
-        }
+        __syncwarp();  // (the next read of tensor memory is one of the whole warp)
       }
       if (valid) {
         if (part) {
@@ -676,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.it_empty[i], 15);  // every warp but this one's
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl.q_full[s], CODES ? 4 : 1);
+      mbar_init(&ctl.q_full[s], 1);
       mbar_init(&ctl.q_empty[s], 1);
       mbar_init(&ctl.s_full[s], 1);
       mbar_init(&ctl.p_full[s], 8);
@@ -687,12 +674,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&ctl.drain, 1);
     for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&ctl.kv_full[i], CODES ? 4 : 1);
+      mbar_init(&ctl.kv_full[i], 1);
       mbar_init(&ctl.kv_empty[i], 1);
-      mbar_init(&ctl.tail_done[i], 1);
+      mbar_init(&ctl.tail_done[i], CODES ? 4 : 1);
     }
     if constexpr (CODES) {
-      for (int i = 0; i < C::kSlots; ++i) mbar_init(&ctl.codes.raw_full[i], 1);
       for (int i = 0; i < kScaleTiles; ++i) mbar_init(&ctl.codes.sc_full[i], 4);
     }
     fence_mbar_init();
@@ -719,10 +705,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (CODES) {
       if (wg <= 1) {
         setmaxnreg_inc<168>();
-        codes_softmax<D>(p, ctl, tmem, wg, warp & 3, lane, LIM);
+        codes_softmax<D>(p, ctl, tmem, sStg + warp * 2048, wg, warp & 3, lane, LIM);
       } else {
         setmaxnreg_dec<104>();
-        codes_convert<D>(p, ctl, sQ, sKV, warp & 3, lane, LIM);
+        codes_convert<D>(p, ctl, sKV, warp & 3, lane, LIM);
       }
     }
   } else if (wg <= 1) {
@@ -1082,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Place next = place(0);
       // Q: key mode takes the two buffers in turn, else stage s takes buffer s
-      for (int s = 0; s < 2 && ok && !is_v && !CODES; ++s) {
+      for (int s = 0; s < 2 && ok && !is_v; ++s) {
         if (w->n[s] == 0 || (key && s == 1)) continue;
         const uint32_t b = key ? (key_items++ & 1) : uint32_t(s);
         ok = warp_wait(&ctl.q_empty[b], (b == 0 ? q_uses[0] : q_uses[1]) & 1 ? 0 : 1, abort_flag, LIM);
@@ -1094,6 +1080,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) {
           mbar_arrive_expect_tx(&ctl.q_full[b], q_bytes);
+          if (CODES) {  // its high and its low parts
+            for (int c = 0; c < 2; ++c)
+              tma_load_4d_hint(sQ + b * C::kTileBytes + c * (C::kTileBytes / 2), &tmQ, &ctl.q_full[b], 0, 0,
+                               c * p.total_q + w->q0 + (key ? 0 : s * p.tok), kvh, pol_q);
+          } else
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
             tma_load_4d_hint(sQ + b * C::kTileBytes + c * 16384, &tmQ, &ctl.q_full[b], c * 64, 0,
@@ -1136,17 +1127,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             in_page[x] = __shfl_sync(0xffffffffu, at.in_page, x);
           }
           if (CODES) {
-            if constexpr (CODES)
-              if (elect_one()) {
-                mbar_arrive_expect_tx(&ctl.codes.raw_full[slot], uint32_t(at.boxes * p.box_rows * D));
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(at.boxes * p.box_rows * D));
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                  if (x >= at.boxes) break;
-                  const int r = x * p.box_rows;  // 32 rows of codes stand where 32 rows of 64 values will
-                  tma_load_4d_hint(dst + (r >> 5) * 4096 + (r & 31) * D, m, &ctl.codes.raw_full[slot], 0, kvh, in_page[x],
-                                   page[x], pol_kv);
-                }
+              for (int x = 0; x < 8; ++x) {
+                if (x >= at.boxes) break;
+                // K's rows of codes follow one another, 32 of V's stand where those of 64 values will
+                const int r = x * p.box_rows;
+                tma_load_4d_hint(dst + (is_v ? (r >> 5) * 4096 + (r & 31) * D : r * D), m, &ctl.kv_full[slot], 0, kvh,
+                                 in_page[x], page[x], pol_kv);
               }
+            }
           } else if (elect_one()) {
             mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(at.boxes * p.box_rows * D * 2));
 #pragma unroll
@@ -1190,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // producer's and all waits, 1.78 -> 1.29 ms on one causal sequence of 16384
     // tokens, against one lane walking: MMA operands are uniform registers).
     {
-      const uint32_t idS = (CODES ? idesc_f16_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0)) | (p.neg_s << 13);
+      const uint32_t idS = (CODES ? idesc_codes_f32(128, 128) : idesc_bf16_f32(128, 128, 0, 0)) | (p.neg_s << 13);
       constexpr uint32_t idPV = CODES ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
       const uint32_t dq = sdesc_lo(smem_u32(sQ), 16), dk = sdesc_lo(smem_u32(sKV), 16),
                      dv = sdesc_lo(smem_u32(sKV), 16384);
@@ -1253,10 +1244,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (!elect_one()) return;
         const uint32_t q0 = sdesc_step(dq, b * C::kTileBytes), b0 = sdesc_step(dk, slot * C::kTileBytes);
+        if constexpr (CODES) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t ko = (kk >> 2) * 16384 + (kk & 3) * 32;
-          mma_ss_lo(tmem + uint32_t(s * 128), sdesc_step(q0, ko), sdesc_step(b0, ko), idS, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {  // 32 of d at a time, Q's high and then its low parts
+            const uint32_t ko = kk % (D / 32) * 32;
+            mma_codes_lo<D == 128 ? kSdescHi : kSdescHi64>(tmem + uint32_t(s * 128), sdesc_step(q0, kk / (D / 32) * (C::kTileBytes / 2) + ko),
+                                                        sdesc_step(b0, ko), idS, kk > 0);
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ko = (kk >> 2) * 16384 + (kk & 3) * 32;
+            mma_ss_lo(tmem + uint32_t(s * 128), sdesc_step(q0, ko), sdesc_step(b0, ko), idS, kk > 0);
+          }
         }
         mma_commit(&ctl.s_full[s]);
       };
@@ -1272,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Work* const w = item(i);
         if (w == nullptr) break;
         const int nt = w->nt;
-        const bool fill = !CODES && w->fill != 0;
+        const bool fill = w->fill != 0;
         if (nt > 0 && (w->flags & kKeyMode)) {
           const uint32_t b = key_items++ & 1;
           ok = wait_phase(&ctl.q_full[b], kPhQ + int(b));
@@ -1280,7 +1280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int s = t & 1;
             uint32_t slot;
             if (t >= 0) {
-              ok = wait_kv(slot) && (!fill || t < nt - 1 || wait_tail(slot)) && wait_phase(&ctl.p_full[s], kPhP + s);
+              ok = wait_kv(slot) && ((!CODES && (!fill || t < nt - 1)) || wait_tail(slot)) && wait_phase(&ctl.p_full[s], kPhP + s);
               if (!ok) break;
               if (s == 0) trace(p.trace, step0 + (t >> 1), 0);
               issue_pv(s, slot, t > 1);
@@ -1306,7 +1306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t u0 = uint32_t(t - a0), u1 = uint32_t(t - a1);
             uint32_t vs = 0, ks = 0;
             if (v) {
-              ok = wait_kv(vs) && (!fill || k || wait_tail(vs));
+              ok = wait_kv(vs) && ((!CODES && (!fill || k)) || wait_tail(vs));
               if (!ok) break;
               trace(p.trace, step0 + t, 0);
               if (u0 < uint32_t(n0)) {
@@ -1369,11 +1369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Its Q and its first K and V tile into L2, a lane to each box: the
         // loads wait for buffers that items before still use, and would then
         // wait for device memory too.
-        const int c = lane % C::kChunks * 64, what = lane / C::kChunks;
+        constexpr int kParts = CODES ? 2 : C::kChunks;
+        const int c = CODES ? 0 : lane % kParts * 64, what = lane / kParts, t0 = CODES ? lane % kParts * p.total_q : 0;
         if (x.nt > 0) {
           if (what < 2) {
             if ((what == 0 ? x.n[0] : x.n[1]) > 0 && !(what == 1 && (x.flags & kKeyMode)))
-              tma_prefetch_l2_4d(&tmQ, c, 0, x.q0 + what * p.tok, x.kvh);
+              tma_prefetch_l2_4d(&tmQ, c, 0, t0 + x.q0 + what * p.tok, x.kvh);
           } else if (!PAGED && what < 4) {
             tma_prefetch_l2_4d(what == 2 ? &tmK : &tmV, c, x.kvh, x.kbase + x.kt * 128, 0);
           }
@@ -1604,6 +1605,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32) seq_join_kernel(const Params 
   }
 }
 
+// Codes: Q's rows, divided by a power of two, as sums of two e4m3 values (see Codes),
+// high parts [total_q, Hq, D] and then the low ones, and what each row was divided by.
+// A pass of its own, over as many bytes as Q has twice: done by the warps of the main
+// kernel that wait for it, it took 15 us of each item of two row tiles.
+template <int D>
+__global__ void __launch_bounds__(256) codes_q_kernel(const __nv_bfloat16* q, long long q_stride, int rows, int Hq,
+                                                      uint8_t* hi_out, uint8_t* lo_out, float* factor) {
+  constexpr int kLanes = D / 8, kAtOnce = 256 / kLanes, kBatch = 4;
+  grid_dep_launch();
+  const int col = threadIdx.x % kLanes, r0 = blockIdx.x * (kAtOnce * kBatch) + threadIdx.x / kLanes;
+  uint4 x[kBatch];
+#pragma unroll
+  for (int e = 0; e < kBatch; ++e) {
+    const int r = r0 + e * kAtOnce, tok = r / Hq;
+    x[e] = make_uint4(0, 0, 0, 0);
+    if (r < rows) x[e] = __ldg(reinterpret_cast<const uint4*>(q + tok * q_stride + 1LL * (r - tok * Hq) * D + col * 8));
+  }
+#pragma unroll
+  for (int e = 0; e < kBatch; ++e) {
+    const int r = r0 + e * kAtOnce;
+    uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
+                          __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
+    m = max(m & 0xffffu, m >> 16);
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (r >= rows) continue;
+    // the row's largest value into [2^7, 2^8); a row that is not finite becomes NaN
+    const int ex = max(int(m >> 7) - 127, -100) - 7;
+    const float f = m < 0x7f80u ? exp2i(-ex) : __int_as_float(0x7fffffff);
+    const uint32_t y[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = u2f(y[k] << 16) * f, c = u2f(y[k] & 0xffff0000u) * f;
+      const uint32_t h = e4m3x2_of(a, c), back = f16x2_of_e4m3x2(uint16_t(h));
+      const uint32_t l = e4m3x2_of(a - f16_lo(back), c - f16_hi(back));
+      hi[k >> 1] |= h << (16 * (k & 1));
+      lo[k >> 1] |= l << (16 * (k & 1));
+    }
+    *reinterpret_cast<uint2*>(hi_out + size_t(r) * D + col * 8) = make_uint2(hi[0], hi[1]);
+    *reinterpret_cast<uint2*>(lo_out + size_t(r) * D + col * 8) = make_uint2(lo[0], lo[1]);
+    if (col == 0) factor[r] = exp2i(ex);
+  }
+}
+
 // --------------------------------------------------------------------------
 // launch
 // --------------------------------------------------------------------------
@@ -1612,14 +1658,20 @@ struct Space {
   Plan<FwdItem> plan;
   float* part_o;
   float2* part_ml;
+  uint8_t* q_parts;  // codes: Q's high and low parts
+  float* q_factor;
   size_t bytes;
 };
-Space carve(uint8_t* base, const SeqProblem& pb, int G, long long units) {
+Space carve(uint8_t* base, const SeqProblem& pb, int G, long long units, bool codes) {
   Space s{};
   Carver c{base, 0};
   s.plan = carve_plan<FwdItem>(c, pb.B, units, pb.Hkv, G);
   s.part_ml = c.take<float2>(size_t(2) * G * 256);
   s.part_o = c.take<float>(size_t(2) * G * 256 * pb.d);
+  if (codes) {
+    s.q_parts = c.take<uint8_t>(size_t(2) * pb.total_q * pb.Hq * pb.d);
+    s.q_factor = c.take<float>(size_t(pb.total_q) * pb.Hq);
+  }
   s.bytes = c.at;
   return s;
 }
@@ -1633,8 +1685,8 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
   const int group = pb.Hq / pb.Hkv, tok = 128 / group;
   Params p{};
   // q: rows (token, head of the group), `tok` tokens to a tile
-  CUtensorMap mq, mk, mv;
-  {
+  CUtensorMap mq{}, mk, mv;
+  if constexpr (KIND != kCodes) {
     const uint64_t dims[4] = {uint64_t(D), uint64_t(group), uint64_t(pb.total_q), uint64_t(pb.Hkv)};
     const uint64_t strides[3] = {uint64_t(D) * 2, uint64_t(pb.q_stride) * 2, uint64_t(group) * D * 2};
     const uint32_t box[4] = {64, uint32_t(group), uint32_t(tok), 1};
@@ -1643,7 +1695,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
   }
   // o: the 32 rows of a warp, where they are whole tokens
   CUtensorMap mo = mq;
-  if (32 % group == 0) {
+  if (KIND != kCodes && 32 % group == 0) {
     p.o_box = 32 / group;
     const uint64_t dims[4] = {uint64_t(D), uint64_t(group), uint64_t(pb.total_q), uint64_t(pb.Hkv)};
     const uint64_t strides[3] = {uint64_t(D) * 2, uint64_t(pb.Hq) * D * 2, uint64_t(group) * D * 2};
@@ -1663,11 +1715,9 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
       const uint64_t strides[3] = {uint64_t(D), row, row * pb.page_size};
       const uint32_t box[4] = {uint32_t(D), 1, uint32_t(p.box_rows), 1};
       if (!encode_tiled(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, kp[i], dims, strides, box,
-                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE))
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : i == 0 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     }
-    p.q = static_cast<const __nv_bfloat16*>(pb.q);
-    p.q_stride = pb.q_stride;
     p.scales[0] = sc->k;
     p.scales[1] = sc->v;
   } else if constexpr (PAGED) {
@@ -1705,14 +1755,32 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
   long long keys = pb.page_table != nullptr ? 1LL * pb.max_pages * pb.page_size : pb.total_k;
   if (pb.window_left >= 0 && pb.window_right >= 0)  // and whole tiles around those that a unit sees
     keys = std::min(keys, 2LL * tok + pb.window_left + pb.window_right + 254);
-  const bool whole = few && units * pb.Hkv <= G && (keys + 127) / 128 + kItemCost <= FwdSide::kPartsCost;
+  const bool whole = KIND != kCodes && few && units * pb.Hkv <= G && (keys + 127) / 128 + kItemCost <= FwdSide::kPartsCost;
   void* ws = nullptr;
   Space sp{};
   if (!whole) {
     cudaMemPool_t pool = workspace_pool();
-    if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr, pb, G, units).bytes, pool, stream) != cudaSuccess)
+    if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr, pb, G, units, KIND == kCodes).bytes, pool, stream) != cudaSuccess)
       return cudaErrorMemoryAllocation;
-    sp = carve(static_cast<uint8_t*>(ws), pb, G, units);
+    sp = carve(static_cast<uint8_t*>(ws), pb, G, units, KIND == kCodes);
+  }
+  if constexpr (KIND == kCodes) {
+    const uint64_t row = uint64_t(pb.Hq) * D;
+    const uint64_t dims[4] = {uint64_t(D), uint64_t(group), 2 * uint64_t(pb.total_q), uint64_t(pb.Hkv)};
+    const uint64_t strides[3] = {uint64_t(D), row, uint64_t(group) * D};
+    const uint32_t box[4] = {uint32_t(D), uint32_t(group), uint32_t(tok), 1};
+    if (!encode_tiled(&mq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, sp.q_parts, dims, strides, box,
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) {
+      cudaFreeAsync(ws, stream);
+      return cudaErrorInvalidValue;
+    }
+    mo = mq;  // (not used)
+    p.q_factor = sp.q_factor;
+    const int rows = pb.total_q * pb.Hq, per_block = 256 / (D / 8) * 4;
+    codes_q_kernel<D><<<unsigned((rows + per_block - 1LL) / per_block), 256, 0, stream>>>(
+        static_cast<const __nv_bfloat16*>(pb.q), pb.q_stride, rows, pb.Hq, sp.q_parts, sp.q_parts + size_t(pb.total_q) * row,
+        sp.q_factor);
+    e = cudaGetLastError();
   }
   PlanArgs<FwdSide> a{};
   a.L = Lens{pb.cu_q, pb.cu_k, pb.lens_k, pb.B, pb.total_q, pb.total_k, 1LL * pb.max_pages * pb.page_size};
@@ -1750,7 +1818,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
   p.wait_limit_ns = dc.wait_limit_ns;
   p.inject = dc.inject;
   p.trace = dc.trace;
-  if (!few) {
+  if (!few && e == cudaSuccess) {
     plan_kernel<FwdSide><<<1, kPlanThreads, 0, stream>>>(a);
     e = cudaGetLastError();
   }
@@ -1764,7 +1832,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
   lc.dynamicSmemBytes = C::kSmemDyn;
   lc.stream = stream;
   lc.attrs = pdl;
-  lc.numAttrs = few ? 0 : 1;
+  lc.numAttrs = few && KIND != kCodes ? 0 : 1;
   if (dc.ev_begin) cudaEventRecord(dc.ev_begin, stream);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&lc, kern, mq, mk, mv, mo, p);
   if (dc.ev_end) cudaEventRecord(dc.ev_end, stream);

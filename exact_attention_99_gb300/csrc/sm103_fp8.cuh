@@ -3,10 +3,36 @@
 #include <cstdint>
 
 #include "sm103_math.cuh"
+#include "sm103_ptx.cuh"
 
 namespace fa {
 
 constexpr int kFp8Block = 16;  // tokens of a block that has a scale (for each head)
+
+// Instruction descriptors: kind::f16 with f16 A and B (bf16's without the format
+// bits), kind::f8f6f4 with e4m3 A and B, both K-major (format 0 too).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t a_mn_major, uint32_t b_mn_major) {
+  return (1u << 4) | (a_mn_major << 15) | (b_mn_major << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_codes_f32(uint32_t M, uint32_t N) { return idesc_f16_f32(M, N, 0, 0); }
+
+// The high descriptor word of rows of 64 bytes with the 64-byte swizzle (layout type
+// 4): 512 bytes from one 8-row group to the next.
+constexpr uint32_t kSdescHi64 = (512u >> 4) | (1u << 14) | (4u << 29);
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3, 32 per K step, descriptors by their low words
+template <uint32_t HI>
+__device__ __forceinline__ void mma_codes_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %5};\n\t"
+      "mov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
+      : "memory");
+}
 
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }

@@ -149,6 +149,29 @@ def test_nan_stays_in_its_rows(fa):
     assert bad[39] and not bad[:39].any() and not bad[40:].any()
 
 
+@pytest.mark.parametrize("new", [3, 60])
+def test_queries_that_are_not_finite(fa, new):
+    c = cu8.filled([300], 1, 64, 16, seed=25)
+    pages, table = c.cuda()
+    q = su.normal((new, 2, 64), su.gen(25))
+    q[0, 0, 3] = math.inf
+    q[1, 1, 0] = math.nan
+    o, _ = fa.forward_paged_fp8(q.cuda(), *pages, su.starts([new]).cuda(), c.lens_k().cuda(), table)
+    bad = o.float().isnan().any(2).cpu()
+    assert bad[0, 0] and bad[1, 1] and bad.sum() == 2
+
+
+@pytest.mark.parametrize("new", [2, 90])
+def test_queries_with_an_outlier(fa, new):
+    # One channel of 30: scores up to 30 * 4 * scale 0.02 and the rounding of q in
+    # two e4m3 parts: 2^-17 of 30 in each channel, times sum |k| < 120 and 0.02: 2^-11
+    # at worst, all of one sign; of random signs (120 -> 11) it is 2^-14.6, within what
+    # the bounds have for the scores.
+    def q_edit(w):
+        w[:, :, 5] = 30.0
+    run(fa, [new], [400], 4, 2, 128, 16, seed=26, scale=0.02, q_edit=q_edit)
+
+
 def test_rows_outside_the_sequences(fa):
     c = cu8.filled([300, 64], 2, 64, 16, seed=21)
     pages, table = c.cuda()
