@@ -446,22 +446,16 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
           // (a product of scales that underflows would make -inf * 0 of a masked score)
           auto factor = [&](float a) { return fmaxf(a * rf, 1.1754944e-38f); };
           float mx = -INFINITY;
-          tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-          tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
+          tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
+          }
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
-            if ((b & 3) == 0) {
-              tmem_wait_ld();
-              if (b == 0) {  // the other half on its way
-                tmem_ld32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
-                tmem_ld32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
-              }
-              if (edge) {
-#pragma unroll
-                for (int c = 16 * b; c < 16 * b + 64; ++c)
-                  if (uint32_t(c - lo) >= span) v[c] = f2u(-INFINITY);
-              }
-            }
             const uint32_t* z = &v[16 * b];
             float ma = fmax3(u2f(z[0]), u2f(z[1]), u2f(z[2])), mb = fmax3(u2f(z[3]), u2f(z[4]), u2f(z[5]));
 #pragma unroll
@@ -586,7 +580,15 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
       const int token = w->q0 + s * p.tok + row_tok, head = w->kvh * p.group + row_head;
       const size_t at = size_t(2 * int(blockIdx.x) + ((w->flags & kCont) ? 0 : 1)) * 256 + s * 128 + row;
       const int dst_row = !valid ? -1 : part ? int(at) : token * p.Hq + head;  // (below 2^31 both)
-      const int turn = (lane >> 1) & 3;  // neighbouring rows' pieces in other banks
+      const int turn = (lane >> 1) & 3, quarter = lane & 3;  // neighbouring rows' pieces in other banks
+      uint8_t* dst[4];  // of this lane's quarter of rows 8 e + lane / 4
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int to = __shfl_sync(0xffffffffu, dst_row, 8 * e + (lane >> 2));
+        dst[e] = to < 0 ? nullptr
+                        : (part ? reinterpret_cast<uint8_t*>(p.part_o + size_t(to) * D + 4 * quarter)
+                                : reinterpret_cast<uint8_t*>(p.o + size_t(to) * D + 4 * quarter));
+      }
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t x[16];
@@ -605,15 +607,15 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
         for (int e = 0; e < 4; ++e)
           *reinterpret_cast<uint4*>(stg + lane * 64 + ((e ^ turn) << 4)) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         __syncwarp();
-#pragma unroll 1
-        for (int rr = lane >> 2; rr < 32; rr += 8) {
-          const int to = __shfl_sync(0xffffffffu, dst_row, rr);
-          const float4 y = *reinterpret_cast<const float4*>(stg + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-          const size_t to_at = size_t(max(to, 0)) * D + c + (lane & 3) * 4;
-          if (to >= 0 && part) {
-            *reinterpret_cast<float4*>(p.part_o + to_at) = y;
-          } else if (to >= 0) {
-            *reinterpret_cast<uint2*>(p.o + to_at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int rr = 8 * e + (lane >> 2);
+          const float4 y = *reinterpret_cast<const float4*>(stg + rr * 64 + ((quarter ^ ((rr >> 1) & 3)) << 4));
+          if (part) {
+            if (dst[e] != nullptr) *reinterpret_cast<float4*>(dst[e] + c * 4) = y;
+          } else {
+            if (dst[e] != nullptr)
+              *reinterpret_cast<uint2*>(dst[e] + c * 2) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
           }
         }
         __syncwarp();  // (the next read of tensor memory is one of the whole warp)
