@@ -570,6 +570,7 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
         ph_of ^= 2;
       }
       tc_fence_after();
+      if (row == 0) trace_stamp(p.trace, step0 - 1, 10 + s);
     }
     if (mine) {
       // 16 columns of each row at a time go through a staging buffer, so that a store

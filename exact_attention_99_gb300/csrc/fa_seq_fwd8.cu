@@ -13,22 +13,20 @@
 // unless a value is below 2^-28 of the row's largest), P' to f16 (off by at most
 // 2^-12 of itself, for all P' above 2^-21 of the largest), O to bf16.
 //
-// Few rows to a kv head (single tokens): bound by the cache's bytes. A warp
-// takes a block of 16 keys at a time. Its codes come by asynchronous copies into
-// the very lanes that use them (16 bytes a lane, a ring of stages per warp), are
-// turned to f16 in registers and are the A operand of mma.sync.m16n8k16, the
-// rows the B operand of 8 columns: S^T = K Q^T, then O^T = V^T P^T. Shared memory
-// carries each byte once in and once out, and no warp waits for another before
-// the end of a unit. (The tensor-memory pipeline of fa_seq_fwd.cu would carry
-// each code through shared memory six times - in as codes, out, back in as f16,
-// to the tensor cores - and that sets its pace below device memory's.)
+// Few rows to a kv head (single tokens): bound by the cache's bytes. A producer warp
+// loads tiles of 128 keys by TMA, and each of 8 warps takes 16 of a tile's keys: their
+// codes are turned to f16 in registers and are the A operand of mma.sync.m16n8k16,
+// the rows the B operand of 8 columns: S^T = K Q^T, then O^T = V^T P^T. Shared memory
+// carries each byte in once and out once, and no warp waits for another before the end
+// of a unit. (The tensor-memory pipeline of fa_seq_fwd.cu takes V's codes through
+// shared memory as f16 as well and has a softmax of 128 rows for each tile: at half the
+// bytes a key it would set the pace.)
 //
 // Work: a unit is up to 8 NT rows of a sequence and kv head with the tiles of
 // 128 keys that they see. All tiles of all units are laid end to end and divided
-// evenly between the CTAs (one per SM), each of which finds its own share; a
-// unit's keys go round its 8 warps by blocks, whose results are joined in shared
-// memory, and the parts of a unit that several CTAs share by a last kernel, in a
-// fixed order.
+// evenly between the CTAs, whose producers find their own shares; a unit's warps join
+// their results in shared memory, and the parts of a unit that several CTAs share are
+// joined by a last kernel, in a fixed order.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -48,7 +46,8 @@ namespace seq8 {
 using seq::Lens;
 using seq::Seq;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kWarps = 8, kThreads = (kWarps + 1) * 32;  // warp 8: the producer
+constexpr int kItems = 4;      // ring of units: the producer is up to three tiles ahead, and each unit has one at least
 constexpr int kItemCost = 2;  // of a unit beside its tiles, in tiles
 // P' is at most 2^15 (f16 holds 65504), and 2^7 where the running maximum is up to date
 constexpr float kTop = 15.0f, kShift = 7.0f;
@@ -67,7 +66,6 @@ struct Params8 {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
-  const uint8_t* pages[2];  // k, v
   const float* scales[2];
   const int* table;
   Lens L;
@@ -80,34 +78,51 @@ struct Params8 {
   float2* part_ml;   // [2 G][8 NT]
   Cut8* cuts;        // [G]
   int* has;          // [G] worker has a share
+  int box_rows;      // keys of a TMA box: they lie in one page
+  unsigned long long wait_limit_ns;
+  int inject;
   unsigned* status;
 };
 
 template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kHalf = 16 * D;             // bytes of a block's K, or V
-  static constexpr int kStages = NT == 4 && D == 128 ? 2 : 4;
-  static constexpr int kRing = kWarps * kStages * 2 * kHalf;
+  // CTAs of an SM: one's units begin and end while the other's keys come in
+  static constexpr int kPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kHalf = 128 * D;            // bytes of a tile's K, or V
+  static constexpr int kStages = D == 64 || NT == 2 ? 4 : 2;
+  static constexpr int kRing = kStages * 2 * kHalf;
   static constexpr int kJoinLd = D + 4;            // (spreads the rows over the banks)
   static constexpr int kJoin = kWarps * kRows * kJoinLd * 4;
-  static constexpr int kSmem = kRing + kJoin;
+  static constexpr int kSmem = kRing + kJoin + 1024;
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+// A unit, or this CTA's part of it.
+struct Item8 {
+  int q0, qlen, klen;   // the sequence
+  int row0, rows;       // the unit's rows of it (token * group + head of the group)
+  int head;             // kv head; -1: there are no more items
+  int k0, k1;           // keys [k0, k1)
+  int slot;             // of a part's results; -1: it is the whole unit
+};
+
+template <int D, int NT>
+struct Ctl8 {
+  Item8 it[kItems];
+  uint64_t it_full[kItems], it_empty[kItems];
+  uint64_t full[Shape<D, NT>::kStages], empty[Shape<D, NT>::kStages];
+  uint64_t join_full, join_empty;
+  float sc[Shape<D, NT>::kStages][2][8];  // scales of a tile's blocks of K, V
+  float2 ml[kWarps][8 * NT];
+  long long sums[kWarps + 1];
+  struct {
+    int b;
+    long long before, of_seq;  // costs of the sequences before it, its own for one head
+    int bad;
+  } start;
+  uint32_t abort;
+};
+
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -202,22 +217,36 @@ struct Walk8 {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Params8 p) {
+__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
+    attend8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params8 p) {
   using C = Shape<D, NT>;
   constexpr int R = C::kRows, S = C::kStages;
   constexpr int KS = D / 16;  // products' steps over d, tiles of 16 d of O^T
-  extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float sc[kWarps][S][2];
-  __shared__ float2 ml[kWarps][R];
-  __shared__ long long sums[kWarps];
-  __shared__ struct {
-    int b;
-    long long before, of_seq;  // costs of the sequences before it, its own for one head
-    int bad;
-  } start;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Ctl8<D, NT> ctl;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* const join = reinterpret_cast<float*>(ring + C::kRing);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int G = gridDim.x, me = blockIdx.x;
+  const uint64_t LIM = p.wait_limit_ns;
   grid_dep_launch();
+  if (tid == 0) {
+    ctl.abort = 0;
+    ctl.start.b = p.L.B;
+    ctl.start.bad = 0;
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&ctl.it_full[i], 1);
+      mbar_init(&ctl.it_empty[i], kWarps);
+    }
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&ctl.full[i], 2);  // the codes and the scales
+      mbar_init(&ctl.empty[i], kWarps);
+    }
+    mbar_init(&ctl.join_full, kWarps);
+    mbar_init(&ctl.join_empty, kWarps);
+    fence_mbar_init();
+  }
+  __syncthreads();
 
   // ---- this worker's share: every thread takes some sequences, in order
   const int per = (p.L.B + kThreads - 1) / kThreads;
@@ -230,31 +259,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Params8 p) {
       for (int r = 0; r < s.qlen * p.group; r += R) t += unit_at(p, s, r, min(R, s.qlen * p.group - r)).nt + kItemCost;
     return t;
   };
-  if (tid == 0) {
-    start.b = p.L.B;
-    start.bad = 0;
-  }
-  __syncthreads();
-  bool ok = true;
+  bool fine = true;
   long long mine = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += cost_of(b, ok);
-  if (!ok) start.bad = 1;
+  for (int b = b0; b < b1; ++b) mine += cost_of(b, fine);
+  if (!fine) ctl.start.bad = 1;
   long long upto = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
     const long long o = __shfl_up_sync(0xffffffffu, upto, m);
     if (lane >= m) upto += o;
   }
-  if (lane == 31) sums[warp] = upto;
+  if (lane == 31) ctl.sums[warp] = upto;
   __syncthreads();
   long long T = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) upto += sums[w];
-    T += sums[w];
+  for (int w = 0; w <= kWarps; ++w) {
+    if (w < warp) upto += ctl.sums[w];
+    T += ctl.sums[w];
   }
-  if (start.bad) {  // lengths that the tensors cannot hold: nothing is computed
+  if (ctl.start.bad) {  // lengths that the tensors cannot hold: nothing is computed
     if (tid == 0) {
       p.cuts[me].c1 = -1;
       p.has[me] = 0;
@@ -263,17 +287,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Params8 p) {
     return;
   }
   const long long all = T * p.Hkv, lo = all * me / G, hi = all * (me + 1) / G;
+  // (a unit without keys lies at the end of its cost: lo - 1 is in it, or before it)
+  const long long target = lo > 0 ? lo - 1 : 0;
   {
-    // (a unit without keys lies at the end of its cost: lo - 1 is in it, or before it)
-    const long long target = lo > 0 ? lo - 1 : 0;
     long long before = (upto - mine) * p.Hkv;
     if (before <= target && target < upto * p.Hkv) {
+#pragma unroll 1
       for (int b = b0; b < b1; ++b) {
-        const long long t = cost_of(b, ok);
+        const long long t = cost_of(b, fine);
         if (target < before + t * p.Hkv) {
-          start.b = b;
-          start.before = before;
-          start.of_seq = t;
+          ctl.start.b = b;
+          ctl.start.before = before;
+          ctl.start.of_seq = t;
           break;
         }
         before += t * p.Hkv;
@@ -281,337 +306,405 @@ __global__ void __launch_bounds__(kThreads, 1) attend8_kernel(const Params8 p) {
     }
   }
   __syncthreads();
-  Walk8<R> fetch;
-  fetch.b = start.b;
-  fetch.kvh = 0;
-  fetch.j = 0;
-  fetch.x = 0;
-  fetch.load(p);
-  if (fetch.b < p.L.B) {
-    fetch.kvh = int(((lo > 0 ? lo - 1 : 0) - start.before) / start.of_seq);
-    fetch.x = start.before + fetch.kvh * start.of_seq;
-  }
-  Walk8<R> work = fetch;
-  const bool end = me == G - 1;
 
-  // ---- fetching: blocks of 16 keys, this warp's of each unit in turn
-  uint8_t* const ring = smem + warp * (S * 2 * C::kHalf);
-  const uint32_t ring_at = smem_u32(ring), sc_at = smem_u32(&sc[warp][0][0]);
-  int f_blk = 0, f_end = 0, f_page = 0, f_row = 0;  // the block to fetch next, its page, its first row there
-  bool f_more = true;
-  auto look_up = [&] {  // the page of the block to fetch next
-    while (f_more && f_blk >= f_end) {
-      f_more = fetch.next(p, lo, hi, end);
-      if (f_more) {
-        f_blk = (fetch.k0 >> 4) + warp;
-        f_end = (fetch.k1 + 15) >> 4;
-      }
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    Walk8<R> walk;
+    walk.b = ctl.start.b;
+    walk.kvh = 0;
+    walk.j = 0;
+    walk.x = 0;
+    walk.load(p);
+    if (walk.b < p.L.B) {
+      walk.kvh = int((target - ctl.start.before) / ctl.start.of_seq);
+      walk.x = ctl.start.before + walk.kvh * ctl.start.of_seq;
     }
-    if (f_more) {
-      const int k = f_blk << 4, pg = k / p.page_size;
-      f_row = k - pg * p.page_size;
-      f_page = p.table[size_t(fetch.b_of) * p.max_pages + pg];
-    }
-  };
-  auto issue = [&](int stage) {
-    if (f_more) {
-      int page = f_page;
-      const bool there = page >= 0 && page < p.num_pages;
-      const uint32_t dst = ring_at + stage * 2 * C::kHalf + lane * 16;
-      if (there) {
-        const long long row = 1LL * page * p.page_size + f_row;
-        const long long tok = 1LL * p.Hkv * D;  // bytes between keys
-        const long long at = (row * p.Hkv + fetch.head) * D;
-        // K: lane (g, c) has keys g and g + 8, of d the 16 at 16 c and (d = 128) at 64 + 16 c
-        const uint8_t* k = p.pages[0] + at + g * tok + c * 16;
-        // V: keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9, of d the D / 8 at g D / 8
-        const uint8_t* v = p.pages[1] + at + 2 * c * tok + g * (D / 8);
-        if constexpr (D == 128) {
-          cp16(dst, k);
-          cp16(dst + 512, k + 64);
-          cp16(dst + 1024, k + 8 * tok);
-          cp16(dst + 1536, k + 8 * tok + 64);
-          cp16(dst + 2048, v);
-          cp16(dst + 2560, v + tok);
-          cp16(dst + 3072, v + 8 * tok);
-          cp16(dst + 3584, v + 9 * tok);
-        } else {
-          cp16(dst, k);
-          cp16(dst + 512, k + 8 * tok);
-          const uint32_t dv = dst + 1024 - lane * 8;
-          cp8(dv, v);
-          cp8(dv + 256, v + tok);
-          cp8(dv + 512, v + 8 * tok);
-          cp8(dv + 768, v + 9 * tok);
-        }
-        if (lane < 2) cp4(sc_at + (stage * 2 + lane) * 4, p.scales[lane] + (row >> 4) * p.Hkv + fetch.head);
-      } else {  // no such page: it reads as zeros, and the caller is told
-        if (lane == 0) atomicOr(p.status, kDevBadArg);
-#pragma unroll
-        for (int i = 0; i < 2 * C::kHalf / 512; ++i)
-          *reinterpret_cast<uint4*>(ring + stage * 2 * C::kHalf + i * 512 + lane * 16) = make_uint4(0, 0, 0, 0);
-        if (lane < 2) sc[warp][stage][lane] = 1.0f;
-      }
-      f_blk += kWarps;
-      look_up();
-    }
-    cp_commit();
-  };
-  look_up();
-#pragma unroll 1
-  for (int s = 0; s < S; ++s) issue(s);
-
-  // ---- the units
-  float* const join = reinterpret_cast<float*>(smem + C::kRing);
-  int stage = 0;
-  Cut8 cut;
-  cut.c1 = -1;
-  bool any = false;
-  while (work.next(p, lo, hi, end)) {
-    any = true;
-    const Seq s = work.seq;
-    // Q^T: rows 8 n + g, of d the 16 at 16 c and (d = 128) 64 + 16 c, as K's; divided by
-    // a power of two of the row so that its largest value is in [2^14, 2^15)
-    uint32_t qf[NT][KS][2];
-    float rf[NT][2];             // factor of rows 8 n + 2 c, 8 n + 2 c + 1
-    int see_lo[NT][2], see_hi[NT][2];  // their keys [see_lo, see_hi)
-    int all_lo = 0, all_hi = 0x7fffffff;  // keys that every row of this lane sees
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = 8 * n + g;
-      uint4 raw[KS / 2];
-#pragma unroll
-      for (int i = 0; i < KS / 2; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-      if (r < work.rows) {
-        const int row = work.row0 + r, tok = row / p.group, hd = row - tok * p.group;
-        const __nv_bfloat16* src = p.q + (s.q0 + tok) * p.q_stride + (1LL * work.head * p.group + hd) * D + 16 * c;
-#pragma unroll
-        for (int i = 0; i < KS / 2; ++i)
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(src + (i >> 1) * 64 + (i & 1) * 8));
-      }
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < KS / 2; ++i) {
-        m = __vmaxu2(m, __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu));
-        m = __vmaxu2(m, __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu));
-      }
-      m = max(m & 0xffffu, m >> 16);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int e = max(int(m >> 7) - 127, -100);  // (a row below 2^-100 keeps what f16 has of it)
-      const float f = exp2i(14 - e);
-#pragma unroll
-      for (int i = 0; i < KS / 2; ++i) {
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw[i]);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          qf[n][2 * i + (x >> 1)][x & 1] = f16x2_of(u2f(w[x] << 16) * f, u2f(w[x] & 0xffff0000u) * f);
-      }
-      const float back = exp2i(e - 14) * p.scale_log2;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        rf[n][x] = __shfl_sync(0xffffffffu, back, (2 * c + x) * 4);
-        const int rr = 8 * n + 2 * c + x;
-        see_lo[n][x] = 0;
-        see_hi[n][x] = s.klen;
-        if (rr < work.rows) {
-          const int pos = s.klen - s.qlen + (work.row0 + rr) / p.group;
-          if (p.wr >= 0) see_hi[n][x] = min(s.klen, pos + p.wr + 1);
-          if (p.wl >= 0) see_lo[n][x] = max(0, pos - p.wl);
-        }
-        all_lo = max(all_lo, see_lo[n][x]);
-        all_hi = min(all_hi, see_hi[n][x]);
-      }
-    }
-    all_lo = __reduce_max_sync(0xffffffffu, all_lo);
-    all_hi = __reduce_min_sync(0xffffffffu, all_hi);
-
-    float acc[NT][KS][4];
-    float mrun[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int t = 0; t < KS; ++t)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) acc[n][t][x] = 0.0f;
-      mrun[n][0] = mrun[n][1] = kLow;
-      l[n][0] = l[n][1] = 0.0f;
-    }
-    const int blk_end = (work.k1 + 15) >> 4;
-#pragma unroll 1
-    for (int blk = (work.k0 >> 4) + warp; blk < blk_end; blk += kWarps) {
-      cp_wait<S - 1>();
-      __syncwarp();
-      const uint8_t* st = ring + stage * 2 * C::kHalf;
-      const float ka = sc[warp][stage][0], vb = sc[warp][stage][1];
-      // S^T, two chains over d
-      float sa[NT][4], sb[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) sa[n][x] = sb[n][x] = 0.0f;
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(st + h * 512 + lane * 16);
-        const uint4 k8 = *reinterpret_cast<const uint4*>(st + (D / 64 + h) * 512 + lane * 16);
-        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&k0);
-        const uint32_t* w8 = reinterpret_cast<const uint32_t*>(&k8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = f16x2_of_e4m3x2(uint16_t(w0[i])), a2 = f16x2_of_e4m3x2(uint16_t(w0[i] >> 16));
-          const uint32_t a1 = f16x2_of_e4m3x2(uint16_t(w8[i])), a3 = f16x2_of_e4m3x2(uint16_t(w8[i] >> 16));
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816((i & 1) ? sb[n] : sa[n], a0, a1, a2, a3, qf[n][4 * h + i][0], qf[n][4 * h + i][1]);
-        }
-      }
-      // exponents, masked where the block reaches past what some row sees
-      const float lb = __log2f(vb), rb = __fdividef(1.0f, vb);
-      const int key = blk << 4;
-      const bool edge = key < all_lo || key + 16 > all_hi;
-      bool over = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sa[n][x] = fmaf(sa[n][x] + sb[n][x], rf[n][x & 1] * ka, lb);
-          if (edge) {
-            const int kk = key + g + (x >> 1) * 8;
-            if (kk < see_lo[n][x & 1] || kk >= see_hi[n][x & 1]) sa[n][x] = -INFINITY;
+    // Tiles three deep: one is loaded, the next one's scales are read, the page of the
+    // one after is looked up.
+    struct Tile {
+      int key;        // first key; -1: there are no more
+      int k0, k1;     // of the unit
+      int b, head;
+      int page;       // of this lane's box, and of its block
+      int page_b;
+      float scale;    // lanes 0-7: K's, 8-15: V's
+    };
+    const int n_box = 128 / p.box_rows;
+    int n_items = 0;
+    bool more = true, ok = true, any = false;
+    Cut8 cut;
+    cut.c1 = -1;
+    int t_key = 0, t_end = 0, t_k0 = 0, t_k1 = 0, t_b = 0, t_head = 0;
+    auto next_tile = [&]() -> Tile {  // the tile that follows, with its pages on their way
+      while (more && t_key >= t_end) {
+        more = walk.next(p, lo, hi, me == G - 1);
+        Item8 x;
+        x.head = -1;
+        if (more) {
+          any = true;
+          x.q0 = walk.seq.q0;
+          x.qlen = walk.seq.qlen;
+          x.klen = walk.seq.klen;
+          x.row0 = walk.row0;
+          x.rows = walk.rows;
+          x.head = walk.head;
+          x.k0 = walk.k0;
+          x.k1 = walk.k1;
+          x.slot = walk.first && walk.last ? -1 : walk.first ? 2 * me + 1 : 2 * me;
+          if (walk.first && !walk.last) {
+            cut.seq0 = x.q0;
+            cut.row0 = x.row0;
+            cut.rows = x.rows;
+            cut.kvh = x.head;
+            cut.c0 = me;
+            cut.c1 = int((walk.y1 * G - 1) / all);  // the last whose share begins before y1
           }
-          over = over || sa[n][x] - mrun[n][x & 1] > kTop - kShift;
+          t_k0 = x.k0;
+          t_k1 = x.k1;
+          t_key = x.k0 & ~127;
+          t_end = max(x.k1, 1);  // (a unit without keys has a tile too, an empty one: see kItems)
+          t_b = walk.b_of;
+          t_head = x.head;
+        }
+        const int i = n_items++;
+        ok = ok && seq::warp_wait(&ctl.it_empty[i % kItems], ((i / kItems) & 1) ^ 1, &ctl.abort, LIM);
+        if (!ok) more = false;
+        if (lane == 0 && ok) {
+          ctl.it[i % kItems] = x;
+          mbar_arrive(&ctl.it_full[i % kItems]);
         }
       }
-      if (__any_sync(0xffffffffu, over)) {  // a new maximum, rare after the first blocks
+      Tile t;
+      t.key = -1;
+      t.page = t.page_b = -1;
+      t.scale = 1.0f;
+      if (!more) return t;
+      t.key = t_key;
+      t.k0 = t_k0;
+      t.k1 = t_k1;
+      t.b = t_b;
+      t.head = t_head;
+      t_key += 128;
+      const int* const row = p.table + size_t(t.b) * p.max_pages;
+      const int kb = t.key + lane * p.box_rows, kc = t.key + (lane & 7) * kFp8Block;
+      // (a box or block that is not wholly outside [k0, k1): the others' pages are not looked up)
+      if (lane < n_box && kb < t.k1 && kb + p.box_rows > t.k0) t.page = row[kb / p.page_size];
+      if (lane < 16 && kc < t.k1 && kc + kFp8Block > t.k0) t.page_b = row[kc / p.page_size];
+      return t;
+    };
+    auto read_scale = [&](Tile& t) {
+      if (t.key >= 0 && t.page_b >= 0 && t.page_b < p.num_pages) {
+        const int k = t.key + (lane & 7) * kFp8Block;
+        t.scale = p.scales[lane >> 3 & 1][(size_t(t.page_b) * (p.page_size / kFp8Block) + k % p.page_size / kFp8Block) * p.Hkv + t.head];
+      }
+    };
+    const uint64_t pol = l2_policy_evict_first();
+    Tile a = next_tile();
+    Tile b = next_tile();
+    read_scale(a);
+    bool injected = false;
+    for (int n = 0; a.key >= 0 && ok; ++n) {
+      Tile c = next_tile();
+      read_scale(b);
+      const int slot = n % S;
+      ok = ok && seq::warp_wait(&ctl.empty[slot], ((n / S) & 1) ^ 1, &ctl.abort, LIM);
+      if (!ok) break;
+      if (lane < 16) ctl.sc[slot][lane >> 3][lane & 7] = a.scale;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.full[slot]);
+      const int kb = a.key + lane * p.box_rows;
+      const bool wanted = lane < n_box && kb < a.k1 && kb + p.box_rows > a.k0;
+      int page = a.page;
+      if (wanted && (page < 0 || page >= p.num_pages)) {  // no such page: it reads as zeros, and the caller is told
+        atomicOr(p.status, kDevBadArg);
+        page = p.num_pages;
+      }
+      const unsigned boxes = __ballot_sync(0xffffffffu, wanted);
+      const int in_page = kb % p.page_size;
+      if (p.inject == 1 && !injected) {  // test hook: never deliver this tile
+        injected = true;
+      } else {
+        uint8_t* const dst = ring + slot * 2 * C::kHalf;
+        if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], uint32_t(2 * __popc(boxes) * p.box_rows * D));
+        for (unsigned left = boxes; left != 0; left &= left - 1) {
+          const int x = __ffs(left) - 1;
+          const int pg = __shfl_sync(0xffffffffu, page, x), at = __shfl_sync(0xffffffffu, in_page, x);
+          if (elect_one()) {
+            tma_load_4d_hint(dst + x * p.box_rows * D, &tmK, &ctl.full[slot], 0, a.head, at, pg, pol);
+            tma_load_4d_hint(dst + C::kHalf + x * p.box_rows * D, &tmV, &ctl.full[slot], 0, a.head, at, pg, pol);
+          }
+          __syncwarp();
+        }
+      }
+      a = b;
+      b = c;
+    }
+    if (lane == 0) {
+      p.cuts[me] = cut;
+      p.has[me] = any ? 1 : 0;
+    }
+    if (*const_cast<volatile uint32_t*>(&ctl.abort)) {  // let copies in flight land before shared memory is released
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+  } else {
+    // ------------------------------------------------------------ a warp's keys
+    const int g = lane >> 2, c = lane & 3;
+    // Product row g (and g + 8) is key g, of odd g key g ^ 4: the reads of two
+    // neighbouring rows' codes then meet in no bank, nor do those of V's rows 2 c.
+    const int gk = (g & 1) ? g ^ 4 : g;
+    int n = 0;  // tiles so far
+    for (int i = 0;; ++i) {
+      if (!seq::warp_wait(&ctl.it_full[i % kItems], (i / kItems) & 1, &ctl.abort, LIM)) break;
+      const Item8 w = ctl.it[i % kItems];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
+      if (w.head < 0) break;
+      // Q^T: rows 8 n + g, of d the 16 at 16 c and (d = 128) 64 + 16 c, as K's; divided by
+      // a power of two of the row so that its largest value is in [2^14, 2^15)
+      uint32_t qf[NT][KS][2];
+      float rf[NT][2];                   // factor of rows 8 n + 2 c, 8 n + 2 c + 1
+      int see_lo[NT][2], see_hi[NT][2];  // their keys [see_lo, see_hi)
+      int all_lo = 0, all_hi = 0x7fffffff;  // keys that every row sees
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+      for (int t = 0; t < NT; ++t) {
+        const int r = 8 * t + g;
+        uint4 raw[KS / 2];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float m = fmaxf(sa[n][x], sa[n][x + 2]);
+        for (int k = 0; k < KS / 2; ++k) raw[k] = make_uint4(0, 0, 0, 0);
+        if (r < w.rows) {
+          const int row = w.row0 + r, tok = row / p.group, hd = row - tok * p.group;
+          const __nv_bfloat16* src = p.q + (w.q0 + tok) * p.q_stride + (1LL * w.head * p.group + hd) * D + 16 * c;
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            m = fmaxf(m, mrun[n][x]);
-            const float f = ex2_mufu(mrun[n][x] - m);
-            mrun[n][x] = m;
-            l[n][x] *= f;
+          for (int k = 0; k < KS / 2; ++k) raw[k] = __ldg(reinterpret_cast<const uint4*>(src + (k >> 1) * 64 + (k & 1) * 8));
+        }
+        uint32_t m = 0;
 #pragma unroll
-            for (int t = 0; t < KS; ++t) {
-              acc[n][t][x] *= f;
-              acc[n][t][x + 2] *= f;
+        for (int k = 0; k < KS / 2; ++k) {
+          m = __vmaxu2(m, __vmaxu2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu));
+          m = __vmaxu2(m, __vmaxu2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu));
+        }
+        m = max(m & 0xffffu, m >> 16);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = max(int(m >> 7) - 127, -100);  // (a row below 2^-100 keeps what f16 has of it)
+        const float f = exp2i(14 - e);
+#pragma unroll
+        for (int k = 0; k < KS / 2; ++k) {
+          const uint32_t y[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            qf[t][2 * k + (x >> 1)][x & 1] = f16x2_of(u2f(y[x] << 16) * f, u2f(y[x] & 0xffff0000u) * f);
+        }
+        const float back = exp2i(e - 14) * p.scale_log2;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          rf[t][x] = __shfl_sync(0xffffffffu, back, (2 * c + x) * 4);
+          const int rr = 8 * t + 2 * c + x;
+          see_lo[t][x] = 0;
+          see_hi[t][x] = w.klen;
+          if (rr < w.rows) {
+            const int pos = w.klen - w.qlen + (w.row0 + rr) / p.group;
+            if (p.wr >= 0) see_hi[t][x] = min(w.klen, pos + p.wr + 1);
+            if (p.wl >= 0) see_lo[t][x] = max(0, pos - p.wl);
+          }
+          all_lo = max(all_lo, see_lo[t][x]);
+          all_hi = min(all_hi, see_hi[t][x]);
+        }
+      }
+      all_lo = __reduce_max_sync(0xffffffffu, all_lo);
+      all_hi = __reduce_min_sync(0xffffffffu, all_hi);
+
+      float acc[NT][KS][4];
+      float mrun[NT][2], l[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[t][k][x] = 0.0f;
+        mrun[t][0] = mrun[t][1] = kLow;
+        l[t][0] = l[t][1] = 0.0f;
+      }
+      bool ok = true;
+      for (int key = (w.k0 & ~127) + warp * 16, last = max(w.k1, 1) + warp * 16; key < last; key += 128, ++n) {
+        const int slot = n % S;
+        ok = seq::warp_wait(&ctl.full[slot], (n / S) & 1, &ctl.abort, LIM);
+        if (!ok) break;
+        if (key < w.k1 && key + 16 > w.k0) {
+          const uint8_t* const kt = ring + slot * 2 * C::kHalf + (warp * 16) * D;
+          const uint8_t* const vt = kt + C::kHalf;
+          const float ka = ctl.sc[slot][0][warp], vb = ctl.sc[slot][1][warp];
+          // S^T, two chains over d
+          float sa[NT][4], sb[NT][4];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sa[t][x] = sb[t][x] = 0.0f;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            // pieces of 16 bytes, swizzled over 128 bytes (d = 128) or 64
+            const int piece = D == 128 ? (4 * h + c) ^ gk : c ^ (gk >> 1 & 3);
+            const uint4 x0 = *reinterpret_cast<const uint4*>(kt + gk * D + piece * 16);
+            const uint4 x8 = *reinterpret_cast<const uint4*>(kt + (gk + 8) * D + piece * 16);
+            const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w8[4] = {x8.x, x8.y, x8.z, x8.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t a0 = f16x2_of_e4m3x2(uint16_t(w0[k])), a2 = f16x2_of_e4m3x2(uint16_t(w0[k] >> 16));
+              const uint32_t a1 = f16x2_of_e4m3x2(uint16_t(w8[k])), a3 = f16x2_of_e4m3x2(uint16_t(w8[k] >> 16));
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+                mma16816((k & 1) ? sb[t] : sa[t], a0, a1, a2, a3, qf[t][4 * h + k][0], qf[t][4 * h + k][1]);
             }
           }
-      }
-      uint32_t pf[NT][2];
+          // exponents, masked where the block reaches past what some row sees
+          const float lb = __log2f(vb), rb = __fdividef(1.0f, vb);
+          const bool edge = key < all_lo || key + 16 > all_hi;
+          bool over = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+          for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sa[n][x] = ex2_mufu(sa[n][x] - (mrun[n][x & 1] - kShift));
-        l[n][0] = fmaf(sa[n][0] + sa[n][2], rb, l[n][0]);
-        l[n][1] = fmaf(sa[n][1] + sa[n][3], rb, l[n][1]);
-        pf[n][0] = transposed8x8(f16x2_of(sa[n][0], sa[n][1]));
-        pf[n][1] = transposed8x8(f16x2_of(sa[n][2], sa[n][3]));
-      }
-      // O^T: the d at g D / 8 + 2 t and + 2 t + 1 are rows g and g + 8 of tile t
-      constexpr int W = D / 32;  // words of a key's D / 8 values
-      uint32_t v[4][W];
+            for (int x = 0; x < 4; ++x) {
+              sa[t][x] = fmaf(sa[t][x] + sb[t][x], rf[t][x & 1] * ka, lb);
+              if (edge) {
+                const int kk = key + gk + (x >> 1) * 8;
+                if (kk < see_lo[t][x & 1] || kk >= see_hi[t][x & 1]) sa[t][x] = -INFINITY;
+              }
+              over = over || sa[t][x] - mrun[t][x & 1] > kTop - kShift;
+            }
+          }
+          if (__any_sync(0xffffffffu, over)) {  // a new maximum, rare after the first blocks
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (D == 128) {
-          *reinterpret_cast<uint4*>(v[i]) = *reinterpret_cast<const uint4*>(st + C::kHalf + i * 512 + lane * 16);
-        } else {
-          *reinterpret_cast<uint2*>(v[i]) = *reinterpret_cast<const uint2*>(st + C::kHalf + i * 256 + lane * 8);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                float m = fmaxf(sa[t][x], sa[t][x + 2]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                // (each row for itself, so that no row's roundings depend on its neighbours)
+                m = m - mrun[t][x] > kTop - kShift ? m : mrun[t][x];
+                const float f = ex2_mufu(mrun[t][x] - m);
+                mrun[t][x] = m;
+                l[t][x] *= f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                  acc[t][k][x] *= f;
+                  acc[t][k][x + 2] *= f;
+                }
+              }
+          }
+          uint32_t pf[NT][2];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sa[t][x] = ex2_mufu(sa[t][x] - (mrun[t][x & 1] - kShift));
+            l[t][0] = fmaf(sa[t][0] + sa[t][2], rb, l[t][0]);
+            l[t][1] = fmaf(sa[t][1] + sa[t][3], rb, l[t][1]);
+            pf[t][0] = transposed8x8(f16x2_of(sa[t][0], sa[t][1]));
+            pf[t][1] = transposed8x8(f16x2_of(sa[t][2], sa[t][3]));
+          }
+          // O^T: lane (g, c) has V's keys of product rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9, and of d the
+          // D / 8 at g D / 8, of which 2 t and 2 t + 1 are rows g and g + 8 of tile t
+          constexpr int W = D / 32;  // words of a key's D / 8 values
+          uint32_t v[4][W];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = 2 * c + (k & 1) + (k >> 1) * 8, r = (k & 1) ? row ^ 4 : row;
+            if constexpr (D == 128) {
+              const uint4 y = *reinterpret_cast<const uint4*>(vt + r * 128 + ((g ^ (r & 7)) << 4));
+              v[k][0] = y.x;
+              v[k][1] = y.y;
+              v[k][W - 2] = y.z;
+              v[k][W - 1] = y.w;
+            } else {
+              const uint2 y = *reinterpret_cast<const uint2*>(vt + r * 64 + (((g >> 1) ^ (r >> 1 & 3)) << 4) + (g & 1) * 8);
+              v[k][0] = y.x;
+              v[k][1] = y.y;
+            }
+            if (key + 16 > w.klen) {  // past the sequence's end: 0 * NaN would stay NaN
+#pragma unroll
+              for (int x = 0; x < W; ++x) v[k][x] = key + r < w.klen ? v[k][x] : 0;
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < W; ++x) {
+            const uint32_t x0 = __byte_perm(v[0][x], v[1][x], 0x5140), x1 = __byte_perm(v[0][x], v[1][x], 0x7362);
+            const uint32_t y0 = __byte_perm(v[2][x], v[3][x], 0x5140), y1 = __byte_perm(v[2][x], v[3][x], 0x7362);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t u = k == 0 ? x0 : x1, y = k == 0 ? y0 : y1;
+              const uint32_t a0 = f16x2_of_e4m3x2(uint16_t(u)), a1 = f16x2_of_e4m3x2(uint16_t(u >> 16));
+              const uint32_t a2 = f16x2_of_e4m3x2(uint16_t(y)), a3 = f16x2_of_e4m3x2(uint16_t(y >> 16));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816(acc[t][2 * x + k], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+            }
+          }
         }
-        if (key + 16 > s.klen) {  // past the sequence's end: 0 * NaN would stay NaN
-          const bool in = key + 2 * c + (i & 1) + (i >> 1) * 8 < s.klen;
-#pragma unroll
-          for (int w = 0; w < W; ++w) v[i][w] = in ? v[i][w] : 0;
-        }
+        __syncwarp();  // every lane has read the tile
+        if (lane == 0) mbar_arrive(&ctl.empty[slot]);
       }
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-        const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t x = i == 0 ? x0 : x1, y = i == 0 ? y0 : y1;
-          const uint32_t a0 = f16x2_of_e4m3x2(uint16_t(x)), a1 = f16x2_of_e4m3x2(uint16_t(x >> 16));
-          const uint32_t a2 = f16x2_of_e4m3x2(uint16_t(y)), a3 = f16x2_of_e4m3x2(uint16_t(y >> 16));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(acc[n][2 * w + i], a0, a1, a2, a3, pf[n][0], pf[n][1]);
-        }
-      }
-      __syncwarp();  // every lane has read the stage
-      issue(stage);
-      stage = stage + 1 == S ? 0 : stage + 1;
-    }
+      if (!ok) break;
 
-    // ---- the warps' results joined
+      // ---- the warps' results joined
+      if (!seq::warp_wait(&ctl.join_empty, (i & 1) ^ 1, &ctl.abort, LIM)) break;  // the unit's before have been read
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float t = l[n][x];
+        for (int x = 0; x < 2; ++x) {
+          float sum = l[t][x];
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-        const int r = 8 * n + 2 * c + x;
-        // O and l are 2^kShift of what belongs to mrun
-        if (g == 0) ml[warp][r] = make_float2(mrun[n][x] == kLow ? kLow : mrun[n][x] - kShift, t);
-        float* dst = join + (warp * R + r) * C::kJoinLd + g * (D / 8);
+          for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          const int r = 8 * t + 2 * c + x;
+          // O and l are 2^kShift of what belongs to mrun
+          if (g == 0) ctl.ml[warp][r] = make_float2(mrun[t][x] == kLow ? kLow : mrun[t][x] - kShift, sum);
+          float* dst = join + (warp * R + r) * C::kJoinLd + g * (D / 8);
 #pragma unroll
-        for (int t4 = 0; t4 < KS / 2; ++t4)
-          *reinterpret_cast<float4*>(dst + 4 * t4) =
-              make_float4(acc[n][2 * t4][x], acc[n][2 * t4][x + 2], acc[n][2 * t4 + 1][x], acc[n][2 * t4 + 1][x + 2]);
+          for (int k = 0; k < KS / 2; ++k)
+            *reinterpret_cast<float4*>(dst + 4 * k) =
+                make_float4(acc[t][2 * k][x], acc[t][2 * k][x + 2], acc[t][2 * k + 1][x], acc[t][2 * k + 1][x + 2]);
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.join_full);
+      if (!seq::warp_wait(&ctl.join_full, i & 1, &ctl.abort, LIM)) break;
+      constexpr int Q4 = D / 4;
+#pragma unroll 1
+      for (int at = tid; at < w.rows * Q4; at += kWarps * 32) {
+        const int r = at / Q4, d4 = (at - r * Q4) * 4;
+        float m = kLow;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) m = fmaxf(m, ctl.ml[k][r].x);
+        float lsum = 0.0f;
+        float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+          const float2 t = ctl.ml[k][r];
+          const float f = ex2_mufu(t.x - m);
+          const float4 y = *reinterpret_cast<const float4*>(join + (k * R + r) * C::kJoinLd + d4);
+          lsum = fmaf(t.y, f, lsum);
+          o.x = fmaf(y.x, f, o.x);
+          o.y = fmaf(y.y, f, o.y);
+          o.z = fmaf(y.z, f, o.z);
+          o.w = fmaf(y.w, f, o.w);
+        }
+        if (w.slot >= 0) {
+          *reinterpret_cast<float4*>(p.part_o + (size_t(w.slot) * R + r) * D + d4) = o;
+          if (d4 == 0) p.part_ml[size_t(w.slot) * R + r] = make_float2(m, lsum);
+        } else {
+          const int row = w.row0 + r, tok = row / p.group, hd = w.head * p.group + row - tok * p.group;
+          const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
+          *reinterpret_cast<uint2*>(p.o + (size_t(w.q0 + tok) * p.Hq + hd) * D + d4) =
+              make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+          if (d4 == 0)
+            p.lse[size_t(hd) * p.total_q + w.q0 + tok] =
+                lsum == 0.0f ? -INFINITY : (m + __log2f(lsum)) * 0.69314718055994531f;
+        }
       }
-    __syncthreads();
-    const bool part = !(work.first && work.last);
-    const int slot = work.first ? 2 * me + 1 : 2 * me;
-    constexpr int Q4 = D / 4;
-    for (int i = tid; i < work.rows * Q4; i += kThreads) {
-      const int r = i / Q4, d4 = (i - r * Q4) * 4;
-      float m = kLow;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w][r].x);
-      float lsum = 0.0f;
-      float4 o = make_float4(0, 0, 0, 0);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 t = ml[w][r];
-        const float f = ex2_mufu(t.x - m);
-        const float4 y = *reinterpret_cast<const float4*>(join + (w * R + r) * C::kJoinLd + d4);
-        lsum = fmaf(t.y, f, lsum);
-        o.x = fmaf(y.x, f, o.x);
-        o.y = fmaf(y.y, f, o.y);
-        o.z = fmaf(y.z, f, o.z);
-        o.w = fmaf(y.w, f, o.w);
-      }
-      if (part) {
-        *reinterpret_cast<float4*>(p.part_o + (size_t(slot) * R + r) * D + d4) = o;
-        if (d4 == 0) p.part_ml[size_t(slot) * R + r] = make_float2(m, lsum);
-      } else {
-        const int row = work.row0 + r, tok = row / p.group, hd = work.head * p.group + row - tok * p.group;
-        const float inv = lsum == 0.0f ? 0.0f : 1.0f / lsum;
-        *reinterpret_cast<uint2*>(p.o + (size_t(s.q0 + tok) * p.Hq + hd) * D + d4) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (d4 == 0)
-          p.lse[size_t(hd) * p.total_q + s.q0 + tok] =
-              lsum == 0.0f ? -INFINITY : (m + __log2f(lsum)) * 0.69314718055994531f;
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.join_empty);
     }
-    if (work.first && !work.last) {
-      cut.seq0 = s.q0;
-      cut.row0 = work.row0;
-      cut.rows = work.rows;
-      cut.kvh = work.head;
-      cut.c0 = me;
-      cut.c1 = int((work.y1 * G - 1) / all);  // the last whose share begins before y1
-    }
-    __syncthreads();  // before the next unit's results
   }
-  cp_wait<0>();
-  if (tid == 0) {
-    p.cuts[me] = cut;
-    p.has[me] = any ? 1 : 0;
-  }
+  __syncthreads();
+  if (tid == 0 && ctl.abort) atomicOr(p.status, kDevTimeout);
 }
 
 // The parts of the units that several workers share: O = sum_i 2^(m_i - m) O_i /
@@ -674,13 +767,11 @@ __global__ void __launch_bounds__(R * 32) join8_kernel(const Params8 p) {
 template <int D, int NT>
 cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream) {
   using C = Shape<D, NT>;
-  const int G = num_sms();
+  const int G = num_sms() * C::kPerSm;
   Params8 p{};
   p.q = static_cast<const __nv_bfloat16*>(pb.q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.pages[0] = static_cast<const uint8_t*>(pb.k);
-  p.pages[1] = static_cast<const uint8_t*>(pb.v);
   p.scales[0] = sc.k;
   p.scales[1] = sc.v;
   p.table = pb.page_table;
@@ -698,6 +789,21 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
   p.wr = pb.window_right;
   p.status = status_word();
   if (p.status == nullptr) return cudaErrorLaunchFailure;
+  const DebugCfg dc = debug_cfg();
+  p.wait_limit_ns = dc.wait_limit_ns;
+  p.inject = dc.inject;
+  CUtensorMap maps[2];
+  p.box_rows = 128;
+  while (pb.page_size % p.box_rows != 0) p.box_rows /= 2;  // 16 at least
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t row = uint64_t(pb.Hkv) * D;
+    const uint64_t dims[4] = {uint64_t(D), uint64_t(pb.Hkv), uint64_t(pb.page_size), uint64_t(pb.num_pages)};
+    const uint64_t strides[3] = {uint64_t(D), row, row * pb.page_size};
+    const uint32_t box[4] = {uint32_t(D), 1, uint32_t(p.box_rows), 1};
+    if (!encode_tiled(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i == 0 ? pb.k : pb.v, dims, strides, box,
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
   auto kern = attend8_kernel<D, NT>;
   static seq::SmemLimit limit;
   cudaError_t e = limit.set(kern, C::kSmem);
@@ -715,7 +821,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
   if (pool == nullptr || cudaMallocFromPoolAsync(&ws, carve(nullptr), pool, stream) != cudaSuccess)
     return cudaErrorMemoryAllocation;
   carve(static_cast<uint8_t*>(ws));
-  kern<<<G, kThreads, C::kSmem, stream>>>(p);
+  kern<<<G, kThreads, C::kSmem, stream>>>(maps[0], maps[1], p);
   e = cudaGetLastError();
   if (e == cudaSuccess) {  // starts while the kernel before it ends, and waits for it
     cudaLaunchAttribute pdl[1];
@@ -736,17 +842,11 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
 }  // namespace seq8
 
 cudaError_t launch_seq_fwd8(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream) {
-  // rows of a unit: as many as the mean sequence has
-  const long long rows = (1LL * pb.total_q + pb.B - 1) / pb.B * (pb.Hq / pb.Hkv);
-  if (rows > 32) return launch_seq_fwd_codes(pb, sc, o, lse, stream);
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  const long long rows = (1LL * pb.total_q + pb.B - 1) / pb.B * (pb.Hq / pb.Hkv);  // of the mean sequence
+  if (rows > 16) return launch_seq_fwd_codes(pb, sc, o, lse, stream);
   if (pb.d == 128)
-    return nt == 1   ? seq8::launch_t<128, 1>(pb, sc, o, lse, stream)
-           : nt == 2 ? seq8::launch_t<128, 2>(pb, sc, o, lse, stream)
-                     : seq8::launch_t<128, 4>(pb, sc, o, lse, stream);
-  return nt == 1   ? seq8::launch_t<64, 1>(pb, sc, o, lse, stream)
-         : nt == 2 ? seq8::launch_t<64, 2>(pb, sc, o, lse, stream)
-                   : seq8::launch_t<64, 4>(pb, sc, o, lse, stream);
+    return rows <= 8 ? seq8::launch_t<128, 1>(pb, sc, o, lse, stream) : seq8::launch_t<128, 2>(pb, sc, o, lse, stream);
+  return rows <= 8 ? seq8::launch_t<64, 1>(pb, sc, o, lse, stream) : seq8::launch_t<64, 2>(pb, sc, o, lse, stream);
 }
 
 }  // namespace fa
