@@ -232,7 +232,8 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 bool encode_tiled(CUtensorMap* m, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
-                  const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+                  const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                  CUtensorMapL2promotion promotion) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return false;
   cuuint64_t d[5], st[4];
@@ -243,8 +244,8 @@ bool encode_tiled(CUtensorMap* m, CUtensorMapDataType dtype, int rank, const voi
     es[i] = 1;
     if (i + 1 < rank) st[i] = strides[i];
   }
-  return encode(m, dtype, rank, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode(m, dtype, rank, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool make_bshd_map(CUtensorMap* m, const void* base, int B, int N, int H, int d, int box_rows) {

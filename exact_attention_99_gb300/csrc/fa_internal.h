@@ -59,9 +59,23 @@ unsigned* status_word();
 bool make_bshd_map(CUtensorMap* m, const void* base, int B, int N, int H, int d, int box_rows);
 
 // Any tiled tensor map: rank <= 5, dims innermost first, strides (bytes) of
-// dims 1..rank-1, zero fill out of range.
+// dims 1..rank-1, zero fill out of range; promotion: what L2 fetches at least.
 bool encode_tiled(CUtensorMap* m, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
-                  const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
+                  const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                  CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+// A tensor map over pages of codes [num_pages, page_size, Hkv, d]: boxes of box_rows
+// rows of one head. L2 fetches no more than the row's own bytes: the next head's, of
+// which 256 bytes would have some too, are gone before their turn (two single tokens
+// over 116000 and 131000 keys read 668 MB and not 506).
+inline bool encode_codes(CUtensorMap* m, const void* pages, int num_pages, int page_size, int Hkv, int d, int box_rows,
+                         CUtensorMapSwizzle swizzle) {
+  const uint64_t row = uint64_t(Hkv) * d;
+  const uint64_t dims[4] = {uint64_t(d), uint64_t(Hkv), uint64_t(page_size), uint64_t(num_pages)};
+  const uint64_t strides[3] = {uint64_t(d), row, row * page_size};
+  const uint32_t box[4] = {uint32_t(d), 1, uint32_t(box_rows), 1};
+  return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pages, dims, strides, box, swizzle,
+                      d == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B);
+}
 
 // Window bounds as the kernels take them: negative -> -1 (no limit); a
 // bound that reaches past every key (>= Nq + Nk) is no limit either.

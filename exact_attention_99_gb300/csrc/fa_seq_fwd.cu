@@ -1710,17 +1710,11 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
     // rows of D bytes; 32 of 64 bytes go together (see the producers)
     p.box_rows = D == 128 ? 128 : 32;
     while (pb.page_size % p.box_rows != 0) p.box_rows /= 2;  // 16 at least
-    const void* kp[2] = {pb.k, pb.v};
-    CUtensorMap* maps[2] = {&mk, &mv};
-    for (int i = 0; i < 2; ++i) {
-      const uint64_t row = uint64_t(pb.Hkv) * D;
-      const uint64_t dims[4] = {uint64_t(D), uint64_t(pb.Hkv), uint64_t(pb.page_size), uint64_t(pb.num_pages)};
-      const uint64_t strides[3] = {uint64_t(D), row, row * pb.page_size};
-      const uint32_t box[4] = {uint32_t(D), 1, uint32_t(p.box_rows), 1};
-      if (!encode_tiled(maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, kp[i], dims, strides, box,
-                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : i == 0 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE))
-        return cudaErrorInvalidValue;
-    }
+    if (!encode_codes(&mk, pb.k, pb.num_pages, pb.page_size, pb.Hkv, D, p.box_rows,
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_codes(&mv, pb.v, pb.num_pages, pb.page_size, pb.Hkv, D, p.box_rows,
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
     p.scales[0] = sc->k;
     p.scales[1] = sc->v;
   } else if constexpr (PAGED) {

@@ -795,15 +795,10 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
   CUtensorMap maps[2];
   p.box_rows = 128;
   while (pb.page_size % p.box_rows != 0) p.box_rows /= 2;  // 16 at least
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t row = uint64_t(pb.Hkv) * D;
-    const uint64_t dims[4] = {uint64_t(D), uint64_t(pb.Hkv), uint64_t(pb.page_size), uint64_t(pb.num_pages)};
-    const uint64_t strides[3] = {uint64_t(D), row, row * pb.page_size};
-    const uint32_t box[4] = {uint32_t(D), 1, uint32_t(p.box_rows), 1};
-    if (!encode_tiled(&maps[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i == 0 ? pb.k : pb.v, dims, strides, box,
+  for (int i = 0; i < 2; ++i)
+    if (!encode_codes(&maps[i], i == 0 ? pb.k : pb.v, pb.num_pages, pb.page_size, pb.Hkv, D, p.box_rows,
                       D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
-  }
   auto kern = attend8_kernel<D, NT>;
   static seq::SmemLimit limit;
   cudaError_t e = limit.set(kern, C::kSmem);
