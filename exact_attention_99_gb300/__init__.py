@@ -609,6 +609,22 @@ def cache_append(k, v, k_pages, v_pages, cu_q, lens_k, page_table, stream=None) 
 
 def _cache8_args(k_pages, v_pages, k_scales, v_scales, cu_q, lens_k, page_table, hkv, d, device):
     """_cache_args of an e4m3 cache, with its scales."""
+    shape, table = k_pages.shape, page_table.shape
+    if len(shape) == 4 and len(table) == 2:
+        num_pages, page_size, h, dd = shape
+        B, max_pages = table
+        # all in one expression, the small calls' time; what is wrong is said below
+        if (h == hkv and dd == d and k_pages.dtype is _e4m3 and v_pages.dtype is _e4m3 and v_pages.shape == shape
+                and k_scales.dtype is _f32 and v_scales.dtype is _f32
+                and k_scales.shape == (num_pages, page_size // 16, hkv) and v_scales.shape == k_scales.shape
+                and cu_q.dtype is _i32 and lens_k.dtype is _i32 and page_table.dtype is _i32
+                and cu_q.shape == (B + 1,) and lens_k.shape == (B,)
+                and k_pages.is_contiguous() and v_pages.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous() and cu_q.is_contiguous() and lens_k.is_contiguous()
+                and page_table.is_contiguous()
+                and k_pages.get_device() == v_pages.get_device() == k_scales.get_device() == v_scales.get_device()
+                == cu_q.get_device() == lens_k.get_device() == page_table.get_device() == device):
+            return B, num_pages, page_size, max_pages
     sizes = _cache_args(k_pages, v_pages, cu_q, lens_k, page_table, hkv, d, device, _e4m3)
     shape = (sizes[1], sizes[2] // 16, hkv)
     _packed("k_scales", k_scales, shape, device, _f32)
@@ -720,21 +736,22 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str | None = No
     return torch.tensor(f, dtype=torch.float64).to(torch.float32), mscale
 
 
-def _rotary(stream, q, k, inv_freq, cu, lens, out, sizes, strides, mscale, interleaved, transposed):
-    hq, hk, total, d = sizes
+def _rotary(stream, q, k, inv_freq, cu, lens, out, hq, hk, total, d, qs, ks, mscale, interleaved, transposed):
+    device = (k if q is None else q).get_device()
     if out is None:
-        qo, ko = (None if x is None else _empty(x.shape, dtype=_bf16, device=x.device) for x in (q, k))
+        qo = None if q is None else _empty((total, hq, d), dtype=_bf16, device=q.device)
+        ko = None if k is None else _empty((total, hk, d), dtype=_bf16, device=k.device)
+        qos, kos = hq * d, hk * d
     else:
         qo, ko = out
-    so = [0, 0]
-    for i, (name, x, y) in enumerate((("q", q, qo), ("k", k, ko))):
-        if (x is None) != (y is None):
-            raise ValueError(f"the outputs must hold {name} if and only if it is given")
-        if y is not None:
-            so[i] = _tokens(f"the output of {name}", y, x.get_device(), x.shape)
-    st = lib().fa_rotary(_ptr(q), _ptr(k), _ptr(qo), _ptr(ko), inv_freq.data_ptr(), cu.data_ptr(), _ptr(lens),
-                         cu.shape[0] - 1, hq, hk, total, d, 2 * inv_freq.shape[0], *strides, *so, mscale, interleaved,
-                         transposed, stream)
+        if (q is None) != (qo is None) or (k is None) != (ko is None):
+            raise ValueError("the outputs must hold q, or k, if and only if it is given")
+        qos = 0 if qo is None else _tokens("the output of q", qo, device, q.shape)
+        kos = 0 if ko is None else _tokens("the output of k", ko, device, k.shape)
+    st = lib().fa_rotary(None if q is None else q.data_ptr(), None if k is None else k.data_ptr(),
+                         None if qo is None else qo.data_ptr(), None if ko is None else ko.data_ptr(),
+                         inv_freq.data_ptr(), cu.data_ptr(), None if lens is None else lens.data_ptr(), cu.shape[0] - 1,
+                         hq, hk, total, d, 2 * inv_freq.shape[0], qs, ks, qos, kos, mscale, interleaved, transposed, stream)
     if st != 0:
         raise FAError(st, "fa_rotary")
     return qo, ko
@@ -743,32 +760,36 @@ def _rotary(stream, q, k, inv_freq, cu, lens, out, sizes, strides, mscale, inter
 def _turn(q, k, inv_freq, cu, lens, interleaved, mscale, out, stream, transposed):
     if q is None and k is None:
         raise ValueError("q or k must be given")
-    some = q if q is not None else k
-    device = _first("q" if q is not None else "k", some)
-    total, _, d = some.shape
-    strides = [0, 0]
+    some = k if q is None else q
+    device = _first("k" if q is None else "q", some)
+    total, hq, d = some.shape
+    hk = qs = ks = 0
     if q is not None:
-        strides[0] = _tokens("q", q, device, q.shape)
+        qs = _tokens("q", q, device, q.shape)
+    else:
+        hq = 0
     if k is not None:
         if k.dim() != 3 or k.shape[0] != total or k.shape[1] < 1 or k.shape[2] != d:
             raise ValueError(f"k must have the shape [{total}, kv heads, {d}]")
-        strides[1] = _tokens("k", k, device, k.shape)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must hold a frequency for each pair")
-    _packed("inv_freq", inv_freq, inv_freq.shape, device, _f32)
+        hk = k.shape[1]
+        ks = _tokens("k", k, device, k.shape)
     n = cu.shape
-    _ints("cu", cu, n, device)
-    if len(n) != 1 or n[0] < 2:
+    if not (len(n) == 1 and n[0] >= 2 and cu.dtype is _i32 and inv_freq.dim() == 1 and inv_freq.dtype is _f32
+            and cu.is_contiguous() and inv_freq.is_contiguous() and cu.get_device() == inv_freq.get_device() == device):
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must hold a frequency for each pair")
+        _packed("inv_freq", inv_freq, inv_freq.shape, device, _f32)
+        _ints("cu", cu, n, device)
         raise ValueError("cu must hold the row offsets of one sequence at least")
     if lens is not None:
         _ints("lens", lens, (n[0] - 1,), device)
-    sizes = (0 if q is None else q.shape[1], 0 if k is None else k.shape[1], total, d)
     s = _here(device, stream)
-    a = (q, k, inv_freq, cu, lens, out, sizes, strides, float(mscale), int(bool(interleaved)), transposed)
     if s is not None:
-        return _rotary(s, *a)
+        return _rotary(s, q, k, inv_freq, cu, lens, out, hq, hk, total, d, qs, ks, mscale, 1 if interleaved else 0,
+                       transposed)
     with _on(device, stream):
-        return _rotary(_current_stream(), *a)
+        return _rotary(_current_stream(), q, k, inv_freq, cu, lens, out, hq, hk, total, d, qs, ks, mscale,
+                       1 if interleaved else 0, transposed)
 
 
 def rotary(q, k, inv_freq, cu, lens=None, interleaved: bool = False, mscale: float = 1.0, out=None, stream=None):

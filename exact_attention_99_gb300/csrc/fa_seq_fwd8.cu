@@ -48,7 +48,7 @@ using seq::Seq;
 
 constexpr int kWarps = 8, kThreads = (kWarps + 1) * 32;  // warp 8: the producer
 constexpr int kItems = 4;      // ring of units: the producer is up to three tiles ahead, and each unit has one at least
-constexpr int kItemCost = 2;  // of a unit beside its tiles, in tiles
+constexpr int kItemCost = 1;  // of a unit beside its tiles, in tiles (64 single tokens: 158 us; of 2, 4, 6: 159, 162, 166)
 // P' is at most 2^15 (f16 holds 65504), and 2^7 where the running maximum is up to date
 constexpr float kTop = 15.0f, kShift = 7.0f;
 constexpr float kLow = -FLT_MAX;  // a running maximum before any key
