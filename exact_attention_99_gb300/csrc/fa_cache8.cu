@@ -50,10 +50,13 @@ struct Part {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) {
+__global__ void __launch_bounds__(kThreads, 4) append8_kernel(const Append8Args a) {
   __shared__ Part parts[kMaxTokens];
+  __shared__ int n_parts;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t0 = blockIdx.x * a.tokens;
+  if (tid == 0) n_parts = 0;
+  __syncthreads();
   for (int i = warp; i < a.tokens; i += kWarps) {
     const int t = t0 + i;
     Part p{-1, t, 0};
@@ -73,33 +76,34 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) 
         }
       }
     }
-    if (lane == 0) parts[i] = p;
+    if (lane == 0 && p.n > 0) parts[atomicAdd(&n_parts, 1)] = p;  // (in any order: no two have a block in common)
   }
   __syncthreads();
   constexpr int kLanes = D / 8;         // lanes of a row, 8 values each
   constexpr int kAtOnce = 32 / kLanes;  // rows of an access
   constexpr int kSteps = kBlock / kAtOnce;
   const int r0 = lane / kLanes, c = lane % kLanes * 8;
-  const int tasks = a.tokens * 2 * a.Hkv;
+  const int tasks = n_parts * 2 * a.Hkv;
   for (int task = blockIdx.y * kWarps + warp; task < tasks; task += gridDim.y * kWarps) {
     const int i = task / (2 * a.Hkv), what = task - i * 2 * a.Hkv, head = what >> 1, kv = what & 1;
     const Part p = parts[i];
-    if (p.n == 0) continue;
     const int held = int(p.row % kBlock);  // rows of the block before the new ones
     float* const scale_at = a.scales[kv] + p.row / kBlock * a.Hkv + head;
     const float before = held > 0 ? *scale_at : 0.0f;
     const uint16_t* src = a.x[kv] + p.t * a.stride[kv] + 1LL * head * D + c;
     uint4 v[kSteps];
+    {
+      const uint16_t* at = src + r0 * a.stride[kv];
+      const long long step = kAtOnce * a.stride[kv];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int r = s * kAtOnce + r0;
-      v[s] = r < p.n ? __ldcs(reinterpret_cast<const uint4*>(src + r * a.stride[kv])) : make_uint4(0, 0, 0, 0);
+      for (int s = 0; s < kSteps; ++s, at += step)
+        v[s] = s * kAtOnce + r0 < p.n ? __ldcs(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
     }
     uint32_t m = 0;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      m = __vmaxu2(m, __vmaxu2(v[s].x & 0x7fff7fffu, v[s].y & 0x7fff7fffu));
-      m = __vmaxu2(m, __vmaxu2(v[s].z & 0x7fff7fffu, v[s].w & 0x7fff7fffu));
+      m = max_u16x2(m, max_u16x2(v[s].x & 0x7fff7fffu, v[s].y & 0x7fff7fffu));
+      m = max_u16x2(m, max_u16x2(v[s].z & 0x7fff7fffu, v[s].w & 0x7fff7fffu));
     }
     uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
     if (top >= 0x7f80u) {  // infinities and NaN, held as NaN, are no part of the scale
@@ -140,14 +144,12 @@ __global__ void __launch_bounds__(kThreads) append8_kernel(const Append8Args a) 
         }
       }
     }
-    uint8_t* dst = a.pages[kv] + (p.row * a.Hkv + head) * D + c;
+    const int row_bytes = a.Hkv * D;
+    uint8_t* dst = a.pages[kv] + ((p.row + r0) * a.Hkv + head) * D + c;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int r = s * kAtOnce + r0;
-      if (r < p.n)
-        *reinterpret_cast<uint2*>(dst + 1LL * r * a.Hkv * D) =
-            make_uint2(e4m3x4_of_bf16(v[s].x, v[s].y, inv), e4m3x4_of_bf16(v[s].z, v[s].w, inv));
-    }
+    for (int s = 0; s < kSteps; ++s, dst += kAtOnce * row_bytes)
+      if (s * kAtOnce + r0 < p.n)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(e4m3x4_of_bf16(v[s].x, v[s].y, inv), e4m3x4_of_bf16(v[s].z, v[s].w, inv));
     if (lane == 0) *scale_at = scale;
   }
   // every wrong length is told, also where no token leads to it

@@ -37,10 +37,8 @@ struct RotaryArgs {
   const float* inv_freq;
   seq::Lens L;
   int heads, hq;     // of both, of q
-  int per_head;      // d / 16 pairs of pieces
-  int turned;        // of those the first rot / 16 are turned
+  int turned;        // of a head's pairs of pieces the first rot / 16 are turned
   int rows;          // tokens of a block
-  int interleaved;
   int copy_rest;     // the part of a head that is not turned: copied, or left alone in place
   float mscale, sign;
   unsigned* status;
@@ -68,44 +66,41 @@ __device__ __forceinline__ unsigned long long turn_of(float f) {
   return (bits >> 31) ? 0 - u : u;
 }
 
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
-  __shared__ float2 cs[kMaxRows][64];
+// A thread's piece: 16 values of a head, the two 16-byte pieces of which are
+// c and c + rot / 16 of the head (halves) or 2 c and 2 c + 1 (neighbours, and what is
+// not turned).
+template <int D, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryArgs a) {
+  constexpr int kPerHead = D / 16;  // pairs of pieces
+  __shared__ __align__(16) float cosines[kMaxRows][D / 2], sines[kMaxRows][D / 2];
   __shared__ int place[kMaxRows];  // of each token in its sequence, or -1
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t0 = blockIdx.x * a.rows;
   const int rows = min(a.rows, a.L.total_q - t0);
   // pieces of this block: (token, head, pair of pieces), all heads of a token together; blockIdx.y takes a share
-  const int per_token = a.heads * a.per_head, n = max(rows, 0) * per_token;
+  const int per_token = a.heads * kPerHead, n = rows * per_token;
   const int per_block = (n + gridDim.y - 1) / gridDim.y;
   const int first = int(blockIdx.y) * per_block, last = min(first + per_block, n);
+  const int c = (first + tid) % kPerHead;  // (the same for all of a thread's pieces: first + tid moves by 256)
+  const bool turn = c < a.turned, idle = !turn && !a.copy_rest;
+  const int one = turn && !NEIGHBOURS ? c : 2 * c, second = turn && !NEIGHBOURS ? a.turned : 1;
 
-  uint4 va[kBatch], vb[kBatch];
-  long long to[kBatch];
-  // of piece i: its place in x and y, its pair of pieces within the head
-  auto locate = [&](int i, int& row, int& c, int& which, long long& in, long long& out, int& second) {
-    row = i / per_token;
-    const int r = i - row * per_token, h = r / a.per_head;
-    c = r - h * a.per_head;
-    which = h < a.hq ? 0 : 1;
-    const int head = which == 0 ? h : h - a.hq;
-    // pieces of the pair: half layout c and c + rot / 16, neighbours 2 c and 2 c + 1 (as the rest's)
-    const int one = c < a.turned && !a.interleaved ? c : 2 * c;
-    second = c < a.turned && !a.interleaved ? a.turned : 1;
-    const long long off = 1LL * head * (2 * a.per_head) + one;
-    in = (t0 + row) * a.xs[which] + off;
-    out = (t0 + row) * a.ys[which] + off;
-  };
   bool ready = false;
   for (int base = first; base < last || !ready; base += kItems) {
+    uint4 va[kBatch], vb[kBatch];
+    uint4* to[kBatch];
+    int row_of[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = base + k * kThreads + tid;
-      if (i >= last) continue;
-      int row, c, which, second;
-      long long in;
-      locate(i, row, c, which, in, to[k], second);
-      if (c >= a.turned && !a.copy_rest) continue;
-      const uint4* p = a.x[which] + in;
+      row_of[k] = -1;
+      if (i >= last || idle) continue;
+      const int head = i / kPerHead, row = head / a.heads, h = head - row * a.heads;
+      const int which = h < a.hq ? 0 : 1;
+      const long long off = 1LL * (which == 0 ? h : h - a.hq) * (2 * kPerHead) + one;
+      const uint4* const p = a.x[which] + ((t0 + row) * a.xs[which] + off);
+      to[k] = a.y[which] + ((t0 + row) * a.ys[which] + off);
+      row_of[k] = row;
       va[k] = __ldcs(p);
       vb[k] = __ldcs(p + second);
     }
@@ -124,51 +119,55 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
       for (int i = tid; i < rows * half; i += kThreads) {
         const int r = i / half, j = i - r * half;
         // the top 32 bits of p f's fraction of a turn, in [-1/2, 1/2) turns
-        const unsigned long long turn = turn_of(a.inv_freq[j]) * static_cast<unsigned long long>(max(place[r], 0));
+        const unsigned long long fraction = turn_of(a.inv_freq[j]) * static_cast<unsigned long long>(max(place[r], 0));
         float sn, cn;
-        sincospif(float(int(turn >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31: in half turns
-        cs[r][j] = make_float2(a.mscale * cn, a.sign * a.mscale * sn);
+        sincospif(float(int(fraction >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31: in half turns
+        cosines[r][j] = a.mscale * cn;
+        sines[r][j] = a.sign * a.mscale * sn;
       }
       __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int i = base + k * kThreads + tid;
-      if (i >= last) continue;
-      int row, c, which, second;
-      long long in, out;
-      locate(i, row, c, which, in, out, second);
-      if (place[row] < 0 || (c >= a.turned && !a.copy_rest)) continue;
-      uint4 x = va[k], y = vb[k];
-      if (c < a.turned) {
-        const float4* f = reinterpret_cast<const float4*>(&cs[row][c * 8]);  // two pairs each
-        uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-        uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+      const int row = row_of[k];
+      if (row < 0 || place[row] < 0) continue;
+      uint32_t x[4] = {va[k].x, va[k].y, va[k].z, va[k].w}, y[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
+      if (turn) {
         auto lo = [](uint32_t w) { return u2f(w << 16); };
         auto hi = [](uint32_t w) { return u2f(w & 0xffff0000u); };
-        if (!a.interleaved) {
+        const float4* const fc = reinterpret_cast<const float4*>(&cosines[row][c * 8]);
+        const float4* const fs = reinterpret_cast<const float4*>(&sines[row][c * 8]);
+        // two pairs (a, b) at a time
+        auto turned2 = [](uint64_t p, uint64_t q, float c0, float c1, float s0, float s1, float* out) {
+          const uint64_t co = pack2(c0, c1), si = pack2(s0, s1);
+          unpack2(ffma2(q, si ^ 0x8000000080000000ull, fmul2(p, co)), out[0], out[1]);
+          unpack2(ffma2(p, si, fmul2(q, co)), out[2], out[3]);
+        };
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 t = f[e];
-            const float a0 = lo(xw[e]), a1 = hi(xw[e]), b0 = lo(yw[e]), b1 = hi(yw[e]);
-            xw[e] = pack_bf16x2(a0 * t.x - b0 * t.y, a1 * t.z - b1 * t.w);
-            yw[e] = pack_bf16x2(b0 * t.x + a0 * t.y, b1 * t.z + a1 * t.w);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 t = f[e >> 1], u = f[2 + (e >> 1)];
-            const float xc = (e & 1) ? t.z : t.x, xs = (e & 1) ? t.w : t.y;
-            const float yc = (e & 1) ? u.z : u.x, ys = (e & 1) ? u.w : u.y;
-            const float a0 = lo(xw[e]), b0 = hi(xw[e]), a1 = lo(yw[e]), b1 = hi(yw[e]);
-            xw[e] = pack_bf16x2(a0 * xc - b0 * xs, b0 * xc + a0 * xs);
-            yw[e] = pack_bf16x2(a1 * yc - b1 * ys, b1 * yc + a1 * ys);
+        for (int e = 0; e < 2; ++e) {  // pairs 4 e .. 4 e + 3
+          const float4 co = fc[e], si = fs[e];
+          float r[8];
+          if constexpr (!NEIGHBOURS) {
+            const uint32_t x0 = x[2 * e], x1 = x[2 * e + 1], y0 = y[2 * e], y1 = y[2 * e + 1];
+            turned2(pack2(lo(x0), hi(x0)), pack2(lo(y0), hi(y0)), co.x, co.y, si.x, si.y, r);
+            turned2(pack2(lo(x1), hi(x1)), pack2(lo(y1), hi(y1)), co.z, co.w, si.z, si.w, r + 4);
+            x[2 * e] = pack_bf16x2(r[0], r[1]);
+            y[2 * e] = pack_bf16x2(r[2], r[3]);
+            x[2 * e + 1] = pack_bf16x2(r[4], r[5]);
+            y[2 * e + 1] = pack_bf16x2(r[6], r[7]);
+          } else {
+            uint32_t* const w = e == 0 ? x : y;
+            turned2(pack2(lo(w[0]), lo(w[1])), pack2(hi(w[0]), hi(w[1])), co.x, co.y, si.x, si.y, r);
+            turned2(pack2(lo(w[2]), lo(w[3])), pack2(hi(w[2]), hi(w[3])), co.z, co.w, si.z, si.w, r + 4);
+            w[0] = pack_bf16x2(r[0], r[2]);
+            w[1] = pack_bf16x2(r[1], r[3]);
+            w[2] = pack_bf16x2(r[4], r[6]);
+            w[3] = pack_bf16x2(r[5], r[7]);
           }
         }
       }
-      uint4* q = a.y[which] + out;
-      q[0] = x;
-      q[second] = y;
+      to[k][0] = make_uint4(x[0], x[1], x[2], x[3]);
+      to[k][second] = make_uint4(y[0], y[1], y[2], y[3]);
     }
   }
   // every wrong length is told, also where no token leads to it
@@ -201,22 +200,31 @@ cudaError_t launch_rotary(const RotaryProblem& pb, cudaStream_t stream) {
   a.L = seq::Lens{pb.cu_q, pb.lens != nullptr ? nullptr : pb.cu_q, pb.lens, pb.B, pb.total, pb.total, 0x7fffffff};
   a.heads = pb.Hq + pb.Hk;
   a.hq = pb.Hq;
-  a.per_head = pb.d / 16;
   a.turned = pb.rot / 16;
   // A block's pieces are a thread's one batch or a little less, while that
   // gives each SM several blocks; a token of very many heads is shared by
   // several blocks, and so is the only token of a call.
-  const int per_token = a.heads * a.per_head;
+  const int per_token = a.heads * (pb.d / 16);
   a.rows = std::max(1, std::min({kMaxRows, kItems / per_token, pb.total / (4 * num_sms())}));
   const long long share = 1LL * a.rows * per_token / kThreads;
   const long long blocks = (1LL * pb.total + a.rows - 1) / a.rows;
   const unsigned split = unsigned(std::max(1LL, std::min({share, 64LL, 2LL * num_sms() / std::max(1LL, blocks)})));
-  a.interleaved = pb.interleaved;
   a.mscale = pb.mscale;
   a.sign = pb.transposed ? -1.0f : 1.0f;
   a.status = status_word();
   if (a.status == nullptr) return cudaErrorLaunchFailure;
-  rotary_kernel<<<dim3(unsigned(blocks), split), kThreads, 0, stream>>>(a);
+  const dim3 grid{unsigned(blocks), split};
+  if (pb.d == 128) {
+    if (pb.interleaved) {
+      rotary_kernel<128, true><<<grid, kThreads, 0, stream>>>(a);
+    } else {
+      rotary_kernel<128, false><<<grid, kThreads, 0, stream>>>(a);
+    }
+  } else if (pb.interleaved) {
+    rotary_kernel<64, true><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    rotary_kernel<64, false><<<grid, kThreads, 0, stream>>>(a);
+  }
   return cudaGetLastError();
 }
 

@@ -1628,8 +1628,8 @@ __global__ void __launch_bounds__(256) codes_q_kernel(const __nv_bfloat16* q, lo
 #pragma unroll
   for (int e = 0; e < kBatch; ++e) {
     const int r = r0 + e * kAtOnce;
-    uint32_t m = __vmaxu2(__vmaxu2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
-                          __vmaxu2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
+    uint32_t m = max_u16x2(max_u16x2(x[e].x & 0x7fff7fffu, x[e].y & 0x7fff7fffu),
+                          max_u16x2(x[e].z & 0x7fff7fffu, x[e].w & 0x7fff7fffu));
     m = max(m & 0xffffu, m >> 16);
 #pragma unroll
     for (int d = 1; d < kLanes; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));

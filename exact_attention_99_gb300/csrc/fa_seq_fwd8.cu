@@ -481,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
         uint32_t m = 0;
 #pragma unroll
         for (int k = 0; k < KS / 2; ++k) {
-          m = __vmaxu2(m, __vmaxu2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu));
-          m = __vmaxu2(m, __vmaxu2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu));
+          m = max_u16x2(m, max_u16x2(raw[k].x & 0x7fff7fffu, raw[k].y & 0x7fff7fffu));
+          m = max_u16x2(m, max_u16x2(raw[k].z & 0x7fff7fffu, raw[k].w & 0x7fff7fffu));
         }
         m = max(m & 0xffffu, m >> 16);
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));

@@ -37,6 +37,13 @@ __device__ __forceinline__ void mma_codes_lo(uint32_t d_tmem, uint32_t a_lo, uin
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// the larger of each pair of halves, unsigned (of bf16 without its sign: the larger magnitude)
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // two e4m3 codes to f16 (which holds every e4m3 value)
 __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint16_t x) {
   uint32_t r;
@@ -68,9 +75,11 @@ __device__ __forceinline__ float f16_hi(uint32_t x) {
 
 // four bf16 values (two words) times f, to four codes
 __device__ __forceinline__ uint32_t e4m3x4_of_bf16(uint32_t x, uint32_t y, float f) {
-  const uint32_t a = e4m3x2_of(u2f(x << 16) * f, u2f(x & 0xffff0000u) * f);
-  const uint32_t b = e4m3x2_of(u2f(y << 16) * f, u2f(y & 0xffff0000u) * f);
-  return a | (b << 16);
+  const uint64_t f2 = pack2(f, f);
+  float a, b, c, d;
+  unpack2(fmul2(pack2(u2f(x << 16), u2f(x & 0xffff0000u)), f2), a, b);
+  unpack2(fmul2(pack2(u2f(y << 16), u2f(y & 0xffff0000u)), f2), c, d);
+  return uint32_t(e4m3x2_of(a, b)) | (uint32_t(e4m3x2_of(c, d)) << 16);
 }
 // four codes times f, rounded to codes again
 __device__ __forceinline__ uint32_t e4m3x4_times(uint32_t x, float f) {
