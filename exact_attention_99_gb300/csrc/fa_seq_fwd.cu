@@ -428,23 +428,32 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
       const int klen = w->klen;
       int kb = (w->kt + (key ? s : w->a[s])) * 128;  // the tile's first key
       for (int j = 0; j < n; ++j, kb += key ? 256 : 128, tile += key ? 2 : 1) {
+        // the scales of the tile's blocks, there before S is
+        const uint32_t ring = tile % kScaleTiles, use = tile / kScaleTiles;
+        // (a product of scales that underflows would make -inf * 0 of a masked score)
+        auto factor = [&](float a) { return fmaxf(a * rf, 1.1754944e-38f); };
+        float f[8], lb[8];
+        if (mine) {
+          if (!warp_wait(&ctl.codes.sc_full[ring], use & 1, &ctl.abort, LIM)) { ok = false; break; }
+          const uint32_t sc = scales_at(ctl.codes.sc[ring]);
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            const float4 t = scales_of(sc, b);
+            f[b] = factor(t.x);
+            lb[b] = t.y;
+          }
+        }
         if (!warp_wait(&ctl.s_full[s], ph_s, &ctl.abort, LIM)) { ok = false; break; }
         ph_s ^= 1;
         if (row == 0) trace_stamp(p.trace, step + j, 4 + 3 * s);
         if (mine) {
           tc_fence_after();
-          // the scales of the tile's blocks
-          const uint32_t ring = tile % kScaleTiles, use = tile / kScaleTiles;
-          if (!warp_wait(&ctl.codes.sc_full[ring], use & 1, &ctl.abort, LIM)) { ok = false; break; }
-          const uint32_t sc = scales_at(ctl.codes.sc[ring]);
           const bool edge = kb + 127 >= klen || (p.wr >= 0 && kb + 127 > stage_pos + p.wr) || (p.wl >= 0 && kb < pos_l - p.wl);
           int hi = klen - kb, lo = 0;  // columns [lo, hi) are visible
           if (p.wr >= 0) hi = min(hi, pos + p.wr + 1 - kb);
           if (p.wl >= 0) lo = max(lo, pos - p.wl - kb);
           const uint32_t span = uint32_t(max(hi - lo, 0));
           uint32_t v[128];
-          // (a product of scales that underflows would make -inf * 0 of a masked score)
-          auto factor = [&](float a) { return fmaxf(a * rf, 1.1754944e-38f); };
           float mx = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[c * 32]));
@@ -464,8 +473,7 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
               mb = fmax3(mb, u2f(z[c + 2]), u2f(z[c + 3]));
             }
             ma = fmaxf(fmax3(ma, u2f(z[14]), u2f(z[15])), mb);
-            const float4 t = scales_of(sc, b);
-            mx = fmaxf(mx, fmaf(ma, factor(t.x), t.y));
+            mx = fmaxf(mx, fmaf(ma, f[b], lb[b]));
           }
           // A maximum that passes the one held by more than kTau is rare after an item's
           // first tile. (Each row for itself, so that no row's roundings depend on its
@@ -484,9 +492,8 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
           uint32_t pk[16];
 #pragma unroll
           for (int b = 0; b < 8; ++b) {
-            const float4 t = scales_of(sc2, b);
-            const float f = factor(t.x), x = t.y + base;
-            const uint64_t f2 = pack2(f, f), x2 = pack2(x, x);
+            const float x = lb[b] + base;
+            const uint64_t f2 = pack2(f[b], f[b]), x2 = pack2(x, x);
             uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -501,9 +508,9 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
               // 2^-12 of each that is 2^-21 of the largest; the row sum keeps 32 bits
               pk[8 * (b & 1) + c] = f16x2_of(a, e);
             }
-            float la, lb;
-            unpack2(fadd2(acc0, acc1), la, lb);
-            l_run = fmaf(la + lb, t.z, l_run);
+            float la, lb2;
+            unpack2(fadd2(acc0, acc1), la, lb2);
+            l_run = fmaf(la + lb2, scales_of(sc2, b).z, l_run);
             if (b == 5) {  // the first 64 keys' P' are there: their product may begin
               tmem_wait_st();
               tc_fence_before();
