@@ -35,6 +35,9 @@
 //   that S is issued a step ahead; measured slower, 16384 causal tokens 1.15
 //   -> 1.22 ms: the two stages' softmax then run in step.)
 //
+// Over a cache of e4m3 codes (fa_fwd_paged_fp8, many rows to a kv head) the same
+// pipeline with other softmax warps and converters; see Codes below.
+//
 // What bounds it, measured:
 //   d = 128, long sequences: the tensor pipe. One causal sequence of 16384
 //     tokens, 32 query and 8 kv heads: 1.29 ms, 1710 TFLOP/s, 0.89 of the
@@ -44,6 +47,11 @@
 //     41 %. (A thread spills 12 bytes; at d = 128 none.)
 //   single tokens: the cache's bytes. 64 sequences of 300 to 32000 keys, 8 kv
 //     heads of 128: 1.70 GB in 258 us, 6.6 TB/s, 0.97 of the measured copy.
+//   codes, 3 chunks of 512 tokens over 6000 to 16384 keys, 32 query and 8 kv heads of
+//     128: 236 us (bf16 205 to 217), 1.6 us a tile of two stages, of which a stage's
+//     softmax takes 0.95 (the converters issue beside it, and 16 keys at a time have
+//     scales of their own), the products behind it 0.65; 3 us at an item's end, where
+//     the softmax warps write O.
 //   items of few tiles: 1.3 to 2.3 us between two items, most of it instruction
 //     fetch (code that runs once per item is not in the cache) and the first
 //     S; with a window and one query head per kv head the first and the last
@@ -116,6 +124,11 @@ struct Tiles {
   static constexpr int kChunks = D / 64;
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kSlots = D == 128 ? 4 : 8;
+  // Over codes the same memory is two rings, as a K tile has half as many bytes as a V
+  // tile's f16 values (one ring of slots for either, as above: 3 chunks of 512 tokens
+  // over 6000 to 16384 keys 245 us, with K's tiles further ahead 236).
+  static constexpr int kKSlots = 4, kVSlots = D == 128 ? 2 : 6, kKBytes = kTileBytes / 2, kVRing = kKSlots * kKBytes;
+  static_assert(kVRing + kVSlots * kTileBytes == kSlots * kTileBytes, "the same memory");
   static constexpr int kStgBytes = 16384;  // O staging: 4 warps x [32 rows x 64 columns] bf16
   static constexpr int kSmemDyn = (2 + kSlots) * kTileBytes + kStgBytes + 1024;
 };
@@ -147,7 +160,6 @@ struct Work {
 // sequences: 36 us either way, 3000: 81 us here, 39 us planned).
 constexpr int kFewUnits = 304, kFewRounds = 4;
 
-//
 // Over a cache of codes (kCodes) the products take K as it is: S = (Q_hi + Q_lo) K^T
 // in e4m3, where a row of Q, divided by a power of two, is the sum of two e4m3
 // values, each off by at most half a step: exact for what is 2^-9 of the row's largest
@@ -162,11 +174,15 @@ constexpr int kFewUnits = 304, kFewRounds = 4;
 // where it weighs most. P' is at most 2^(kShift + kTau) = 2^15, which f16 holds.
 constexpr float kShift = 7.0f;
 constexpr float kLow = -3.4028235e38f;  // the running maximum before any key
-constexpr int kScaleTiles = 8;  // ring of scales (a tile's are used before the tile seven on is converted)
+// Ring of scales. A tile's go out when V of the tile three before has landed, so that V of
+// kVSlots tiles before that has been taken, and with it all S up to there but one.
+constexpr int kScaleTiles = 16;
 struct Codes {
+  uint64_t k_full[kMaxSlots], k_empty[kMaxSlots];  // K's tiles; V's are the other rings' (kv_full, ...)
   uint64_t sc_full[kScaleTiles];
   float4 sc[kScaleTiles][8];       // of each block: a scale log2(e), log2(b), 1 / b
 };
+static_assert(kScaleTiles >= Tiles<128>::kVSlots + 4 && kScaleTiles >= Tiles<64>::kVSlots + 4, "see there");
 struct NoCodes {};
 
 template <Kind KIND>
@@ -247,8 +263,9 @@ __device__ __forceinline__ const Work* next_item(Ctl<KIND>& ctl, int i, uint64_t
 // by each warp once all its lanes have read the item: warp 15 may then write the next one over it
 template <Kind KIND>
 __device__ __forceinline__ void release_item(Ctl<KIND>& ctl, int i) {
+  const int lane = threadIdx.x & 31;
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
+  if (lane == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
 }
 
 // Codes: rows [32 cw, 32 cw + 32) of every V tile turned to f16; the tiles' scales.
@@ -256,7 +273,7 @@ template <int D>
 __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl, uint8_t* sKV, int cw, int lane,
                                               uint64_t LIM) {
   using C = Tiles<D>;
-  uint32_t base = 0, tiles0 = 0;
+  uint32_t tiles0 = 0;  // tiles of the items before
   bool ok = true;
   // A lane reads 16 codes of a row and writes them as two pieces of 8 values.
   // Four lanes have half a row (d = 128); the rows of neighbouring fours differ in
@@ -268,7 +285,6 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
     const Work* const w = next_item(ctl, i, LIM);
     if (w == nullptr) break;
     const int nt = w->nt, kvh = w->kvh, kt = w->kt, klen = w->klen, fill = w->fill;
-    const bool key = (w->flags & kKeyMode) != 0;
     const int seen = p.wl >= 0 ? w->pos - p.wl : 0;  // the first key that a row of the item sees
     const int* const row_of_table = p.table + size_t(w->kbase) * p.max_pages;
     // row of the scales of block 2 cw + lane of tile t, or -1: not used
@@ -290,30 +306,22 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
     int page0 = look_up(0);
     int page1 = look_up(1);
     float2 next = read(0, page0);
-    const int d = min(key ? 2 : 1, nt);
+    int published = 0;  // tiles whose scales are out
 #pragma unroll 1
-    for (int x = 0; x < 2 * nt; ++x) {
-      // the ring's entries: K(0..d-1), then V(t), K(t + d) in turn, then the last V
-      const int y = x - d;
-      const bool is_v = y >= 0 && (y >= 2 * (nt - d) || (y & 1) == 0);
-      const int t = y < 0 ? x : y >= 2 * (nt - d) ? y - (nt - d) : (y >> 1) + ((y & 1) ? d : 0);
-      const uint32_t entry = base + uint32_t(x), slot = entry % C::kSlots;
-      if (!is_v) {
-        if (lane < 2)
-          ctl.codes.sc[(tiles0 + t) % kScaleTiles][2 * cw + lane] =
-              make_float4(next.x * p.scale_log2, __log2f(next.y), __fdividef(1.0f, next.y), 0.0f);
+    for (int t = 0; t < nt; ++t) {
+      // S runs up to two tiles ahead of V
+      for (; published < min(nt, t + 3); ++published) {
+        float4* const sc = ctl.codes.sc[(tiles0 + published) % kScaleTiles];
+        if (lane < 2) sc[2 * cw + lane] = make_float4(next.x * p.scale_log2, __log2f(next.y), __fdividef(1.0f, next.y), 0.0f);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.codes.sc_full[(tiles0 + t) % kScaleTiles]);
-        next = read(t + 1, page1);
-        page1 = look_up(t + 2);
+        if (lane == 0) mbar_arrive(&ctl.codes.sc_full[(tiles0 + published) % kScaleTiles]);
+        next = read(published + 1, page1);
+        page1 = look_up(published + 2);
       }
-      // (K's tiles too, whose codes stay: a phase that is not waited for might still be
-      // open at the next wait for the slot, which would then return at once)
-      ok = warp_wait(&ctl.kv_full[slot], (entry / C::kSlots) & 1, &ctl.abort, LIM);
+      const uint32_t slot = (tiles0 + t) % C::kVSlots;
+      ok = warp_wait(&ctl.kv_full[slot], ((tiles0 + t) / C::kVSlots) & 1, &ctl.abort, LIM);
       if (!ok) break;
-      if (!is_v) continue;
-      if (threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 14);
-      uint8_t* const tile = sKV + slot * C::kTileBytes;
+      uint8_t* const tile = sKV + C::kVRing + slot * C::kTileBytes;
       uint8_t* const mine = tile + cw * 4096;
       constexpr int kHalves = D / 64;
       uint4 c[4][kHalves];
@@ -351,7 +359,6 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
       if (threadIdx.x == 256) trace_stamp(p.trace, int(tiles0) + t, 15);
       if (lane == 0) mbar_arrive(&ctl.tail_done[slot]);
     }
-    base += uint32_t(2 * nt);
     tiles0 += uint32_t(nt);
     if (ok) release_item(ctl, i);
   }
@@ -689,6 +696,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl.tail_done[i], CODES ? 4 : 1);
     }
     if constexpr (CODES) {
+      for (int i = 0; i < C::kKSlots; ++i) {
+        mbar_init(&ctl.codes.k_full[i], 1);
+        mbar_init(&ctl.codes.k_empty[i], 1);
+      }
       for (int i = 0; i < kScaleTiles; ++i) mbar_init(&ctl.codes.sc_full[i], 4);
     }
     fence_mbar_init();
@@ -1106,13 +1117,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int d = min(key ? 2 : 1, nt);
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
-        const uint32_t entry = base + uint32_t(is_v ? (t < nt - d ? d + 2 * t : nt + t) : (t < d ? t : 2 * t - d + 1));
-        const uint32_t slot = entry % C::kSlots, use = entry / C::kSlots;
-        uint8_t* dst = sKV + slot * C::kTileBytes;
+        const uint32_t entry =
+            CODES ? base + uint32_t(t) : base + uint32_t(is_v ? (t < nt - d ? d + 2 * t : nt + t) : (t < d ? t : 2 * t - d + 1));
+        const uint32_t slots = !CODES ? C::kSlots : is_v ? C::kVSlots : C::kKSlots, slot = entry % slots, use = entry / slots;
+        uint8_t* dst = sKV + (!CODES ? slot * C::kTileBytes : is_v ? C::kVRing + slot * C::kTileBytes : slot * C::kKBytes);
+        uint64_t *full = &ctl.kv_full[slot], *empty = &ctl.kv_empty[slot];
+        if constexpr (CODES) {
+          if (!is_v) {
+            full = &ctl.codes.k_full[slot];
+            empty = &ctl.codes.k_empty[slot];
+          }
+        }
         // (The warp's entry before this one is at most 3 back: what it waited
         // for has been taken, and all before it, so that this wait is for the
         // slot's last use and no earlier one.)
-        ok = warp_wait(&ctl.kv_empty[slot], (use & 1) ^ 1, abort_flag, LIM);
+        ok = warp_wait(empty, (use & 1) ^ 1, abort_flag, LIM);
         if (!ok) break;
         if (p.inject == 1 && !is_v && !injected) {  // test hook: never deliver this tile
           injected = true;
@@ -1138,13 +1157,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (CODES) {
             if (elect_one()) {
-              mbar_arrive_expect_tx(&ctl.kv_full[slot], uint32_t(at.boxes * p.box_rows * D));
+              mbar_arrive_expect_tx(full, uint32_t(at.boxes * p.box_rows * D));
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
                 if (x >= at.boxes) break;
                 // K's rows of codes follow one another, 32 of V's stand where those of 64 values will
                 const int r = x * p.box_rows;
-                tma_load_4d_hint(dst + (is_v ? (r >> 5) * 4096 + (r & 31) * D : r * D), m, &ctl.kv_full[slot], 0, kvh,
+                tma_load_4d_hint(dst + (is_v ? (r >> 5) * 4096 + (r & 31) * D : r * D), m, full, 0, kvh,
                                  in_page[x], page[x], pol_kv);
               }
             }
@@ -1182,7 +1201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&ctl.tail_done[slot]);
         }
       }
-      base += uint32_t(2 * nt);
+      base += uint32_t(CODES ? nt : 2 * nt);
       release(i);
     }
   } else if (warp == 13) {
@@ -1194,11 +1213,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idS = (CODES ? idesc_codes_f32(128, 128) : idesc_bf16_f32(128, 128, 0, 0)) | (p.neg_s << 13);
       constexpr uint32_t idPV = CODES ? idesc_f16_f32(128, D, 0, 1) : idesc_bf16_f32(128, D, 0, 1);
       const uint32_t dq = sdesc_lo(smem_u32(sQ), 16), dk = sdesc_lo(smem_u32(sKV), 16),
-                     dv = sdesc_lo(smem_u32(sKV), 16384);
+                     dv = sdesc_lo(smem_u32(sKV) + (CODES ? C::kVRing : 0), 16384);
       // Phases of the barriers of each stage (or slot), a bit each: arrays
       // indexed by the stage would be kept in memory.
       uint32_t phases = 0, tail_phases = 0;
-      uint32_t E = 0, key_items = 0;  // ring entry that follows
+      uint32_t E = 0, EK = 0, key_items = 0;  // ring entry that follows (over codes V's, K's)
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
         return warp_wait(bar, phase, abort_flag, LIM);
@@ -1213,10 +1232,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // the next ring entry, loaded
       auto wait_kv = [&](uint32_t& slot) -> bool {
-        slot = E % C::kSlots;
-        const uint32_t phase = (E / C::kSlots) & 1;
+        constexpr int kSlots = CODES ? C::kVSlots : C::kSlots;
+        slot = E % kSlots;
+        const uint32_t phase = (E / kSlots) & 1;
         ++E;
         return wait(&ctl.kv_full[slot], phase);
+      };
+      // the next K tile of codes
+      auto wait_k = [&](uint32_t& slot) -> bool {
+        if constexpr (CODES) {
+          slot = EK % C::kKSlots;
+          const uint32_t phase = (EK / C::kKSlots) & 1;
+          ++EK;
+          return wait(&ctl.codes.k_full[slot], phase);
+        } else {
+          return wait_kv(slot);
+        }
+      };
+      auto k_empty = [&](uint32_t slot) -> uint64_t* {
+        if constexpr (CODES) {
+          return &ctl.codes.k_empty[slot];
+        } else {
+          return &ctl.kv_empty[slot];
+        }
       };
       // rows of a V tile past the sequence's end zeroed
       auto wait_tail = [&](uint32_t slot) -> bool {
@@ -1253,7 +1291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_s = [&](int s, uint32_t b, uint32_t slot) {
         tc_fence_after();
         if (!elect_one()) return;
-        const uint32_t q0 = sdesc_step(dq, b * C::kTileBytes), b0 = sdesc_step(dk, slot * C::kTileBytes);
+        const uint32_t q0 = sdesc_step(dq, b * C::kTileBytes), b0 = sdesc_step(dk, slot * (CODES ? C::kKBytes : C::kTileBytes));
         if constexpr (CODES) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // 32 of d at a time, Q's high and then its low parts
@@ -1298,10 +1336,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               commit(&ctl.kv_empty[slot]);
             }
             if (t + 2 < nt) {
-              ok = wait_kv(slot);
+              ok = wait_k(slot);
               if (!ok) break;
               issue_s(s, b, slot);
-              commit(&ctl.kv_empty[slot]);
+              commit(k_empty(slot));
               if (t + 3 == nt) commit(&ctl.q_empty[b]);
             }
           }
@@ -1329,7 +1367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (k) {
-              ok = wait_kv(ks);
+              ok = wait_k(ks);
               if (!ok) break;
               if (u0 + 1 < uint32_t(n0)) {
                 issue_s(0, 0, ks);
@@ -1349,7 +1387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_s(1, 1, ks);
                 if (u1 + 2 == uint32_t(n1)) commit(&ctl.q_empty[1]);
               }
-              commit(&ctl.kv_empty[ks]);
+              commit(k_empty(ks));
             }
             if (v) trace(p.trace, step0 + t, 3);
           }
