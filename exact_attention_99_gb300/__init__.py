@@ -785,10 +785,10 @@ def _turn(q, k, inv_freq, cu, lens, interleaved, mscale, out, stream, transposed
         _ints("lens", lens, (n[0] - 1,), device)
     s = _here(device, stream)
     if s is not None:
-        return _rotary(s, q, k, inv_freq, cu, lens, out, hq, hk, total, d, qs, ks, mscale, 1 if interleaved else 0,
+        return _rotary(s, q, k, inv_freq, cu, lens, out, hq, hk, total, d, qs, ks, float(mscale), 1 if interleaved else 0,
                        transposed)
     with _on(device, stream):
-        return _rotary(_current_stream(), q, k, inv_freq, cu, lens, out, hq, hk, total, d, qs, ks, mscale,
+        return _rotary(_current_stream(), q, k, inv_freq, cu, lens, out, hq, hk, total, d, qs, ks, float(mscale),
                        1 if interleaved else 0, transposed)
 
 

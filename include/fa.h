@@ -339,8 +339,8 @@ int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, 
  * fa_fwd_paged's, and k_scales and v_scales [num_pages, page_size / 16, Hkv]
  * (fp32) a scale for each block of 16 tokens and head: row r of a page stands
  * for scale[page][r / 16][head] * code[page][r][head][...]. A scale that is used
- * must be positive and finite. Conventions, limits and errors are those of the
- * bf16 calls; scales are aligned to 4 bytes.
+ * must lie between 2^-126 and 2^126. Conventions, limits and errors are those of
+ * the bf16 calls; scales are aligned to 4 bytes.
  */
 
 /*
@@ -363,10 +363,17 @@ int fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pag
 
 /*
  * fa_fwd_paged_fp8 — fa_fwd_paged over such a cache: the attention of the
- *   values that it stands for (nothing of them is rounded; P is rounded to 11
- *   bits). Rows past a sequence's end are not used, whatever their codes; their
- *   block's scale is that of the rows before them. Workspace: from the pool, 20
- *   MB at most.
+ *   values that it stands for. Of those nothing is rounded; P is rounded to f16
+ *   (11 bits), and q to f16 after a division by a power of two of its row where
+ *   the batch's sequences have few rows (new tokens * query heads of a group: 16
+ *   or fewer on the mean, 2^16 in all), to the sum of two e4m3 values where
+ *   they have many: exact for what is 2^-9 of the row's largest value or more,
+ *   off by at most 2^-17 of that below. A row of q that is not finite gives NaN.
+ *   Rows past a sequence's end are not used, whatever their codes; their block's
+ *   scale is that of the rows before them. A row's result does not depend on what
+ *   else is in the call but for how its keys are divided (the order of fp32 sums).
+ *   Workspace, from the pool: few rows, 5 MB; many, as fa_fwd_paged and
+ *   (2 * d + 4) * total_q * Hq bytes for q.
  */
 int fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
                      const float* v_scales, void* o, float* lse, const int* cu_q, const int* lens_k,
