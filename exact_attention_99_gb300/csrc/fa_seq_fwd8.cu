@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
     if (before <= target && target < upto * p.Hkv) {
 #pragma unroll 1
       for (int b = b0; b < b1; ++b) {
-        const long long t = cost_of(b, fine);
+        const long long t = per == 1 ? mine : cost_of(b, fine);
         if (target < before + t * p.Hkv) {
           ctl.start.b = b;
           ctl.start.before = before;
@@ -399,22 +399,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
       }
     };
     const uint64_t pol = l2_policy_evict_first();
-    Tile a = next_tile();
-    Tile b = next_tile();
-    read_scale(a);
     bool injected = false;
-    for (int n = 0; a.key >= 0 && ok; ++n) {
-      Tile c = next_tile();
-      read_scale(b);
-      const int slot = n % S;
-      ok = ok && seq::warp_wait(&ctl.empty[slot], ((n / S) & 1) ^ 1, &ctl.abort, LIM);
-      if (!ok) break;
-      if (lane < 16) ctl.sc[slot][lane >> 3][lane & 7] = a.scale;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.full[slot]);
-      const int kb = a.key + lane * p.box_rows;
-      const bool wanted = lane < n_box && kb < a.k1 && kb + p.box_rows > a.k0;
-      int page = a.page;
+    auto load = [&](const Tile& t, int slot) {
+      const int kb = t.key + lane * p.box_rows;
+      const bool wanted = lane < n_box && kb < t.k1 && kb + p.box_rows > t.k0;
+      int page = t.page;
       if (wanted && (page < 0 || page >= p.num_pages)) {  // no such page: it reads as zeros, and the caller is told
         atomicOr(p.status, kDevBadArg);
         page = p.num_pages;
@@ -423,19 +412,43 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
       const int in_page = kb % p.page_size;
       if (p.inject == 1 && !injected) {  // test hook: never deliver this tile
         injected = true;
-      } else {
-        uint8_t* const dst = ring + slot * 2 * C::kHalf;
-        if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], uint32_t(2 * __popc(boxes) * p.box_rows * D));
-        for (unsigned left = boxes; left != 0; left &= left - 1) {
-          const int x = __ffs(left) - 1;
-          const int pg = __shfl_sync(0xffffffffu, page, x), at = __shfl_sync(0xffffffffu, in_page, x);
-          if (elect_one()) {
-            tma_load_4d_hint(dst + x * p.box_rows * D, &tmK, &ctl.full[slot], 0, a.head, at, pg, pol);
-            tma_load_4d_hint(dst + C::kHalf + x * p.box_rows * D, &tmV, &ctl.full[slot], 0, a.head, at, pg, pol);
-          }
-          __syncwarp();
-        }
+        return;
       }
+      uint8_t* const dst = ring + slot * 2 * C::kHalf;
+      if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], uint32_t(2 * __popc(boxes) * p.box_rows * D));
+      for (unsigned left = boxes; left != 0; left &= left - 1) {
+        const int x = __ffs(left) - 1;
+        const int pg = __shfl_sync(0xffffffffu, page, x), at = __shfl_sync(0xffffffffu, in_page, x);
+        if (elect_one()) {
+          tma_load_4d_hint(dst + x * p.box_rows * D, &tmK, &ctl.full[slot], 0, t.head, at, pg, pol);
+          tma_load_4d_hint(dst + C::kHalf + x * p.box_rows * D, &tmV, &ctl.full[slot], 0, t.head, at, pg, pol);
+        }
+        __syncwarp();
+      }
+    };
+    auto hand_out_scale = [&](const Tile& t, int slot) {
+      if (lane < 16) ctl.sc[slot][lane >> 3][lane & 7] = t.scale;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.full[slot]);
+    };
+    Tile a = next_tile(), b;
+    b.key = -1;
+    if (a.key >= 0 && ok) {  // the first is loaded before anything else is looked at: a short call is a chain of reads
+      load(a, 0);
+      read_scale(a);
+      hand_out_scale(a, 0);
+      a = next_tile();
+      b = next_tile();
+      read_scale(a);
+    }
+    for (int n = 1; a.key >= 0 && ok; ++n) {
+      const Tile c = next_tile();
+      read_scale(b);
+      const int slot = n % S;
+      ok = ok && seq::warp_wait(&ctl.empty[slot], ((n / S) & 1) ^ 1, &ctl.abort, LIM);
+      if (!ok) break;
+      hand_out_scale(a, slot);
+      load(a, slot);
       a = b;
       b = c;
     }
@@ -720,7 +733,11 @@ __global__ void __launch_bounds__(R * 32) join8_kernel(const Params8 p) {
   for (int c0 = k.c0; c0 <= k.c1; c0 += 32) {
     const int c = c0 + lane;
     float2 t = make_float2(kLow, 0.0f);
-    if (c <= k.c1 && p.has[c]) t = p.part_ml[size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * R + r];
+    if (c <= k.c1) {  // (a worker without a share has no part: what its slot holds is not used)
+      const int has = p.has[c];
+      const float2 x = p.part_ml[size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * R + r];
+      if (has) t = x;
+    }
     float mn = fmaxf(m, t.x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
