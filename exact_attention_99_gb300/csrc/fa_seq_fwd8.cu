@@ -721,54 +721,68 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
 }
 
 // The parts of the units that several workers share: O = sum_i 2^(m_i - m) O_i /
-// sum_i 2^(m_i - m) l_i, in the workers' order; a warp per row.
+// sum_i 2^(m_i - m) l_i. A block to a unit, 32 warps: several to a row, each of
+// which takes every W-th part (one after the other, 19 parts took 5 us), summed
+// in the warps' order.
 template <int D, int R>
-__global__ void __launch_bounds__(R * 32) join8_kernel(const Params8 p) {
+__global__ void __launch_bounds__(1024) join8_kernel(const Params8 p) {
+  constexpr int W = 32 / R;  // warps of a row
+  constexpr int V = D / 32;  // columns of a lane
+  __shared__ float so[32][D];
   grid_dep_wait();
   const Cut8 k = p.cuts[blockIdx.x];
-  const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (k.c1 < 0 || r >= k.rows) return;
-  constexpr int V = D / 32;
+  if (k.c1 < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = warp / W, w = warp % W;
   float m = kLow, l = 0.0f, o[V] = {};
-  for (int c0 = k.c0; c0 <= k.c1; c0 += 32) {
-    const int c = c0 + lane;
-    float2 t = make_float2(kLow, 0.0f);
-    if (c <= k.c1) {  // (a worker without a share has no part: what its slot holds is not used)
-      const int has = p.has[c];
-      const float2 x = p.part_ml[size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * R + r];
-      if (has) t = x;
-    }
-    float mn = fmaxf(m, t.x);
+  if (r < k.rows) {
+    for (int c0 = k.c0; c0 <= k.c1; c0 += 32) {  // 32 parts at a time; all their (m, l) by each warp
+      const int c = c0 + lane;
+      float2 t = make_float2(kLow, 0.0f);
+      if (c <= k.c1) {  // (a worker without a share has no part: what its slot holds is not used)
+        const int has = p.has[c];
+        const float2 x = p.part_ml[size_t(c == k.c0 ? 2 * c + 1 : 2 * c) * R + r];
+        if (has) t = x;
+      }
+      float mn = fmaxf(m, t.x);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-    const float wa = ex2_mufu(m - mn), wb = ex2_mufu(t.x - mn);
-    float ls = t.y * wb;
+      for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+      const float wa = ex2_mufu(m - mn), wb = ex2_mufu(t.x - mn);
+      float ls = t.y * wb;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-    l = l * wa + ls;
-    m = mn;
+      for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+      l = l * wa + ls;
+      m = mn;
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] *= wa;
-    const int n = min(32, k.c1 - c0 + 1);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, wb, i), li = __shfl_sync(0xffffffffu, t.y, i);
-      if (li == 0.0f) continue;  // no part, or no key of it visible to the row
-      const int ci = c0 + i;
-      const float* src = p.part_o + (size_t(ci == k.c0 ? 2 * ci + 1 : 2 * ci) * R + r) * D + lane * V;
-      if constexpr (V == 4) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        o[0] = fmaf(y.x, wi, o[0]);
-        o[1] = fmaf(y.y, wi, o[1]);
-        o[2] = fmaf(y.z, wi, o[2]);
-        o[3] = fmaf(y.w, wi, o[3]);
-      } else {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        o[0] = fmaf(y.x, wi, o[0]);
-        o[1] = fmaf(y.y, wi, o[1]);
+      for (int e = 0; e < V; ++e) o[e] *= wa;
+      const int n = min(32, k.c1 - c0 + 1);
+#pragma unroll 8
+      for (int i = w; i < n; i += W) {
+        const float wi = __shfl_sync(0xffffffffu, wb, i), li = __shfl_sync(0xffffffffu, t.y, i);
+        if (li == 0.0f) continue;  // no part, or no key of it visible to the row
+        const int ci = c0 + i;
+        const float* src = p.part_o + (size_t(ci == k.c0 ? 2 * ci + 1 : 2 * ci) * R + r) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src);
+          o[0] = fmaf(y.x, wi, o[0]);
+          o[1] = fmaf(y.y, wi, o[1]);
+          o[2] = fmaf(y.z, wi, o[2]);
+          o[3] = fmaf(y.w, wi, o[3]);
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(src);
+          o[0] = fmaf(y.x, wi, o[0]);
+          o[1] = fmaf(y.y, wi, o[1]);
+        }
       }
     }
   }
+#pragma unroll
+  for (int e = 0; e < V; ++e) so[warp][lane * V + e] = o[e];
+  __syncthreads();
+  if (w != 0 || r >= k.rows) return;
+#pragma unroll
+  for (int x = 1; x < W; ++x)
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] += so[warp + x][lane * V + e];
   const int row = k.row0 + r, tok = row / p.group, hd = k.kvh * p.group + row - tok * p.group;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   __nv_bfloat16* dst = p.o + (size_t(k.seq0 + tok) * p.Hq + hd) * D + lane * V;
@@ -841,7 +855,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(G);
-    lc.blockDim = dim3(C::kRows * 32);
+    lc.blockDim = dim3(1024);
     lc.stream = stream;
     lc.attrs = pdl;
     lc.numAttrs = 1;
