@@ -47,12 +47,16 @@ KERNEL_SOURCES = {"fa_fwd_kernel": ("fa_fwd.cu", "fa_fwd_pipeline.cuh"),
                   "bwd_main_kernel": ("fa_bwd.cu", "fa_bwd_layout.h"),
                   "fa_fwd8_kernel": ("fa_fwd8.cu", "fa_fwd_pipeline.cuh"),
                   "fa_fwd_pair_kernel": ("fa_fwd.cu", "fa_fwd_pipeline.cuh"),
-                  "seq_fwd_kernel": ("fa_seq_fwd.cu", "fa_seq_plan.cuh", "fa_seq.cuh"),
+                  "seq_fwd_kernel": ("fa_seq_fwd.cu", "fa_seq_plan.cuh", "fa_seq.cuh", "sm103_fp8.cuh"),
+                  "attend8_kernel": ("fa_seq_fwd8.cu", "fa_seq.cuh", "sm103_fp8.cuh"),
                   "seq_bwd_kernel": ("fa_seq_bwd.cu", "fa_seq_plan.cuh", "fa_seq.cuh", "fa_bwd_layout.h")}
 # profiling targets of the packed calls: causal sequences one behind the other
 PACKED_CASES = {"packed_causal_b1_hq32_hkv8_n16384_d128": dict(lens=[16384], Hq=32, Hkv=8, d=128, seed=1050),
                 "packed_causal_b1_hq32_hkv8_n16384_d64": dict(lens=[16384], Hq=32, Hkv=8, d=64, seed=1051),
                 "packed_causal_b2_hq32_hkv8_n4096_d128": dict(lens=[4096, 4096], Hq=32, Hkv=8, d=128, seed=1052)}
+# and of the attention over an 8-bit cache: the last `new` of each sequence's tokens are queries
+CODES_CASES = {"codes_single_b16_hq32_hkv8_n8192_d128": dict(B=16, new=1, n=8192, Hq=32, Hkv=8, d=128, page=64, seed=1060),
+               "codes_chunk512_b1_hq32_hkv8_n16384_d128": dict(B=1, new=512, n=16384, Hq=32, Hkv=8, d=128, page=64, seed=1061)}
 PANEL = 1024  # query rows of one oracle sample
 
 
@@ -761,6 +765,8 @@ def run_profile_target(args):
         raise ValueError("bad --exp2-split")
     if args.profile_workload in PACKED_CASES:
         return run_packed_profile_target(fa, args, PACKED_CASES[args.profile_workload])
+    if args.profile_workload in CODES_CASES:
+        return run_codes_profile_target(fa, args, CODES_CASES[args.profile_workload])
     if args.profile_workload == WINDOW_CASE["name"]:
         c = WINDOW_CASE
         x = workloads.make_inputs(c["B"], c["H"], c["H"], c["N"], c["N"], c["d"], c["seed"], with_dout=True)
@@ -806,6 +812,28 @@ def run_packed_profile_target(fa, args, c):
             fa.forward_varlen(q, k, v, cu, cu, causal=True, out=(o, lse))
         else:
             fa.backward_varlen(q, k, v, o, lse, do, cu, cu, causal=True)
+    torch.cuda.synchronize()
+    if fa.fa_get_status() != 0:
+        raise RuntimeError("device status not OK")
+
+
+def run_codes_profile_target(fa, args, c):
+    """run_profile_target for a case of the attention over an 8-bit cache."""
+    import torch
+    if args.profile_pass != "fwd":
+        raise ValueError("the 8-bit cache has a forward only")
+    B, n, hk, d, page = c["B"], c["n"], c["Hkv"], c["d"], c["page"]
+    x = workloads.make_inputs(1, c["Hq"], hk, B * c["new"], B * n, d, c["seed"], with_dout=False)
+    q, k, v = (x[name][0].cuda() for name in ("q", "k", "v"))
+    pages = [torch.zeros((B * n // page, page, hk, d), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+    pages += [torch.zeros((B * n // page, page // 16, hk), device="cuda") for _ in range(2)]
+    g = torch.Generator(device="cpu").manual_seed(c["seed"])
+    table = torch.randperm(B * n // page, generator=g).to(torch.int32).view(B, -1).cuda()
+    i = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    fa.cache_append_fp8(k, v, *pages, i * n, lens, table)
+    for _ in range(args.warmup + args.steps):
+        fa.forward_paged_fp8(q, *pages, i * c["new"], lens, table)
     torch.cuda.synchronize()
     if fa.fa_get_status() != 0:
         raise RuntimeError("device status not OK")
