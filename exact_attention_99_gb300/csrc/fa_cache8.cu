@@ -9,7 +9,9 @@
 // of two further, which a floating type does not need: its relative error is
 // the same over all its normal values.)
 //
-// Each value is read once (2 bytes) and written once (1 byte), so memory bound.
+// Each value is read once (2 bytes) and written once (1 byte), so memory bound:
+// 51000 tokens of 8 heads of 128 in prompts take 53 us, 5.9 TB/s (the measured copy
+// 6.8); 100 single tokens 4.2 us, the launch and a chain of four loads.
 // The first new token of a block speaks for it: a warp takes the block's new
 // rows of one head of K or V, all 16 rows' loads in flight, finds their largest
 // magnitude by packed 16-bit integer maxima (of bf16's bits without the sign),

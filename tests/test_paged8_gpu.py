@@ -86,6 +86,19 @@ def test_many_items_per_cta(fa, hq, hk, d):
     run(fa, new, keys, hq, hk, d, 16, seed=hq)
 
 
+@pytest.mark.parametrize("window", [None, (70, 0)])
+@pytest.mark.parametrize("hq,hk,d", [(8, 1, 64), (8, 2, 128)])
+def test_more_units_than_a_cta_plans_for_itself(fa, hq, hk, d, window):
+    g = torch.Generator().manual_seed(d)
+    new = torch.randint(0, 21, (400,), generator=g).tolist()
+    keys = [n + int(m) for n, m in zip(new, torch.randint(0, 300, (400,), generator=g))]
+    run(fa, new, keys, hq, hk, d, 32, seed=d, window=window)
+
+
+def test_long_prompt(fa):
+    run(fa, [3100, 700], [3100, 2000], 2, 1, 64, 64, seed=3)
+
+
 @pytest.mark.parametrize("causal,window", [(True, (100, 0)), (False, (40, 7)), (False, None), (True, (0, 0))])
 @pytest.mark.parametrize("d", [64, 128])
 def test_masks(fa, causal, window, d):
@@ -108,12 +121,13 @@ def test_values_of_very_different_blocks(fa):
     run(fa, [1, 40], [1500, 700], 4, 2, 128, 16, seed=16, sigma=(1e-6, 1.0, 1e5, 1e-3))
 
 
+@pytest.mark.parametrize("new", [[1, 3], [1, 20]])
 @pytest.mark.parametrize("size", [1e-30, 1e-4, 300.0, 1e20])
-def test_queries_of_any_size(fa, size):
+def test_queries_of_any_size(fa, size, new):
     def edit(w):
         w *= size
         w[0, 0] = 0.0
-    run(fa, [1, 20], [300, 200], 4, 2, 64, 16, seed=17, scale=0.1 / size, q_edit=edit)
+    run(fa, new, [300, 200], 4, 2, 64, 16, seed=17, scale=0.1 / size, q_edit=edit)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
@@ -226,10 +240,10 @@ def test_bad_page_reads_as_zeros(fa):
     cu8.check_forward(o, lse, su.reference(seqs, 0.125, True), seqs, su.starts([1]))
 
 
-def test_repeatable(fa):
-    c = cu8.filled([5000, 77, 900], 2, 128, 16, seed=24)
+@pytest.mark.parametrize("new,keys", [([1, 30, 200], [5000, 77, 900]), ([1, 1, 2], [5000, 77, 900]), ([30] * 300, [200] * 300)])
+def test_repeatable(fa, new, keys):
+    c = cu8.filled(keys, 2, 128, 16, seed=24)
     pages, table = c.cuda()
-    new = [1, 30, 200]
     q = su.normal((sum(new), 8, 128), su.gen(24)).cuda()
     args = (q, *pages, su.starts(new).cuda(), c.lens_k().cuda(), table)
     o, lse = fa.forward_paged_fp8(*args)
