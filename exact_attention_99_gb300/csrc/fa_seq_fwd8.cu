@@ -29,10 +29,11 @@
 // joined by a last kernel, in a fixed order.
 //
 // Measured (the same calls over a bf16 cache in brackets):
-//   64 single tokens over 300 to 32000 keys, 8 kv heads of 128: 0.89 GB in 154 us, 5.8
-//     TB/s (268 us); two tokens over 116000 and 131000 keys: 92 us (153). A further key
-//     costs its bytes at 6.7 TB/s; the rest, 13 to 15 us, is the launch, the CTA's plan
-//     (1.6 us), the first lookups (1.5 us), the first tile and the joins.
+//   64 single tokens over 300 to 32000 keys, 8 kv heads of 128: 0.89 GB in 154 to 160 us
+//     (by the GPU), 5.8 TB/s (268 us); two tokens over 116000 and 131000 keys: 92 to 98
+//     us (153). A further key costs its bytes at 6.7 TB/s; the rest, 13 to 15 us, is the
+//     launch, the CTA's plan (1.6 us), the first lookups (1.5 us), the first tile and the
+//     joins.
 //   one token over 1000 keys: 12.1 us (13.3), that chain alone.
 //   Tried, the 64 tokens (159 us when the first three of these were measured): loads by
 //     cp.async, 16 warps a CTA 213 us, four CTAs of 4 warps 194; TMA with 256-byte
@@ -880,13 +881,19 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
 }  // namespace seq8
 
 cudaError_t launch_seq_fwd8(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream) {
-  // Few rows or many: by the mean sequence's, as the lengths are on the device. 64
-  // sequences of 2000 to 8000 keys, 8 kv heads of 128: up to 8 rows 107 us, 16 rows 148
-  // us, 24 rows 278 us here, 191 us whatever the rows there (of 64: 86, 136, 258 and
-  // 141). A batch with one long sequence among empty ones is slower here than there by
-  // as much as its rows pass 16, so this is for 2^16 rows at most.
+  // Few rows or many: by the mean sequence's, as the lengths are on the device.
+  //   Up to 8 rows: here. 64 sequences of 2000 to 8000 keys, 8 kv heads of 128: 107 us,
+  //     191 us there (d = 64: 86, 141); also where half of the rows are one sequence's (64
+  //     of 8000 keys: 259 us, 296). Over 2^16 rows such a sequence could be long.
+  //   9 to 16 rows: single tokens of wide groups here (the 64 sequences: 173 us, 185
+  //     there) and small batches (4 tokens of a group of 4 over 1000 keys: 13.4 us, 17.1;
+  //     4 sequences of them over 8000: 30, 32); others may be single tokens and a prompt,
+  //     whose keys are read anew for each 16 rows: 31 single tokens and 96, over 8000: 224
+  //     us, 174 there; 255 and a chunk of 512, over 2000 to 8000 keys: 1133 us, 728 there.
+  //   More: there (24 rows of the 64 sequences: 278 us here, 191 there).
   const long long all = 1LL * pb.total_q * (pb.Hq / pb.Hkv), rows = (all + pb.B - 1) / pb.B;
-  if (rows > 16 || all > (1 << 16)) return launch_seq_fwd_codes(pb, sc, o, lse, stream);
+  const bool few = rows <= 8 || (rows <= 16 && (pb.total_q <= pb.B || all <= 64));
+  if (!few || all > (1 << 16)) return launch_seq_fwd_codes(pb, sc, o, lse, stream);
   if (pb.d == 128)
     return rows <= 8 ? seq8::launch_t<128, 1>(pb, sc, o, lse, stream) : seq8::launch_t<128, 2>(pb, sc, o, lse, stream);
   return rows <= 8 ? seq8::launch_t<64, 1>(pb, sc, o, lse, stream) : seq8::launch_t<64, 2>(pb, sc, o, lse, stream);

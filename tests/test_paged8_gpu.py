@@ -63,6 +63,14 @@ def test_chunks(fa, new, d):
     run(fa, [new], [new + 200], 4, 1, d, 16, seed=new)
 
 
+@pytest.mark.parametrize("window", [None, (5, 0), (300, 2)])
+@pytest.mark.parametrize("new,keys", [([4, 1, 3], [300, 2000, 77]), ([10, 1, 1], [12, 900, 3000]), ([16], [4000]),
+                                      ([0, 9, 0, 3, 1], [50, 700, 0, 1500, 1])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_tokens_of_few_sequences(fa, new, keys, d, window):
+    run(fa, new, keys, 8, 2, d, 32, window=window, seed=len(new))
+
+
 @pytest.mark.parametrize("new", [[200, 260], [128, 64], [513]])
 def test_prompts_of_their_own(fa, new):
     # every key is new
