@@ -717,7 +717,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  grid_dep_wait();    // the plan
+  // The plan; of codes also Q's parts, for which only Q's producer and the softmax warps
+  // (their rows' factors) wait where there is no plan: the lengths are a caller's, there
+  // before the kernel that makes the parts began.
+  if (!CODES || p.items != nullptr || wg <= 1 || warp == 12) grid_dep_wait();
   grid_dep_launch();  // the joining kernel may start (and wait) meanwhile
   const uint32_t tmem = ctl.tmem_base;
   auto item = [&](int i) { return next_item(ctl, i, LIM); };
