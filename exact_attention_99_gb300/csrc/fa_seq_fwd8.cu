@@ -29,8 +29,8 @@
 // joined by a last kernel, in a fixed order.
 //
 // Measured (the same calls over a bf16 cache in brackets):
-//   64 single tokens over 300 to 32000 keys, 8 kv heads of 128: 0.89 GB in 154 to 160 us
-//     (by the GPU), 5.8 TB/s (268 us); two tokens over 116000 and 131000 keys: 92 to 98
+//   64 single tokens over 300 to 32000 keys, 8 kv heads of 128: 0.89 GB in 150 to 160 us
+//     (by the GPU), 5.8 TB/s (268 us); two tokens over 116000 and 131000 keys: 91 to 98
 //     us (153). A further key costs its bytes at 6.7 TB/s; the rest, 13 to 15 us, is the
 //     launch, the CTA's plan (1.6 us), the first lookups (1.5 us), the first tile and the
 //     joins.
@@ -171,7 +171,7 @@ __device__ __forceinline__ Unit unit_at(const Params8& p, const Seq& s, int row0
 template <int ROWS>
 struct Walk8 {
   int b, kvh, j;   // the unit that follows
-  int n;           // units of the sequence and head
+  int n;           // units of the sequence and head; 0: the sequence is to be found yet, at b or after
   Seq s;
   long long x;
   // the unit found by next(): what of it is this worker's
@@ -181,18 +181,32 @@ struct Walk8 {
   long long y0, y1;
   bool first, last;  // the unit's first, last part
 
+  // The next sequence with rows, by the whole warp: its lanes look at 32 at a time
+  // (a captured call's unused places are empty sequences).
   __device__ __forceinline__ void load(const Params8& p) {
-    n = 0;
-    while (b < p.L.B) {
-      seq::seq_at(p.L, b, s);
+    for (; b < p.L.B; b += 32) {
+      Seq t{};
+      const int at = b + int(threadIdx.x & 31);
+      const bool rows_there = at < p.L.B && seq::seq_at(p.L, at, t) && t.qlen > 0;
+      const unsigned found = __ballot_sync(0xffffffffu, rows_there);
+      if (found == 0) continue;
+      const int of = __ffs(found) - 1;
+      b += of;
+      s.q0 = __shfl_sync(0xffffffffu, t.q0, of);
+      s.qlen = __shfl_sync(0xffffffffu, t.qlen, of);
+      s.klen = __shfl_sync(0xffffffffu, t.klen, of);
       n = (s.qlen * p.group + ROWS - 1) / ROWS;
-      if (n > 0) break;
-      ++b;
+      return;
     }
   }
   // the worker's next part of a unit, if any: lo, hi its share; end: it has what lies at the end too
   __device__ __forceinline__ bool next(const Params8& p, long long lo, long long hi, bool end) {
-    while (b < p.L.B) {
+    for (;;) {
+      if (n == 0) {
+        if (x + kItemCost >= hi && !end) return false;  // (what follows is others': not looked for)
+        load(p);
+      }
+      if (b >= p.L.B) return false;
       seq = s;
       head = kvh;
       b_of = b;
@@ -208,7 +222,7 @@ struct Walk8 {
         if (++kvh == p.Hkv) {
           kvh = 0;
           ++b;
-          load(p);
+          n = 0;
         }
       }
       if (u.nt == 0) {
@@ -224,7 +238,6 @@ struct Walk8 {
       k1 = last ? u.hi : (u.kt + int(hi - y0)) << 7;
       return true;
     }
-    return false;
   }
 };
 
@@ -326,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
     walk.kvh = 0;
     walk.j = 0;
     walk.x = 0;
-    walk.load(p);
+    walk.n = 0;
     if (walk.b < p.L.B) {
       walk.kvh = int((target - ctl.start.before) / ctl.start.of_seq);
       walk.x = ctl.start.before + walk.kvh * ctl.start.of_seq;
@@ -522,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
           for (int x = 0; x < 4; ++x)
             qf[t][2 * k + (x >> 1)][x & 1] = f16x2_of(u2f(y[x] << 16) * f, u2f(y[x] & 0xffff0000u) * f);
         }
-        const float back = exp2i(e - 14) * p.scale_log2;
+        // (a row that is not finite gives NaN, also where all its scores are -inf)
+        const float back = m < 0x7f80u ? exp2i(e - 14) * p.scale_log2 : __int_as_float(0x7fffffff);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           rf[t][x] = __shfl_sync(0xffffffffu, back, (2 * c + x) * 4);

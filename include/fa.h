@@ -339,8 +339,11 @@ int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, 
  * fa_fwd_paged's, and k_scales and v_scales [num_pages, page_size / 16, Hkv]
  * (fp32) a scale for each block of 16 tokens and head: row r of a page stands
  * for scale[page][r / 16][head] * code[page][r][head][...]. A scale that is used
- * must lie between 2^-126 and 2^126. Conventions, limits and errors are those of
- * the bf16 calls; scales are aligned to 4 bytes.
+ * must lie between 2^-90 and 2^120, and V's scales of one sequence and head within
+ * a factor of 2^100 of each other: farther apart, keys of the smaller scales that have
+ * less than 2^-33 of the largest weight are lost, and in the end all of them.
+ * Conventions, limits and errors are those of the bf16 calls; scales are aligned to
+ * 4 bytes.
  */
 
 /*

@@ -118,6 +118,16 @@ def test_more_tokens_than_keys(fa):
     run(fa, [10, 300, 4, 1], [4, 129, 0, 0], 4, 2, 64, 16, seed=14)
 
 
+@pytest.mark.parametrize("where", ["ends", "gaps"])
+def test_slots_without_a_sequence(fa, where):
+    # a captured call's unused places, more than a warp looks at in one go
+    n, keys = [0] * 700, [0] * 700
+    for b in [0, 1, 2, 40, 41] if where == "ends" else [33, 66, 69, 300, 699]:
+        n[b], keys[b] = 1 + b % 2, 500 + 3 * b
+    keys[450] = 90  # keys, but no new tokens
+    run(fa, n, keys, 8, 2, 64, 16, seed=29)
+
+
 def test_many_sequences(fa):
     g = torch.Generator().manual_seed(15)
     keys = torch.randint(0, 200, (1200,), generator=g).tolist()
@@ -156,6 +166,30 @@ def test_any_scales_of_blocks(fa):
         for s in c.scales:
             s *= torch.rand(s.shape, generator=g) + 0.5
     run(fa, [1, 90], [700, 200], 4, 2, 128, 16, seed=19, edit=edit)
+
+
+@pytest.mark.parametrize("new", [[1, 3], [70, 20]])
+@pytest.mark.parametrize("low,high", [(2.0 ** -80, 2.0 ** -80),
+                                      (2.0 ** 100, 2.0 ** 100), (2.0 ** -70, 2.0 ** 25), (2.0 ** 10, 2.0 ** 100)])
+def test_scales_of_far_apart_sizes(fa, new, low, high):
+    # V's blocks in turn: the row sum is over all of them, whatever V's size
+    def edit(c):
+        c.scales[1][:, 0::2] *= low
+        c.scales[1][:, 1::2] *= high
+    run(fa, new, [700, 200], 4, 2, 128, 64, seed=27, edit=edit)
+
+
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_are_all_minus_infinity(fa, new, d):
+    c = cu8.filled([300], 1, d, 16, seed=28)
+    c.codes[0].view(torch.uint8)[..., 3] = 0xB8  # -1
+    pages, table = c.cuda()
+    q = su.normal((new, 2, d), su.gen(28))
+    q[0, 1, 3] = math.inf
+    o, _ = fa.forward_paged_fp8(q.cuda(), *pages, su.starts([new]).cuda(), c.lens_k().cuda(), table)
+    bad = o.float().isnan().all(2).cpu()
+    assert bad[0, 1] and o.float().isnan().any(2).sum() == 1
 
 
 def test_nan_stays_in_its_rows(fa):
