@@ -44,6 +44,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
@@ -442,14 +443,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
       }
       uint8_t* const dst = ring + slot * 2 * C::kHalf;
       if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], uint32_t(2 * __popc(boxes) * p.box_rows * D));
-      for (unsigned left = boxes; left != 0; left &= left - 1) {
-        const int x = __ffs(left) - 1;
-        const int pg = __shfl_sync(0xffffffffu, page, x), at = __shfl_sync(0xffffffffu, in_page, x);
+      auto issue = [&](auto most) {  // (unrolled, so that no box's page waits for the box before)
+        constexpr int N = decltype(most)::value;
+        int pg[N], at[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+          pg[x] = __shfl_sync(0xffffffffu, page, x);
+          at[x] = __shfl_sync(0xffffffffu, in_page, x);
+        }
         if (elect_one()) {
-          tma_load_4d_hint(dst + x * p.box_rows * D, &tmK, &ctl.full[slot], 0, t.head, at, pg, pol);
-          tma_load_4d_hint(dst + C::kHalf + x * p.box_rows * D, &tmV, &ctl.full[slot], 0, t.head, at, pg, pol);
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            if (!(boxes >> x & 1)) continue;
+            tma_load_4d_hint(dst + x * p.box_rows * D, &tmK, &ctl.full[slot], 0, t.head, at[x], pg[x], pol);
+            tma_load_4d_hint(dst + C::kHalf + x * p.box_rows * D, &tmV, &ctl.full[slot], 0, t.head, at[x], pg[x], pol);
+          }
         }
         __syncwarp();
+      };
+      if (n_box <= 2) {
+        issue(std::integral_constant<int, 2>{});
+      } else {
+        issue(std::integral_constant<int, 8>{});
       }
     };
     auto hand_out_scale = [&](const Tile& t, int slot) {
