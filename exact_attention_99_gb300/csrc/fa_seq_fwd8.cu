@@ -101,7 +101,7 @@ template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   // CTAs of an SM: one's units begin and end while the other's keys come in
-  static constexpr int kPerSm = NT == 1 ? 2 : 1;
+  static constexpr int kPerSm = NT == 1 ? 2 : D == 64 ? 2 : 1;
   static constexpr int kHalf = 128 * D;            // bytes of a tile's K, or V
   static constexpr int kStages = D == 64 || NT == 2 ? 4 : 2;
   static constexpr int kRing = kStages * 2 * kHalf;
