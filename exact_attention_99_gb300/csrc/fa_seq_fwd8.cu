@@ -101,7 +101,9 @@ template <int D, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   // CTAs of an SM: one's units begin and end while the other's keys come in
-  static constexpr int kPerSm = NT == 1 ? 2 : D == 64 ? 2 : 1;
+  // (of 16 rows of 64 too: 64 tokens over 2000 to 8000 keys 139 -> 101 us; of 128 they
+  // have no registers for that)
+  static constexpr int kPerSm = NT == 1 || D == 64 ? 2 : 1;
   static constexpr int kHalf = 128 * D;            // bytes of a tile's K, or V
   static constexpr int kStages = D == 64 || NT == 2 ? 4 : 2;
   static constexpr int kRing = kStages * 2 * kHalf;
@@ -912,16 +914,18 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
 cudaError_t launch_seq_fwd8(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream) {
   // Few rows or many: by the mean sequence's, as the lengths are on the device.
   //   Up to 8 rows: here. 64 sequences of 2000 to 8000 keys, 8 kv heads of 128: 107 us,
-  //     191 us there (d = 64: 86, 141); also where half of the rows are one sequence's (64
+  //     191 us there (d = 64: 83, 150); also where half of the rows are one sequence's (64
   //     of 8000 keys: 259 us, 296). Over 2^16 rows such a sequence could be long.
-  //   9 to 16 rows: single tokens of wide groups here (the 64 sequences: 173 us, 185
+  //   9 to 16 rows, d = 64: here (the 64 sequences: 101 us, 150 there; 31 single tokens and
+  //     a prompt of 96, over 8000 keys: 129, 149; 255 and a chunk of 512: 630, 586).
+  //   The same, d = 128: single tokens of wide groups here (the 64 sequences: 173 us, 185
   //     there) and small batches (4 tokens of a group of 4 over 1000 keys: 13.4 us, 17.1;
   //     4 sequences of them over 8000: 30, 32); others may be single tokens and a prompt,
-  //     whose keys are read anew for each 16 rows: 31 single tokens and 96, over 8000: 224
-  //     us, 174 there; 255 and a chunk of 512, over 2000 to 8000 keys: 1133 us, 728 there.
+  //     whose keys are read anew for each 16 rows: the 31 and 96: 224 us, 174 there; the
+  //     255 and 512: 1133 us, 728 there.
   //   More: there (24 rows of the 64 sequences: 278 us here, 191 there).
   const long long all = 1LL * pb.total_q * (pb.Hq / pb.Hkv), rows = (all + pb.B - 1) / pb.B;
-  const bool few = rows <= 8 || (rows <= 16 && (pb.total_q <= pb.B || all <= 64));
+  const bool few = rows <= 8 || (rows <= 16 && (pb.d == 64 || pb.total_q <= pb.B || all <= 64));
   if (!few || all > (1 << 16)) return launch_seq_fwd_codes(pb, sc, o, lse, stream);
   if (pb.d == 128)
     return rows <= 8 ? seq8::launch_t<128, 1>(pb, sc, o, lse, stream) : seq8::launch_t<128, 2>(pb, sc, o, lse, stream);

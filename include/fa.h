@@ -369,8 +369,8 @@ int fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pag
  *   values that it stands for. Of those nothing is rounded; P is rounded to f16
  *   (11 bits), and q to f16 after a division by a power of two of its row where
  *   the batch's sequences have few rows (new tokens * query heads of a group: on the
- *   mean 8 or fewer, or 16 where there are no more tokens than sequences or 64 rows in
- *   all; 2^16 in all), to the sum of two e4m3 values where they have many: exact
+ *   mean 8 or fewer, or 16 where d = 64 or there are no more tokens than sequences or 64
+ *   rows in all; 2^16 in all), to the sum of two e4m3 values where they have many: exact
  *   for what is 2^-9 of the row's largest value or more, off by at most 2^-17 of that
  *   below. A row of q that is not finite gives NaN.
  *   Rows past a sequence's end are not used, whatever their codes; their block's
