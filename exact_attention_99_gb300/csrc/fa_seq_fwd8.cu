@@ -29,12 +29,12 @@
 // joined by a last kernel, in a fixed order.
 //
 // Measured (the same calls over a bf16 cache in brackets):
-//   64 single tokens over 300 to 32000 keys, 8 kv heads of 128: 0.89 GB in 150 to 160 us
-//     (by the GPU), 5.8 TB/s (268 us); two tokens over 116000 and 131000 keys: 91 to 98
-//     us (153). A further key costs its bytes at 6.7 TB/s; the rest, 13 to 15 us, is the
-//     launch, the CTA's plan (1.6 us), the first lookups (1.5 us), the first tile and the
-//     joins.
-//   one token over 1000 keys: 12.1 us (13.3), that chain alone.
+//   64 single tokens over 300 to 32000 keys, 8 kv heads of 128: 0.89 GB in 146 to 160 us
+//     (by the GPU), 5.6 to 6.1 TB/s (268 us); two tokens over 116000 and 131000 keys: 90
+//     to 98 us (153). A further key costs its bytes at 6.7 TB/s; the rest, 13 to 15 us, is
+//     the launch, the CTA's plan (1.6 us), the first lookups (1.5 us), the first tile and
+//     the joins.
+//   one token over 1000 keys: 11.5 us (13.3), that chain alone.
 //   Tried, the 64 tokens (159 us when the first three of these were measured): loads by
 //     cp.async, 16 warps a CTA 213 us, four CTAs of 4 warps 194; TMA with 256-byte
 //     promotion in L2 201 (a third more is read from memory than is asked for); an L2
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
       }
       uint8_t* const dst = ring + slot * 2 * C::kHalf;
       if (lane == 0) mbar_arrive_expect_tx(&ctl.full[slot], uint32_t(2 * __popc(boxes) * p.box_rows * D));
-      auto issue = [&](auto most) {  // (unrolled, so that no box's page waits for the box before)
+      auto issue = [&](auto most) {  // (all pages first: pages of 16, 64 tokens 152 -> 127 us, d = 64 133 -> 97)
         constexpr int N = decltype(most)::value;
         int pg[N], at[N];
 #pragma unroll
@@ -913,17 +913,18 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
 
 cudaError_t launch_seq_fwd8(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* lse, cudaStream_t stream) {
   // Few rows or many: by the mean sequence's, as the lengths are on the device.
-  //   Up to 8 rows: here. 64 sequences of 2000 to 8000 keys, 8 kv heads of 128: 107 us,
-  //     191 us there (d = 64: 83, 150); also where half of the rows are one sequence's (64
-  //     of 8000 keys: 259 us, 296). Over 2^16 rows such a sequence could be long.
-  //   9 to 16 rows, d = 64: here (the 64 sequences: 101 us, 150 there; 31 single tokens and
-  //     a prompt of 96, over 8000 keys: 129, 149; 255 and a chunk of 512: 630, 586).
-  //   The same, d = 128: single tokens of wide groups here (the 64 sequences: 173 us, 185
-  //     there) and small batches (4 tokens of a group of 4 over 1000 keys: 13.4 us, 17.1;
-  //     4 sequences of them over 8000: 30, 32); others may be single tokens and a prompt,
-  //     whose keys are read anew for each 16 rows: the 31 and 96: 224 us, 174 there; the
-  //     255 and 512: 1133 us, 728 there.
-  //   More: there (24 rows of the 64 sequences: 278 us here, 191 there).
+  // 64 sequences of 2000 to 8000 keys, 8 kv heads, in us here and there, d = 128 (64):
+  //   4 rows (single tokens)    125, 181 (84, 149)
+  //   16 rows                   155, 184 (101, 151)
+  //   24 rows                   294, 187 (185, 151)
+  // Of batches that are not alike, over 8000 keys or as above:
+  //   63 single tokens and 65 of one sequence (8 rows on the mean)   225, 294 (179, 253)
+  //   31 and 96 (16 rows)                                            192, 172 (129, 149)
+  //   255 and a chunk of 512 (12 rows)                               964, 740 (631, 602)
+  // as the keys of a long one are read anew for each 16 rows. So up to 16 rows come here,
+  // but of d = 128 from 9 on only single tokens of wide groups and small batches (4
+  // tokens of a group of 4 over 1000 keys: 13.3, 15.5). Above 2^16 rows such a sequence
+  // could be very long.
   const long long all = 1LL * pb.total_q * (pb.Hq / pb.Hkv), rows = (all + pb.B - 1) / pb.B;
   const bool few = rows <= 8 || (rows <= 16 && (pb.d == 64 || pb.total_q <= pb.B || all <= 64));
   if (!few || all > (1 << 16)) return launch_seq_fwd_codes(pb, sc, o, lse, stream);
