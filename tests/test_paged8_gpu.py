@@ -65,7 +65,8 @@ def test_chunks(fa, new, d):
 
 @pytest.mark.parametrize("window", [None, (5, 0), (300, 2)])
 @pytest.mark.parametrize("new,keys", [([4, 1, 3], [300, 2000, 77]), ([10, 1, 1], [12, 900, 3000]), ([16], [4000]),
-                                      ([0, 9, 0, 3, 1], [50, 700, 0, 1500, 1])])
+                                      ([0, 9, 0, 3, 1], [50, 700, 0, 1500, 1]),
+                                      ([4] * 30 + [1], [5 + 40 * i for i in range(30)] + [3])])
 @pytest.mark.parametrize("d", [64, 128])
 def test_few_tokens_of_few_sequences(fa, new, keys, d, window):
     run(fa, new, keys, 8, 2, d, 32, window=window, seed=len(new))
