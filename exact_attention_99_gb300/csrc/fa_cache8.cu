@@ -11,7 +11,7 @@
 //
 // Each value is read once (2 bytes) and written once (1 byte), so memory bound:
 // 51000 tokens of 8 heads of 128 in prompts take 53 us, 5.9 TB/s (the measured copy
-// 6.8); 100 single tokens 4.2 us, the launch and a chain of four loads.
+// 6.8); 100 single tokens 3.8 us, the launch and a chain of four loads.
 // The first new token of a block speaks for it: a warp takes the block's new
 // rows of one head of K or V, all 16 rows' loads in flight, finds their largest
 // magnitude by packed 16-bit integer maxima (of bf16's bits without the sign),
@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "fa_seq.cuh"
@@ -86,24 +87,26 @@ __global__ void __launch_bounds__(kThreads, 4) append8_kernel(const Append8Args 
   constexpr int kSteps = kBlock / kAtOnce;
   const int r0 = lane / kLanes, c = lane % kLanes * 8;
   const int tasks = n_parts * 2 * a.Hkv;
-  for (int task = blockIdx.y * kWarps + warp; task < tasks; task += gridDim.y * kWarps) {
-    const int i = task / (2 * a.Hkv), what = task - i * 2 * a.Hkv, head = what >> 1, kv = what & 1;
-    const Part p = parts[i];
+  // A block's new rows of one head of K or V, in kN accesses. A single token has one:
+  // the instructions of seven idle ones took longer than its memory (256 tokens of 8
+  // heads of 128 5.3 -> 4.3 us, 4096 35 -> 27 us).
+  auto write = [&](auto steps, const Part& p, int head, int kv) {
+    constexpr int kN = decltype(steps)::value;
     const int held = int(p.row % kBlock);  // rows of the block before the new ones
     float* const scale_at = a.scales[kv] + p.row / kBlock * a.Hkv + head;
     const float before = held > 0 ? *scale_at : 0.0f;
     const uint16_t* src = a.x[kv] + p.t * a.stride[kv] + 1LL * head * D + c;
-    uint4 v[kSteps];
+    uint4 v[kN];
     {
       const uint16_t* at = src + r0 * a.stride[kv];
       const long long step = kAtOnce * a.stride[kv];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s, at += step)
+      for (int s = 0; s < kN; ++s, at += step)
         v[s] = s * kAtOnce + r0 < p.n ? __ldcs(reinterpret_cast<const uint4*>(at)) : make_uint4(0, 0, 0, 0);
     }
     uint32_t m = 0;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
+    for (int s = 0; s < kN; ++s) {
       m = max_u16x2(m, max_u16x2(v[s].x & 0x7fff7fffu, v[s].y & 0x7fff7fffu));
       m = max_u16x2(m, max_u16x2(v[s].z & 0x7fff7fffu, v[s].w & 0x7fff7fffu));
     }
@@ -111,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 4) append8_kernel(const Append8Args 
     if (top >= 0x7f80u) {  // infinities and NaN, held as NaN, are no part of the scale
       uint32_t fin = 0;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
+      for (int s = 0; s < kN; ++s) {
         uint32_t* w = reinterpret_cast<uint32_t*>(&v[s]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -149,10 +152,19 @@ __global__ void __launch_bounds__(kThreads, 4) append8_kernel(const Append8Args 
     const int row_bytes = a.Hkv * D;
     uint8_t* dst = a.pages[kv] + ((p.row + r0) * a.Hkv + head) * D + c;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s, dst += kAtOnce * row_bytes)
+    for (int s = 0; s < kN; ++s, dst += kAtOnce * row_bytes)
       if (s * kAtOnce + r0 < p.n)
         *reinterpret_cast<uint2*>(dst) = make_uint2(e4m3x4_of_bf16(v[s].x, v[s].y, inv), e4m3x4_of_bf16(v[s].z, v[s].w, inv));
     if (lane == 0) *scale_at = scale;
+  };
+  for (int task = blockIdx.y * kWarps + warp; task < tasks; task += gridDim.y * kWarps) {
+    const int i = task / (2 * a.Hkv), what = task - i * 2 * a.Hkv, head = what >> 1, kv = what & 1;
+    const Part p = parts[i];
+    if (p.n <= kAtOnce) {
+      write(std::integral_constant<int, 1>{}, p, head, kv);
+    } else {
+      write(std::integral_constant<int, kSteps>{}, p, head, kv);
+    }
   }
   // every wrong length is told, also where no token leads to it
   bool ok = true;
