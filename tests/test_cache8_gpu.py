@@ -62,6 +62,12 @@ def test_single_tokens_after_prompts(fa, hk):
     steps(fa, [[5, 16, 31, 0]] + [[1, 1, 1, 1]] * 20, hk, 128, 16, seed=hk, sigma=(1.0, 0.01, 3.0, 1.0, 300.0, 2.0))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_tokens_at_a_time(fa, d):
+    # every size about an access's rows, at many places of a block
+    steps(fa, [[1, 2, 3, 4, 5, 6, 0]] * 9, 3, d, 16, seed=10 + d, sigma=(1.0, 0.1, 7.0, 300.0))
+
+
 def test_chunks_that_end_inside_blocks(fa):
     steps(fa, [[3, 40, 0], [20, 1, 7], [0, 0, 10], [9, 70, 1]], 2, 64, 32, seed=4, sigma=(1.0, 8.0, 1e-3, 30.0))
 
