@@ -79,6 +79,7 @@ struct Params8 {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
+  const uint8_t* v_codes;
   const float* scales[2];
   const int* table;
   Lens L;
@@ -114,7 +115,7 @@ struct Shape {
 
 // A unit, or this CTA's part of it.
 struct Item8 {
-  int q0, qlen, klen;   // the sequence
+  int b, q0, qlen, klen;  // the sequence
   int row0, rows;       // the unit's rows of it (token * group + head of the group)
   int head;             // kv head; -1: there are no more items
   int k0, k1;           // keys [k0, k1)
@@ -129,6 +130,7 @@ struct Ctl8 {
   uint64_t join_full, join_empty;
   float sc[Shape<D, NT>::kStages][2][8];  // scales of a tile's blocks of K, V
   float2 ml[kWarps][8 * NT];
+  uint32_t nans[kWarps];  // not 0: NaN codes of V were taken as zeros
   long long sums[kWarps + 1];
   struct {
     int b;
@@ -167,6 +169,28 @@ __device__ __forceinline__ Unit unit_at(const Params8& p, const Seq& s, int row0
     u.nt = ((u.hi - 1) >> 7) - u.kt + 1;
   }
   return u;
+}
+
+// Four columns of V's rows (their place in the first row: codes): a byte of the result is not
+// 0 where one of the keys [lo, hi) of sequence b is a NaN code. Not looked at are the blocks
+// of 16 keys that lie in [all_lo, all_hi).
+__device__ __noinline__ uint32_t hidden_nans(const Params8& p, int b, int lo, int hi, const uint8_t* codes, int d,
+                                             int all_lo, int all_hi) {
+  const int* const row = p.table + size_t(b) * p.max_pages;
+  uint32_t nans = 0;
+#pragma unroll 1
+  for (int k = lo; k < hi; ++k) {
+    const int block = k & ~15;
+    if (block >= all_lo && block + 16 <= all_hi) {  // on to the first that does not
+      k = (all_hi & ~15) - 1;
+      continue;
+    }
+    const int page = row[k / p.page_size];
+    if (page < 0 || page >= p.num_pages) continue;
+    const long long token = 1LL * page * p.page_size + k % p.page_size;
+    nans |= nan_codes(*reinterpret_cast<const uint32_t*>(codes + token * p.Hkv * d));
+  }
+  return nans;
 }
 
 // A walk over the units in the order (sequence, kv head, rows), with the place
@@ -370,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
         x.head = -1;
         if (more) {
           any = true;
+          x.b = walk.b_of;
           x.q0 = walk.seq.q0;
           x.qlen = walk.seq.qlen;
           x.klen = walk.seq.klen;
@@ -584,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
         l[t][0] = l[t][1] = 0.0f;
       }
       bool ok = true;
+      uint32_t nans = 0;  // not 0: NaN codes were taken as zeros
       for (int key = (w.k0 & ~127) + warp * 16, last = max(w.k1, 1) + warp * 16; key < last; key += 128, ++n) {
         const int slot = n % S;
         ok = seq::warp_wait(&ctl.full[slot], (n / S) & 1, &ctl.abort, LIM);
@@ -683,6 +709,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
               for (int x = 0; x < W; ++x) v[k][x] = key + r < w.klen ? v[k][x] : 0;
             }
           }
+          // A NaN code of V that some rows do not see would reach them, as 0 * NaN is NaN: a zero here,
+          // and the rows that see it are found at the unit's end (hidden_nans)
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int x = 0; x < W; ++x) {
+                const uint32_t m = nan_codes(v[k][x]);
+                nans |= m;
+                v[k][x] &= ~m;
+              }
+          }
 #pragma unroll
           for (int x = 0; x < W; ++x) {
             const uint32_t x0 = __byte_perm(v[0][x], v[1][x], 0x5140), x1 = __byte_perm(v[0][x], v[1][x], 0x7362);
@@ -720,10 +758,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
             *reinterpret_cast<float4*>(dst + 4 * k) =
                 make_float4(acc[t][2 * k][x], acc[t][2 * k][x + 2], acc[t][2 * k + 1][x], acc[t][2 * k + 1][x + 2]);
         }
+      nans = __any_sync(0xffffffffu, nans != 0);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.join_full);
+      if (lane == 0) {
+        ctl.nans[warp] = nans;
+        mbar_arrive(&ctl.join_full);
+      }
       if (!seq::warp_wait(&ctl.join_full, i & 1, &ctl.abort, LIM)) break;
       constexpr int Q4 = D / 4;
+      nans = 0;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) nans |= ctl.nans[k];
 #pragma unroll 1
       for (int at = tid; at < w.rows * Q4; at += kWarps * 32) {
         const int r = at / Q4, d4 = (at - r * Q4) * 4;
@@ -742,6 +787,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kPerSm)
           o.y = fmaf(y.y, f, o.y);
           o.z = fmaf(y.z, f, o.z);
           o.w = fmaf(y.w, f, o.w);
+        }
+        if (nans != 0) {
+          const int pos = w.klen - w.qlen + (w.row0 + r) / p.group;
+          const uint32_t x = hidden_nans(p, w.b, p.wl >= 0 ? max(w.k0, pos - p.wl) : w.k0,
+                                         p.wr >= 0 ? min(w.k1, pos + p.wr + 1) : w.k1, p.v_codes + 1LL * w.head * D + d4, D,
+                                         all_lo, all_hi);
+          const float nan = __int_as_float(0x7fffffff);
+          if (x & 0xffu) o.x = nan;
+          if (x & 0xff00u) o.y = nan;
+          if (x & 0xff0000u) o.z = nan;
+          if (x & 0xff000000u) o.w = nan;
         }
         if (w.slot >= 0) {
           *reinterpret_cast<float4*>(p.part_o + (size_t(w.slot) * R + r) * D + d4) = o;
@@ -847,6 +903,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales& sc, void* o, float* 
   p.q = static_cast<const __nv_bfloat16*>(pb.q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
+  p.v_codes = static_cast<const uint8_t*>(pb.v);
   p.scales[0] = sc.k;
   p.scales[1] = sc.v;
   p.table = pb.page_table;

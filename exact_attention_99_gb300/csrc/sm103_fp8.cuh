@@ -73,6 +73,11 @@ __device__ __forceinline__ float f16_hi(uint32_t x) {
   return r;
 }
 
+// 0xff where a byte of x is a NaN code, of either sign
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) {
+  return (((x & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu;
+}
+
 // four bf16 values (two words) times f, to four codes
 __device__ __forceinline__ uint32_t e4m3x4_of_bf16(uint32_t x, uint32_t y, float f) {
   const uint64_t f2 = pack2(f, f);
