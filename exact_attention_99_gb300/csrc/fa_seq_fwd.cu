@@ -101,6 +101,7 @@ struct Params {
   int o_box;           // tokens of a warp's 32 rows, if they are whole tokens (tmO's boxes), else 0
   int num_pages, page_size, box_rows, max_pages;
   const float* scales[2];  // codes: of K, V, [num_pages, page_size / 16, Hkv]
+  const uint8_t* v_codes;
   float scale_log2;    // |scale| * log2(e)
   uint32_t neg_s;      // 1 for a negative scale
   int wl, wr;
@@ -181,6 +182,7 @@ struct Codes {
   uint64_t k_full[kMaxSlots], k_empty[kMaxSlots];  // K's tiles; V's are the other rings' (kv_full, ...)
   uint64_t sc_full[kScaleTiles];
   float4 sc[kScaleTiles][8];       // of each block: a scale log2(e), log2(b), 1 / b
+  uint32_t nans[kItems];           // not 0: NaN codes of V were taken as zeros (see Seen)
 };
 static_assert(kScaleTiles >= Tiles<128>::kVSlots + 4 && kScaleTiles >= Tiles<64>::kVSlots + 4, "see there");
 struct NoCodes {};
@@ -268,6 +270,43 @@ __device__ __forceinline__ void release_item(Ctl<KIND>& ctl, int i) {
   if (lane == 0) mbar_arrive(&ctl.it_empty[i % kItems]);
 }
 
+// Codes: the keys [lo, hi) that every row of an item sees. A NaN code of V would reach the
+// rows that do not see it, as 0 * NaN is NaN: among 32 keys that not all rows see it becomes
+// zero, and the rows that see it are found at the item's end (hidden_nans). Elsewhere
+// the products do that.
+struct Seen {
+  int lo, hi;
+  // the 32 keys from k on, of klen
+  __device__ __forceinline__ bool hides(int k, int klen) const { return k < lo || min(k + 32, klen) > hi; }
+};
+__device__ __forceinline__ Seen seen_by_all(const Params& p, int pos, int ntok) {
+  return Seen{p.wl >= 0 ? pos + ntok - 1 - p.wl : 0, p.wr >= 0 ? pos + p.wr + 1 : 0x7fffffff};
+}
+// A bit for each of 16 columns of V's rows (their place in the first row: codes) in which one
+// of the keys [lo, hi) of sequence b, in 32 that hide some, is a NaN code.
+__device__ __forceinline__ uint32_t hidden_nans(const Params& p, int b, int lo, int hi, int klen, Seen seen,
+                                                 const uint8_t* codes, int d) {
+  const int* const row = p.table + size_t(b) * p.max_pages;
+  uint4 nans = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (int k = lo; k < hi; ++k) {
+    if (!seen.hides(k & ~31, klen)) {  // on to the next 32
+      k |= 31;
+      continue;
+    }
+    const int page = row[k / p.page_size];
+    if (page < 0 || page >= p.num_pages) continue;
+    const long long token = 1LL * page * p.page_size + k % p.page_size;
+    const uint4 x = *reinterpret_cast<const uint4*>(codes + token * p.Hkv * d);
+    nans.x |= nan_codes(x.x);
+    nans.y |= nan_codes(x.y);
+    nans.z |= nan_codes(x.z);
+    nans.w |= nan_codes(x.w);
+  }
+  auto bits = [](uint32_t x) { return (x & 1u) | (x >> 7 & 2u) | (x >> 14 & 4u) | (x >> 21 & 8u); };
+  return bits(nans.x) | bits(nans.y) << 4 | bits(nans.z) << 8 | bits(nans.w) << 12;
+}
+
 // Codes: rows [32 cw, 32 cw + 32) of every V tile turned to f16; the tiles' scales.
 template <int D>
 __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl, uint8_t* sKV, int cw, int lane,
@@ -286,6 +325,7 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
     if (w == nullptr) break;
     const int nt = w->nt, kvh = w->kvh, kt = w->kt, klen = w->klen, fill = w->fill;
     const int seen = p.wl >= 0 ? w->pos - p.wl : 0;  // the first key that a row of the item sees
+    const Seen by_all = seen_by_all(p, w->pos, w->ntok);
     const int* const row_of_table = p.table + size_t(w->kbase) * p.max_pages;
     // row of the scales of block 2 cw + lane of tile t, or -1: not used
     auto block_key = [&](int t) { return ((kt + t) * 8 + 2 * cw + lane) * kFp8Block; };
@@ -323,6 +363,21 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
       if (!ok) break;
       uint8_t* const tile = sKV + C::kVRing + slot * C::kTileBytes;
       uint8_t* const mine = tile + cw * 4096;
+      if (by_all.hides((kt + t) * 128 + cw * 32, klen)) {
+        uint32_t nans = 0;
+        const int end = t == nt - 1 && fill != 0 ? max(0, min(32, fill - cw * 32)) * (D / 16) : 2 * D;
+#pragma unroll 1
+        for (int g = lane; g < end; g += 32) {
+          uint4* const at = reinterpret_cast<uint4*>(mine) + g;
+          const uint4 z = *at, m = make_uint4(nan_codes(z.x), nan_codes(z.y), nan_codes(z.z), nan_codes(z.w));
+          if ((m.x | m.y | m.z | m.w) != 0) {
+            nans = 1;
+            *at = make_uint4(z.x & ~m.x, z.y & ~m.y, z.z & ~m.z, z.w & ~m.w);
+          }
+        }
+        if (nans != 0) ctl.codes.nans[i % kItems] = 1;
+        __syncwarp();
+      }
       constexpr int kHalves = D / 64;
       uint4 c[4][kHalves];
 #pragma unroll
@@ -331,7 +386,7 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
         for (int h = 0; h < kHalves; ++h)
           c[g][h] = *reinterpret_cast<const uint4*>(
               mine + (g * 8 + in8) * D + (D == 128 ? ((h * 4 + quarter) ^ in8) << 4 : quarter << 4));
-      if (t == nt - 1 && fill != 0) {  // rows past the sequence's end: 0 * NaN would stay NaN
+      if (t == nt - 1 && fill != 0) {  // rows past the sequence's end, whatever they hold
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           if (cw * 32 + g * 8 + in8 >= fill)
@@ -604,6 +659,8 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
                         : (part ? reinterpret_cast<uint8_t*>(p.part_o + size_t(to) * D + 4 * quarter)
                                 : reinterpret_cast<uint8_t*>(p.o + size_t(to) * D + 4 * quarter));
       }
+      // (the converters' word, from before the products that o_full told of)
+      const bool nans = n > 0 && valid && *const_cast<volatile uint32_t*>(&ctl.codes.nans[i % kItems]) != 0;
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t x[16];
@@ -617,6 +674,15 @@ __device__ __forceinline__ void codes_softmax(const Params& p, Ctl<kCodes>& ctl,
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[e] = f2u(fmaf(u2f(y[e]), f1, u2f(x[e])));
+        }
+        if (nans) {
+          const int pos = w->pos + (key ? 0 : s * p.tok) + row_tok, k0 = w->kt * 128, k1 = min(w->klen, k0 + w->nt * 128);
+          const uint32_t bits = hidden_nans(p, w->kbase, p.wl >= 0 ? max(k0, pos - p.wl) : k0,
+                                            p.wr >= 0 ? min(k1, pos + p.wr + 1) : k1, w->klen,
+                                            seen_by_all(p, w->pos, w->ntok), p.v_codes + 1LL * w->kvh * D + c, D);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (bits >> e & 1) x[e] = 0x7fffffffu;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -1437,6 +1503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(&ctl.it_empty[i % kItems], ((i / kItems) & 1) ^ 1, abort_flag, LIM)) return false;
       if (lane == 0) {
         ctl.it[i % kItems] = x;
+        if constexpr (CODES) ctl.codes.nans[i % kItems] = 0;
         mbar_arrive(&ctl.it_full[i % kItems]);
       }
       return true;
@@ -1767,6 +1834,7 @@ cudaError_t launch_t(const SeqProblem& pb, const Fp8Scales* sc, void* o, float* 
       return cudaErrorInvalidValue;
     p.scales[0] = sc->k;
     p.scales[1] = sc->v;
+    p.v_codes = static_cast<const uint8_t*>(pb.v);
   } else if constexpr (PAGED) {
     p.box_rows = 128;
     while (pb.page_size % p.box_rows != 0) p.box_rows /= 2;  // 16 at least

@@ -374,7 +374,9 @@ int fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pag
  *   for what is 2^-9 of the row's largest value or more, off by at most 2^-17 of that
  *   below. A row of q that is not finite gives NaN.
  *   Rows past a sequence's end are not used, whatever their codes; their block's
- *   scale is that of the rows before them. A row's result does not depend on what
+ *   scale is that of the rows before them. NaN codes of v, of rows that some tokens'
+ *   mask hides too, reach the tokens that see them and no others (a call that meets
+ *   any among keys that only some see looks them up again, which takes longer). A row's result does not depend on what
  *   else is in the call but for this rounding of q and how its keys are divided
  *   (the order of fp32 sums).
  *   Workspace, from the pool: few rows, 5 MB; many, as fa_fwd_paged and

@@ -85,3 +85,38 @@ def test_few_rows_without_a_mask(fa):
 
 def test_few_rows_in_larger_pages(fa):
     run(fa, [4, 2], [600, 129], 4, 2, 64, 64, 33, [[-1, -2, 128], [-1, 128]], window=(128, 0))
+
+
+# many rows
+MANY = [
+    ([200], [333], 4, 1, [[-1, -2, -100, 50, 332, 133, 127, 128]], None),
+    ([513], [513], 4, 2, [[-1, 0, 250, 511, 300, 7]], None),          # a whole prompt
+    ([300], [129], 4, 1, [[0, 64, -1]], None),                         # rows that see nothing
+    ([20], [6000], 4, 1, [[-1, -5, 30, 4000, -20]], None),            # keys divided, one tile of rows
+    ([40], [6000], 4, 1, [[-1, 5944, 5900, 5855, 3, -39]], (100, 0)),  # divided, behind the window
+    ([100, 1, 0, 70], [900, 333, 20, 70], 8, 2, [[-1, 799, 700, 860], [-1, 300, 331], [0], [-1, 0, 69, 35]], (64, 0)),
+    ([200], [333], 2, 1, [[-1, 100, 140, 240, 2]], (20, 1)),
+    ([1, 260], [400, 500], 32, 1, [[-1, 100, 380], [-1, 240, 499, 370]], (300, 0)),
+    ([60, 200, 33], [700, 333, 33], 20, 4, [[-1, 600, 640, 5], [-1, -40, 199, 150], [-1, 3]], None),
+]
+
+
+@pytest.mark.parametrize("new,keys,hq,hk,places,window", MANY)
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows(fa, new, keys, hq, hk, places, window, d):
+    bad = run(fa, new, keys, hq, hk, d, 16, 34, places, window=window)
+    assert bad.any() and not bad.flatten(1).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_many_items_per_cta(fa, d):
+    g = torch.Generator().manual_seed(d)
+    new = [1 + i % 5 if i % 3 else int(n) for i, n in enumerate(torch.randint(1, 200, (40,), generator=g))]
+    keys = [n + int(m) for n, m in zip(new, torch.randint(0, 500, (40,), generator=g))]
+    places = [[-1, keys[b] // 2, keys[b] - new[b] // 2 - 1] if b % 4 == 0 else [] for b in range(40)]
+    run(fa, new, keys, 16, 8, d, 16, 35, places)
+    run(fa, new, keys, 16, 8, d, 32, 36, places, window=(50, 0))
+
+
+def test_many_rows_without_a_mask(fa):
+    run(fa, [90], [300], 4, 1, 128, 48, 37, [[0, -1, 150]], causal=False)
