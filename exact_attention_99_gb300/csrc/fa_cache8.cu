@@ -5,7 +5,9 @@
 // largest finite value of its rows is at most 448 (e4m3's largest) times it.
 // A division by a power of two is exact, so a code is the rounding of the exact
 // value, and a block that later rows make coarser loses bits only where a code
-// becomes subnormal. (The scale amax / 448 would use the range up to a factor
+// becomes subnormal. In a block with a scale of another kind (something else filled it)
+// quotients and products are cut with their last bit set before they become codes, so
+// that these too are the roundings of the exact values. (The scale amax / 448 would use the range up to a factor
 // of two further, which a floating type does not need: its relative error is
 // the same over all its normal values.)
 //
@@ -131,6 +133,8 @@ __global__ void __launch_bounds__(kThreads, 4) append8_kernel(const Append8Args 
     const int e = max(-64, int(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0));
     float scale = exp2i(e);
     float inv = exp2i(-e);
+    // a block that something else filled may have a scale that is no power of two
+    const bool odd = held > 0 && (f2u(before) & 0x7fffffu) != 0;
     if (held > 0) {
       const float ratio = before * inv;
       if (before >= scale) {
@@ -142,19 +146,27 @@ __global__ void __launch_bounds__(kThreads, 4) append8_kernel(const Append8Args 
 #pragma unroll 1
         for (int r = r0; r < held; r += kAtOnce) {
           uint2* at = reinterpret_cast<uint2*>(dst + 1LL * r * a.Hkv * D);
-          uint2 x = *at;
-          x.x = e4m3x4_times(x.x, ratio);
-          x.y = e4m3x4_times(x.y, ratio);
-          *at = x;
+          const uint2 x = *at;
+          *at = odd ? make_uint2(e4m3x4_odd_times(x.x, ratio), e4m3x4_odd_times(x.y, ratio))
+                    : make_uint2(e4m3x4_times(x.x, ratio), e4m3x4_times(x.y, ratio));
         }
       }
     }
     const int row_bytes = a.Hkv * D;
     uint8_t* dst = a.pages[kv] + ((p.row + r0) * a.Hkv + head) * D + c;
+    if (odd && scale == before) {
 #pragma unroll
-    for (int s = 0; s < kN; ++s, dst += kAtOnce * row_bytes)
-      if (s * kAtOnce + r0 < p.n)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(e4m3x4_of_bf16(v[s].x, v[s].y, inv), e4m3x4_of_bf16(v[s].z, v[s].w, inv));
+      for (int s = 0; s < kN; ++s, dst += kAtOnce * row_bytes)
+        if (s * kAtOnce + r0 < p.n)
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(e4m3x4_of_bf16_over(v[s].x, v[s].y, scale), e4m3x4_of_bf16_over(v[s].z, v[s].w, scale));
+    } else {
+#pragma unroll
+      for (int s = 0; s < kN; ++s, dst += kAtOnce * row_bytes)
+        if (s * kAtOnce + r0 < p.n)
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(e4m3x4_of_bf16(v[s].x, v[s].y, inv), e4m3x4_of_bf16(v[s].z, v[s].w, inv));
+    }
     if (lane == 0) *scale_at = scale;
   };
   for (int task = blockIdx.y * kWarps + warp; task < tasks; task += gridDim.y * kWarps) {

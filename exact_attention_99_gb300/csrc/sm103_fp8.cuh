@@ -78,7 +78,7 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t x) {
   return (((x & 0x7f7f7f7fu) + 0x01010101u) >> 7 & 0x01010101u) * 0xffu;
 }
 
-// four bf16 values (two words) times f, to four codes
+// four bf16 values (two words) times f, a power of two, to four codes
 __device__ __forceinline__ uint32_t e4m3x4_of_bf16(uint32_t x, uint32_t y, float f) {
   const uint64_t f2 = pack2(f, f);
   float a, b, c, d;
@@ -86,10 +86,37 @@ __device__ __forceinline__ uint32_t e4m3x4_of_bf16(uint32_t x, uint32_t y, float
   unpack2(fmul2(pack2(u2f(y << 16), u2f(y & 0xffff0000u)), f2), c, d);
   return uint32_t(e4m3x2_of(a, b)) | (uint32_t(e4m3x2_of(c, d)) << 16);
 }
-// four codes times f, rounded to codes again
+// four codes times f, a power of two, rounded to codes again
 __device__ __forceinline__ uint32_t e4m3x4_times(uint32_t x, float f) {
   const uint32_t a = f16x2_of_e4m3x2(uint16_t(x)), b = f16x2_of_e4m3x2(uint16_t(x >> 16));
   return uint32_t(e4m3x2_of(f16_lo(a) * f, f16_hi(a) * f)) | (uint32_t(e4m3x2_of(f16_lo(b) * f, f16_hi(b) * f)) << 16);
+}
+
+
+// The same where the product or quotient is not exact: cut to 32 bits with its last bit set, so
+// that rounding it to fewer bits is rounding the value itself. (A quotient, or a product with
+// more bits, may lie nearer to halfway between two codes than 32 bits can tell.)
+__device__ __forceinline__ float odd_of(float cut, float rest) {
+  return rest == 0.0f ? cut : u2f(f2u(cut) | 1u);
+}
+__device__ __forceinline__ float odd_product(float a, float f) {
+  const float y = __fmul_rz(a, f);
+  return odd_of(y, fmaf(a, f, -y));
+}
+__device__ __forceinline__ float odd_quotient(float a, float f) {
+  const float y = __fdiv_rz(a, f);
+  return odd_of(y, fmaf(-y, f, a));
+}
+// four bf16 values over f, to four codes
+__device__ __forceinline__ uint32_t e4m3x4_of_bf16_over(uint32_t x, uint32_t y, float f) {
+  return uint32_t(e4m3x2_of(odd_quotient(u2f(x << 16), f), odd_quotient(u2f(x & 0xffff0000u), f))) |
+         (uint32_t(e4m3x2_of(odd_quotient(u2f(y << 16), f), odd_quotient(u2f(y & 0xffff0000u), f))) << 16);
+}
+// four codes times f, rounded to codes again
+__device__ __forceinline__ uint32_t e4m3x4_odd_times(uint32_t x, float f) {
+  const uint32_t a = f16x2_of_e4m3x2(uint16_t(x)), b = f16x2_of_e4m3x2(uint16_t(x >> 16));
+  return uint32_t(e4m3x2_of(odd_product(f16_lo(a), f), odd_product(f16_hi(a), f))) |
+         (uint32_t(e4m3x2_of(odd_product(f16_lo(b), f), odd_product(f16_hi(b), f))) << 16);
 }
 
 }  // namespace fa

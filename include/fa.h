@@ -352,7 +352,8 @@ int fa_cache_append(const void* k, const void* v, void* k_pages, void* v_pages, 
  *   is 2^e with the smallest whole e, -64 at least, for which every finite value
  *   of its rows is at most 448 * 2^e. New rows of a block that holds rows of the
  *   sequence before them leave its scale or raise it; raised, the rows held are
- *   rounded again in the new scale (exactly, but where a code becomes subnormal).
+ *   rounded again in the new scale (exactly, but where a code becomes subnormal or
+ *   the old scale, of something else that filled the block, is no power of two).
  *   Rows behind the new ones keep their codes, whose meaning goes with the
  *   block's scale. Codes are the nearest, ties to even; infinities and NaN are
  *   held as NaN, and a block of nothing else has the smallest scale. Two
