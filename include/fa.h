@@ -403,8 +403,8 @@ int fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, co
  *     mscale * (a cos t - b sin t), mscale * (b cos t + a sin t), t = p * inv_freq[j],
  *   with transposed = 1 the same with -t: the gradient of the call's inputs
  *   from that of its outputs. The other values of a head are copied. Angles
- *   are exact to 2^-31 of a half turn at every place; cos and sin are rounded to
- *   fp32 and the results to bf16.
+ *   are off by less than 2^-24 of a half turn, whatever the place and the frequency;
+ *   cos and sin are rounded to fp32 and the results to bf16.
  *   rot is a multiple of 16, 16 <= rot <= d, d in {64, 128}; (Hq + Hk) * d below
  *   2^30, total * (Hq + Hk) below 2^31. Outputs may not overlap other rows of
  *   the inputs. Rows outside every sequence are left as they are. Needs no
