@@ -48,10 +48,10 @@
 //   single tokens: the cache's bytes. 64 sequences of 300 to 32000 keys, 8 kv
 //     heads of 128: 1.70 GB in 258 us, 6.6 TB/s, 0.97 of the measured copy.
 //   codes, 3 chunks of 512 tokens over 6000 to 16384 keys, 32 query and 8 kv heads of
-//     128: 236 us (bf16 205 to 217), 1.6 us a tile of two stages, of which a stage's
+//     128: 230 us (bf16 205 to 217), 1.6 us a tile of two stages, of which a stage's
 //     softmax takes 0.95 (the converters issue beside it, and 16 keys at a time have
 //     scales of their own), the products behind it 0.65; 3 us at an item's end, where
-//     the softmax warps write O.
+//     the softmax warps write O. (Of d = 128 a thread spills 16 bytes, of d = 64 none.)
 //   items of few tiles: 1.3 to 2.3 us between two items, most of it instruction
 //     fetch (code that runs once per item is not in the cache) and the first
 //     S; with a window and one query head per kv head the first and the last
@@ -117,7 +117,7 @@ struct Params {
 //   softmax s   4+3s S ready, 5+3s alpha published, 6+3s P stored
 //   correction  10+s O released for PV
 //   epilogue s  12+s O written (step of the item's last tile)
-//   codes       14 a V tile's codes landed, 15 turned to f16
+//   codes       15 a V tile's codes turned to f16
 constexpr int kItems = 4;  // ring of work items
 
 template <int D>
@@ -319,7 +319,6 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
   // bits 0 and 2, so that neither the reads of codes (128-byte swizzle, or rows of 64
   // bytes) nor the writes meet in a bank.
   const int in8 = (0x63724150u >> (4 * (lane >> 2))) & 7, quarter = lane & 3;
-  // this lane's block of a tile (lanes 0, 1) and its scales, looked up two tiles ahead, read one ahead
   for (int i = 0; ok; ++i) {
     const Work* const w = next_item(ctl, i, LIM);
     if (w == nullptr) break;
@@ -327,7 +326,8 @@ __device__ __forceinline__ void codes_convert(const Params& p, Ctl<kCodes>& ctl,
     const int seen = p.wl >= 0 ? w->pos - p.wl : 0;  // the first key that a row of the item sees
     const Seen by_all = seen_by_all(p, w->pos, w->ntok);
     const int* const row_of_table = p.table + size_t(w->kbase) * p.max_pages;
-    // row of the scales of block 2 cw + lane of tile t, or -1: not used
+    // This lane's block of a tile, 2 cw + lane (lanes 0, 1): its page looked up two tiles ahead
+    // (-1: not used), its scales read one ahead.
     auto block_key = [&](int t) { return ((kt + t) * 8 + 2 * cw + lane) * kFp8Block; };
     auto look_up = [&](int t) {
       const int k = block_key(t);

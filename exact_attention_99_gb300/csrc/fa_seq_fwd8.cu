@@ -11,7 +11,7 @@
 // is an f16 value, so both products are f16 x f16 with 32-bit accumulators.
 // Roundings: q to f16 after a division by a power of two of its row (exact
 // unless a value is below 2^-28 of the row's largest), P' to f16 (off by at most
-// 2^-11 of itself, for all P' above 2^-21 of the largest), O to bf16.
+// 2^-11 of itself for all P' above 2^-21 of the largest, by 2^-32 of that below), O to bf16.
 //
 // Few rows to a kv head (single tokens): bound by the cache's bytes. A producer warp
 // loads tiles of 128 keys by TMA, and each of 8 warps takes 16 of a tile's keys: their
@@ -34,7 +34,8 @@
 //     to 98 us (153). A further key costs its bytes at 6.7 TB/s; the rest, 13 to 15 us, is
 //     the launch, the CTA's plan (1.6 us), the first lookups (1.5 us), the first tile and
 //     the joins.
-//   one token over 1000 keys: 11.5 us (13.3), that chain alone.
+//   one token over 1000 keys: 11.8 us (13.3), that chain alone. 16 tokens over 8192 keys,
+//     0.27 GB: 53 us, of which the bytes are 40.
 //   Tried, the 64 tokens (159 us when the first three of these were measured): loads by
 //     cp.async, 16 warps a CTA 213 us, four CTAs of 4 warps 194; TMA with 256-byte
 //     promotion in L2 201 (a third more is read from memory than is asked for); an L2
@@ -978,7 +979,10 @@ cudaError_t launch_seq_fwd8(const SeqProblem& pb, const Fp8Scales& sc, void* o, 
   //   63 single tokens and 65 of one sequence (8 rows on the mean)   225, 294 (179, 253)
   //   31 and 96 (16 rows)                                            192, 172 (129, 149)
   //   255 and a chunk of 512 (12 rows)                               964, 740 (631, 602)
-  // as the keys of a long one are read anew for each 16 rows. So up to 16 rows come here,
+  // as the keys of a long one are read anew for each 8 or 16 rows. Empty places count too: 255 of
+  // them and a chunk of 512 over 8000 keys (8 rows on the mean) take 578 (492), the chunk by
+  // itself, there, 70 (61); 63 and 192 tokens 44 there (118 here, d = 64), by themselves 42 (35).
+  // So up to 16 rows come here,
   // but of d = 128 from 9 on only single tokens of wide groups and small batches (4
   // tokens of a group of 4 over 1000 keys: 13.3, 15.5). Above 2^16 rows such a sequence
   // could be very long.

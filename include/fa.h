@@ -367,8 +367,10 @@ int fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pag
 
 /*
  * fa_fwd_paged_fp8 — fa_fwd_paged over such a cache: the attention of the
- *   values that it stands for. Of those nothing is rounded; P is rounded to f16
- *   (11 bits), and q to f16 after a division by a power of two of its row where
+ *   values that it stands for. Of those nothing is rounded; P times V's scale is
+ *   rounded to f16 for the product with V's codes (off by at most 2^-11 of itself, or
+ *   2^-32 of the row's largest where that is more; the row sum keeps 32 bits), and q
+ *   to f16 after a division by a power of two of its row where
  *   the batch's sequences have few rows (new tokens * query heads of a group: on the
  *   mean 8 or fewer, or 16 where d = 64 or there are no more tokens than sequences or 64
  *   rows in all; 2^16 in all), to the sum of two e4m3 values where they have many: exact
@@ -380,7 +382,7 @@ int fa_cache_append_fp8(const void* k, const void* v, void* k_pages, void* v_pag
  *   any among keys that only some see looks them up again, which takes longer). A row's result does not depend on what
  *   else is in the call but for this rounding of q and how its keys are divided
  *   (the order of fp32 sums).
- *   Workspace, from the pool: few rows, 5 MB; many, as fa_fwd_paged and
+ *   Workspace, from the pool: few rows, 2.6 MB; many, as fa_fwd_paged and
  *   (2 * d + 4) * total_q * Hq bytes for q.
  */
 int fa_fwd_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
